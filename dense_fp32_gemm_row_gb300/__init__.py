@@ -15,6 +15,9 @@ Raw entry points (pointers and the stream are plain integers)::
 Tensor convenience (torch CUDA tensors, float32, row-major contiguous)::
 
     matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None) -> C
+
+8-bit activation checkpoints and the operators that read them are in
+:mod:`dense_fp32_gemm_row_gb300.q8` and exported here.
 """
 
 from __future__ import annotations
@@ -143,6 +146,7 @@ def load():
                      "gemm_f32_release",
                      "gemm_f32_version"):
             getattr(lib, name).restype = ctypes.c_int
+        _q8._declare(lib)
         _lib = lib
         return lib
 
@@ -290,3 +294,9 @@ def matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None):
                                   int(splits), s.cuda_stream)
     check(st, "matmul")
     return out
+
+
+from dense_fp32_gemm_row_gb300 import q8 as _q8  # noqa: E402
+from dense_fp32_gemm_row_gb300.q8 import *  # noqa: E402,F401,F403
+
+__all__ += _q8.__all__

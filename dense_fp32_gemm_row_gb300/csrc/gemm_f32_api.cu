@@ -1033,6 +1033,27 @@ int run(const Problem& q, int algo, int splits, cudaStream_t stream,
     return enqueue(q, algo, splits, d, dev, stream, ev_begin, ev_end, tile);
 }
 
+}  // namespace
+
+namespace gemm_f32_impl {
+
+std::mutex& api_mutex() { return g_mutex; }
+
+int call_state(cudaStream_t stream, CallState* out) {
+    DeviceState* d = nullptr;
+    int dev = 0;
+    const int st = device_state(&d, &dev, &stream);
+    if (st != GEMM_F32_SUCCESS) return st;
+    out->dev = dev;
+    out->sm_count = d->sm_count;
+    out->fault = d->fault;
+    return GEMM_F32_SUCCESS;
+}
+
+}  // namespace gemm_f32_impl
+
+namespace {
+
 // ---- host-buffer entry: copies overlapped with the GEMM, by row panels ----
 constexpr int kMaxPanels = 16;
 constexpr int kMaxColBlocks = 4;  // column blocks of the first and last row panel

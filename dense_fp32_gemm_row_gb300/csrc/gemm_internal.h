@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 #include <cuda.h>
 #include <cuda_runtime_api.h>
 
@@ -183,6 +184,61 @@ cudaError_t launch_scale_c(float* C, long long ldc, int M, int N, float beta, cu
 cudaError_t launch_fill_zero(float* C, long long count, cudaStream_t s);
 // watchdog self-test: waits on a never-completed barrier for timeout_ns
 cudaError_t launch_watchdog_selftest(unsigned* fault, long long timeout_ns, cudaStream_t s);
+
+// ---- 8-bit activation checkpoints (q8_elementwise.cu, q8_wgrad.cu) ----------
+// One checkpoint's arrays (rows x cols codes, rows x ceil(cols / 32) exponent
+// bytes), as the kernels take them.
+struct Q8In {
+    const unsigned char* codes;
+    const unsigned char* scales;
+    long long ldcodes, ldscales;
+};
+struct Q8Out {
+    unsigned char* codes;
+    unsigned char* scales;
+    long long ldcodes, ldscales;
+};
+cudaError_t launch_q8_store(const float* x, long long ldx, int rows, int cols, int format,
+                            const Q8Out& q, cudaStream_t s);
+cudaError_t launch_q8_restore(const Q8In& q, int rows, int cols, int format, void* x,
+                              long long ldx, int bf16, cudaStream_t s);
+struct GatedArgs {
+    const float *g, *u;
+    float* h;
+    long long ldg, ldu, ldh;
+    Q8Out gq, uq;
+    int rows, cols, format, act;
+};
+cudaError_t launch_q8_gated(const GatedArgs& a, cudaStream_t s);
+struct GatedBackwardArgs {
+    Q8In gq, uq;
+    const float* dh;
+    float *dg, *du;
+    long long lddh, lddg, lddu;
+    Q8Out hq;  // codes null: not wanted
+    int rows, cols, format, act;
+};
+cudaError_t launch_q8_gated_backward(const GatedBackwardArgs& a, cudaStream_t s);
+struct Q8WgradArgs {
+    Q8In x;
+    const float* dy;
+    float* dw;
+    long long lddy, lddw;
+    int rows, cols, N, format;  // tokens, features of x, columns of dY
+    float alpha, beta;
+    int mode;  // epilogue.cuh
+};
+cudaError_t launch_q8_wgrad_ffma(const Q8WgradArgs& a, cudaStream_t s);
+
+// ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------
+// Device look-up and set-up, workspace and descriptors are one library-wide
+// state; api_mutex() is held around them and the launches of a call.
+struct CallState {
+    int dev, sm_count;
+    unsigned* fault;
+};
+std::mutex& api_mutex();
+int call_state(cudaStream_t stream, CallState* out);
 
 // gemm_f32_noalloc's fault word on device `dev` (0 if that entry point has
 // not set the device up); blocking read, zeroed afterwards when `clear`.

@@ -1,0 +1,236 @@
+// q8_api.cu -- the C ABI of the 8-bit activation checkpoints: argument
+// checks, the edge rules and kernel dispatch.  Empty matrices are a
+// successful no-op, as in the GEMM entry points; nothing here exits the
+// process.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <limits>
+
+#include "gemm_f32.h"
+#include "gemm_internal.h"
+
+using namespace gemm_f32_impl;
+
+namespace {
+
+// A matrix in memory, in bytes: `rows` rows of `width` bytes, `stride` apart.
+struct Region {
+    const void* base;
+    long long rows, width, stride;
+};
+
+// Whether two regions share a byte.  Matrices with the same stride may lie
+// side by side in the same rows of one buffer (the halves of a wider
+// product): then they are apart when their columns are.  With different
+// strides, address ranges that meet count as shared.
+bool share(const Region& a, const Region& b) {
+    if (!a.base || !b.base || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.base), b0 = reinterpret_cast<uintptr_t>(b.base);
+    const uintptr_t a1 = a0 + static_cast<uintptr_t>((a.rows - 1) * a.stride + a.width);
+    const uintptr_t b1 = b0 + static_cast<uintptr_t>((b.rows - 1) * b.stride + b.width);
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.stride != b.stride || a.rows == 1 || b.rows == 1) return true;
+    // b's first byte, counted from the start of the row of a that holds it
+    const long long diff = static_cast<long long>(b0) - static_cast<long long>(a0);
+    const long long at = ((diff % a.stride) + a.stride) % a.stride;
+    return !(at >= a.width && at + b.width <= a.stride);
+}
+
+bool bad_dims(long long rows, long long cols, long long ld) {
+    return ld < (cols > 1 ? cols : 1) ||
+           (rows > 0 && ld > std::numeric_limits<long long>::max() / 16 / rows);
+}
+
+// A float (or, elem = 2, bf16) matrix argument: pointer present and aligned
+// to its element, row stride at least the row.
+int check_matrix(const void* p, long long rows, long long cols, long long ld, int elem) {
+    if (bad_dims(rows, cols, ld) || !p) return GEMM_F32_ERR_INVALID_VALUE;
+    if (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(elem - 1))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    return GEMM_F32_SUCCESS;
+}
+
+Region region(const void* p, long long rows, long long cols, long long ld, int elem) {
+    return {p, rows, cols * elem, ld * elem};
+}
+
+long long blocks_of(long long cols) {
+    return (cols + GEMM_F32_Q8_BLOCK - 1) / GEMM_F32_Q8_BLOCK;
+}
+
+int check_shape(const gemm_f32_q8* q) {
+    if (!q || q->rows < 0 || q->cols < 0) return GEMM_F32_ERR_INVALID_VALUE;
+    if (q->format != GEMM_F32_Q8_INT8 && q->format != GEMM_F32_Q8_E4M3)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    return GEMM_F32_SUCCESS;
+}
+
+// The arrays of a nonempty checkpoint: 16-byte aligned, row strides multiples
+// of 16 bytes that hold a row.
+int check_arrays(const gemm_f32_q8* q) {
+    if (!q->codes || !q->scales) return GEMM_F32_ERR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(q->codes) | reinterpret_cast<uintptr_t>(q->scales)) & 15u)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if ((q->ldcodes & 15) || (q->ldscales & 15)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (bad_dims(q->rows, q->cols, q->ldcodes) ||
+        bad_dims(q->rows, blocks_of(q->cols), q->ldscales))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    return GEMM_F32_SUCCESS;
+}
+
+Region codes_of(const gemm_f32_q8* q) { return region(q->codes, q->rows, q->cols, q->ldcodes, 1); }
+Region scales_of(const gemm_f32_q8* q) {
+    return region(q->scales, q->rows, blocks_of(q->cols), q->ldscales, 1);
+}
+
+// Outputs that share memory with one another or with an input.
+int check_apart(const Region* out, int nout, const Region* in, int nin) {
+    for (int i = 0; i < nout; ++i) {
+        for (int j = i + 1; j < nout; ++j)
+            if (share(out[i], out[j])) return GEMM_F32_ERR_INVALID_VALUE;
+        for (int j = 0; j < nin; ++j)
+            if (share(out[i], in[j])) return GEMM_F32_ERR_INVALID_VALUE;
+    }
+    return GEMM_F32_SUCCESS;
+}
+
+bool same_shape(const gemm_f32_q8* a, const gemm_f32_q8* b) {
+    return a->rows == b->rows && a->cols == b->cols && a->format == b->format;
+}
+
+Q8In in_of(const gemm_f32_q8* q) { return {q->codes, q->scales, q->ldcodes, q->ldscales}; }
+Q8Out out_of(const gemm_f32_q8* q) { return {q->codes, q->scales, q->ldcodes, q->ldscales}; }
+
+int status(cudaError_t e) { return e == cudaSuccess ? GEMM_F32_SUCCESS : static_cast<int>(e); }
+
+}  // namespace
+
+#define Q8_TRY(expr)                                  \
+    do {                                              \
+        const int st_ = (expr);                       \
+        if (st_ != GEMM_F32_SUCCESS) return st_;      \
+    } while (0)
+
+extern "C" {
+
+int gemm_f32_q8_store(const float* X, long long ldx, const gemm_f32_q8* q, cudaStream_t stream) {
+    Q8_TRY(check_shape(q));
+    if (q->rows == 0 || q->cols == 0) return GEMM_F32_SUCCESS;
+    Q8_TRY(check_arrays(q));
+    Q8_TRY(check_matrix(X, q->rows, q->cols, ldx, 4));
+    const Region out[] = {codes_of(q), scales_of(q)};
+    const Region in[] = {region(X, q->rows, q->cols, ldx, 4)};
+    Q8_TRY(check_apart(out, 2, in, 1));
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState c;
+    Q8_TRY(call_state(stream, &c));
+    return status(launch_q8_store(X, ldx, q->rows, q->cols, q->format, out_of(q), stream));
+}
+
+int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
+                        cudaStream_t stream) {
+    Q8_TRY(check_shape(q));
+    if (type != GEMM_F32_Q8_TO_F32 && type != GEMM_F32_Q8_TO_BF16)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    if (q->rows == 0 || q->cols == 0) return GEMM_F32_SUCCESS;
+    const int elem = type == GEMM_F32_Q8_TO_F32 ? 4 : 2;
+    Q8_TRY(check_arrays(q));
+    Q8_TRY(check_matrix(X, q->rows, q->cols, ldx, elem));
+    const Region out[] = {region(X, q->rows, q->cols, ldx, elem)};
+    const Region in[] = {codes_of(q), scales_of(q)};
+    Q8_TRY(check_apart(out, 1, in, 2));
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState c;
+    Q8_TRY(call_state(stream, &c));
+    return status(launch_q8_restore(in_of(q), q->rows, q->cols, q->format, X, ldx, elem == 2,
+                                    stream));
+}
+
+int gemm_f32_q8_gated(int act, const float* G, long long ldg, const float* U, long long ldu,
+                      float* H, long long ldh, const gemm_f32_q8* gq, const gemm_f32_q8* uq,
+                      cudaStream_t stream) {
+    if (act != GEMM_F32_ACT_SILU && act != GEMM_F32_ACT_GELU) return GEMM_F32_ERR_INVALID_VALUE;
+    Q8_TRY(check_shape(gq));
+    Q8_TRY(check_shape(uq));
+    if (!same_shape(gq, uq)) return GEMM_F32_ERR_INVALID_VALUE;
+    const int rows = gq->rows, cols = gq->cols;
+    if (rows == 0 || cols == 0) return GEMM_F32_SUCCESS;
+    Q8_TRY(check_arrays(gq));
+    Q8_TRY(check_arrays(uq));
+    Q8_TRY(check_matrix(G, rows, cols, ldg, 4));
+    Q8_TRY(check_matrix(U, rows, cols, ldu, 4));
+    Q8_TRY(check_matrix(H, rows, cols, ldh, 4));
+    const Region out[] = {region(H, rows, cols, ldh, 4), codes_of(gq), scales_of(gq), codes_of(uq),
+                          scales_of(uq)};
+    const Region in[] = {region(G, rows, cols, ldg, 4), region(U, rows, cols, ldu, 4)};
+    Q8_TRY(check_apart(out, 5, in, 2));
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState c;
+    Q8_TRY(call_state(stream, &c));
+    GatedArgs a = {G, U, H, ldg, ldu, ldh, out_of(gq), out_of(uq), rows, cols, gq->format, act};
+    return status(launch_q8_gated(a, stream));
+}
+
+int gemm_f32_q8_gated_backward(int act, const gemm_f32_q8* gq, const gemm_f32_q8* uq,
+                               const float* dH, long long lddh, float* dG, long long lddg,
+                               float* dU, long long lddu, const gemm_f32_q8* hq,
+                               cudaStream_t stream) {
+    if (act != GEMM_F32_ACT_SILU && act != GEMM_F32_ACT_GELU) return GEMM_F32_ERR_INVALID_VALUE;
+    Q8_TRY(check_shape(gq));
+    Q8_TRY(check_shape(uq));
+    if (!same_shape(gq, uq)) return GEMM_F32_ERR_INVALID_VALUE;
+    if (hq) {
+        Q8_TRY(check_shape(hq));
+        if (!same_shape(gq, hq)) return GEMM_F32_ERR_INVALID_VALUE;
+    }
+    const int rows = gq->rows, cols = gq->cols;
+    if (rows == 0 || cols == 0) return GEMM_F32_SUCCESS;
+    Q8_TRY(check_arrays(gq));
+    Q8_TRY(check_arrays(uq));
+    if (hq) Q8_TRY(check_arrays(hq));
+    Q8_TRY(check_matrix(dH, rows, cols, lddh, 4));
+    Q8_TRY(check_matrix(dG, rows, cols, lddg, 4));
+    Q8_TRY(check_matrix(dU, rows, cols, lddu, 4));
+    Region out[4] = {region(dG, rows, cols, lddg, 4), region(dU, rows, cols, lddu, 4)};
+    const Region in[] = {region(dH, rows, cols, lddh, 4), codes_of(gq), scales_of(gq), codes_of(uq),
+                         scales_of(uq)};
+    int nout = 2;
+    if (hq) {
+        out[nout++] = codes_of(hq);
+        out[nout++] = scales_of(hq);
+    }
+    Q8_TRY(check_apart(out, nout, in, 5));
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState c;
+    Q8_TRY(call_state(stream, &c));
+    GatedBackwardArgs a = {in_of(gq), in_of(uq), dH, dG, dU, lddh, lddg, lddu,
+                           hq ? out_of(hq) : Q8Out{nullptr, nullptr, 0, 0},
+                           rows, cols, gq->format, act};
+    return status(launch_q8_gated_backward(a, stream));
+}
+
+int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int N, float alpha,
+                      float beta, float* dW, long long lddw, cudaStream_t stream) {
+    Q8_TRY(check_shape(x));
+    if (N < 0) return GEMM_F32_ERR_INVALID_VALUE;
+    if (x->cols == 0 || N == 0) return GEMM_F32_SUCCESS;
+    Q8_TRY(check_matrix(dW, x->cols, N, lddw, 4));
+    const bool reads = x->rows > 0 && alpha != 0.0f;
+    if (x->rows > 0) {
+        Q8_TRY(check_arrays(x));
+        Q8_TRY(check_matrix(dY, x->rows, N, lddy, 4));
+        const Region out[] = {region(dW, x->cols, N, lddw, 4)};
+        const Region in[] = {codes_of(x), scales_of(x), region(dY, x->rows, N, lddy, 4)};
+        Q8_TRY(check_apart(out, 1, in, 3));
+    }
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState c;
+    Q8_TRY(call_state(stream, &c));
+    if (!reads) return status(launch_scale_c(dW, lddw, x->cols, N, beta, stream));
+    Q8WgradArgs a = {in_of(x), dY, dW, lddy, lddw, x->rows, x->cols, N, x->format, alpha, beta,
+                     beta != 0.0f ? 2 : alpha == 1.0f ? 0 : 1};
+    return status(launch_q8_wgrad_ffma(a, stream));
+}
+
+}  // extern "C"

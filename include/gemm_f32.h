@@ -344,6 +344,104 @@ int gemm_f32_noalloc(const float* A, const float* B, float* C, int M, int N, int
  */
 int gemm_f32_noalloc_selftest_watchdog(long long timeout_ns, cudaStream_t stream);
 
+/* ---- 8-bit activation checkpoints -------------------------------------- */
+/*
+ * What a training step keeps of a layer between its forward and its backward
+ * pass, in 8 bits an element, and the operators of the backward pass that
+ * read it in that form: the weight gradient of a linear layer and the
+ * derivative of a gated unit.  The pages have no counterpart: these serve the
+ * callers that use the product above to train.
+ *
+ * The form: rows x cols elements, a code byte each, and for each block of 32
+ * consecutive columns of a row (the last may be shorter) one exponent byte E,
+ * the power-of-two scale of the OCP microscaling formats:
+ *   GEMM_F32_Q8_INT8   value = code * 2^(E - 133), code in -127 .. 127
+ *   GEMM_F32_Q8_E4M3   value = code * 2^(E - 127), code an 8-bit float with 4
+ *                      exponent and 3 mantissa bits, at most 448
+ * E is the smallest exponent at which the block's largest magnitude fits
+ * (INT8: at most 127 * 2^(E-133); E4M3: at most 448 * 2^(E-127)), but at
+ * least 7 (10 for E4M3), so that every nonzero value is a normal float, and
+ * for INT8 at most 254.  Codes are rounded to nearest, ties to even.  A block
+ * that holds a NaN or an infinity gets E = 255 and codes 0, and all of it
+ * restores to NaN.  An E below its least value reads as a scale of zero.
+ * Every value is exactly representable in bf16.
+ *
+ * Layout: row i's codes are at codes + i * ldcodes, its exponents at scales +
+ * i * ldscales (bytes).  Both arrays are in device memory, 16-byte aligned,
+ * with row strides that are multiples of 16, ldcodes >= cols and ldscales >=
+ * ceil(cols / 32).  Bytes beyond a row's last column or block are neither
+ * read for their value nor written.  The caller owns them.
+ *
+ * For all five entry points: matrices are row-major with leading dimensions
+ * in elements, any 4-byte (bf16: 2-byte) alignment and any leading dimension
+ * at least the row; an output may not share an element with an input or
+ * another output (matrices side by side in one buffer, with equal leading
+ * dimensions, are apart), else GEMM_F32_ERR_INVALID_VALUE; a matrix without
+ * elements is a successful no-op; asynchronous on `stream`, with the status
+ * codes, workspace and graph-capture rules above.  Results are deterministic.
+ */
+#define GEMM_F32_Q8_INT8   0
+#define GEMM_F32_Q8_E4M3   1
+#define GEMM_F32_Q8_BLOCK  32
+typedef struct gemm_f32_q8 {
+    unsigned char* codes;
+    unsigned char* scales;
+    long long ldcodes;
+    long long ldscales;
+    int rows;
+    int cols;
+    int format; /* GEMM_F32_Q8_INT8 or _E4M3 */
+} gemm_f32_q8;
+
+/* gemm_f32_q8_store -- write the 8-bit form of X (q->rows x q->cols floats,
+ * row stride ldx) into q's arrays. */
+int gemm_f32_q8_store(const float* X, long long ldx, const gemm_f32_q8* q, cudaStream_t stream);
+
+/* gemm_f32_q8_restore -- write the values that q stands for to X (row stride
+ * ldx elements), as floats or, also exactly, as bf16. */
+#define GEMM_F32_Q8_TO_F32   0
+#define GEMM_F32_Q8_TO_BF16  1
+int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
+                        cudaStream_t stream);
+
+/*
+ * gemm_f32_q8_wgrad -- the weight gradient of a linear layer Y = X W from
+ * the 8-bit form x of its input (x->rows tokens, x->cols features):
+ *
+ *     dW = alpha * x^T * dY + beta * dW
+ *
+ * dY is x->rows x N (row stride lddy), dW x->cols x N (row stride lddw).
+ * x's values enter exactly and products are summed in fp32 (see the accuracy
+ * note in q8_wgrad.cu).  With beta == 0 the old dW is not read; with alpha ==
+ * 0 or no rows, x and dY are not read and dW = beta * dW.  A NaN or infinity
+ * in dY or a block of x that restores to NaN gives non-finite outputs in the
+ * columns or rows of dW it enters.
+ */
+int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int N, float alpha,
+                      float beta, float* dW, long long lddw, cudaStream_t stream);
+
+/*
+ * gemm_f32_q8_gated -- the forward pass of a gated unit, H = act(G) * U
+ * elementwise, which also stores G and U in gq and uq (equal rows, cols and
+ * format) for the backward pass.  H comes from G and U as given, not from
+ * their 8-bit form.  act: GEMM_F32_ACT_SILU (z / (1 + e^-z)) or
+ * GEMM_F32_ACT_GELU (z times the normal distribution function of z).
+ *
+ * gemm_f32_q8_gated_backward -- from those and dH:
+ *     dU = dH * act(G^),   dG = dH * U^ * act'(G^)
+ * and, with hq not NULL, the 8-bit form of act(G^) * U^, the input of the
+ * layer that follows, for its weight gradient: H need not be kept.
+ */
+#define GEMM_F32_ACT_SILU 0
+#define GEMM_F32_ACT_GELU 1
+int gemm_f32_q8_gated(int act, const float* G, long long ldg, const float* U, long long ldu,
+                      float* H, long long ldh, const gemm_f32_q8* gq, const gemm_f32_q8* uq,
+                      cudaStream_t stream);
+int gemm_f32_q8_gated_backward(int act, const gemm_f32_q8* gq, const gemm_f32_q8* uq,
+                               const float* dH, long long lddh, float* dG, long long lddg,
+                               float* dU, long long lddu, const gemm_f32_q8* hq,
+                               cudaStream_t stream);
+
 /* Release every workspace (synchronises each device that has one). */
 int gemm_f32_release(void);
 
