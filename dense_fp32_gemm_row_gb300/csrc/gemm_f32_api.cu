@@ -132,19 +132,27 @@ int get_encoder() {
     return GEMM_F32_SUCCESS;
 }
 
-// 2-D fp32 tensor map over a row-major matrix: dim0 (contiguous) x dim1 rows
-// with a row stride of ld elements.
-int encode_2d(CUtensorMap* map, const float* base, long long dim0, long long dim1, long long ld,
-              int box0, int box1, CUtensorMapSwizzle swizzle) {
+// 2-D tensor map over a row-major matrix: dim0 (contiguous) x dim1 rows,
+// ld_bytes apart.
+int encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long dim0,
+               long long dim1, long long ld_bytes, int box0, int box1,
+               CUtensorMapSwizzle swizzle) {
     if (injected(GEMM_F32_INJECT_DESCRIPTOR)) return GEMM_F32_ERR_DESCRIPTOR;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim0), static_cast<cuuint64_t>(dim1)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 4u};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld_bytes)};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1)};
     const cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+    CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_F32_SUCCESS : GEMM_F32_ERR_DESCRIPTOR;
+}
+
+// The same for floats, with the row stride in elements.
+int encode_2d(CUtensorMap* map, const float* base, long long dim0, long long dim1, long long ld,
+              int box0, int box1, CUtensorMapSwizzle swizzle) {
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, dim0, dim1, 4 * ld, box0, box1,
+                      swizzle);
 }
 
 // Workspace of at least `bytes` for (dev, stream); g_mutex must be held.
@@ -1048,6 +1056,21 @@ int call_state(cudaStream_t stream, CallState* out) {
     out->sm_count = d->sm_count;
     out->fault = d->fault;
     return GEMM_F32_SUCCESS;
+}
+
+int call_workspace(const CallState& c, cudaStream_t stream, size_t bytes, unsigned char** out) {
+    void* w = nullptr;
+    const int st = workspace(c.dev, stream, bytes, &w);
+    *out = static_cast<unsigned char*>(w);
+    return st;
+}
+
+int call_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long dim0,
+                    long long dim1, long long ld_bytes, int box0, int box1) {
+    const int st = get_encoder();
+    if (st != GEMM_F32_SUCCESS) return st;
+    return encode_map(map, type, base, dim0, dim1, ld_bytes, box0, box1,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace gemm_f32_impl

@@ -229,6 +229,28 @@ struct Q8WgradArgs {
     int mode;  // epilogue.cuh
 };
 cudaError_t launch_q8_wgrad_ffma(const Q8WgradArgs& a, cudaStream_t s);
+// The tensor-core form: CTA pairs, 256 x 256 tiles.  tmY is dY as {N, T}
+// floats, box 128 x 32; tmC the codes as {cols, T} bytes, box 128 x 32; tmS
+// the exponents as {ceil(cols / 32), T} bytes, box 16 x 32; none swizzled.
+// out is dW, or with splits > 1 the partials (alpha, beta by mode).
+struct Q8WgradTile {
+    int features, columns, tokens;  // of a tile; of a pipeline stage
+};
+Q8WgradTile q8_wgrad_tile();
+struct Q8WgradPairArgs {
+    CUtensorMap tmY, tmC, tmS;
+    float* out;
+    long long ldo, split_stride;
+    int rows, cols, N, format;
+    int kb_per_split;  // stages per split; every split has at least one
+    int splits;
+    int chunk;         // stages per tensor-core sum
+    unsigned* fault;
+    long long timeout_ns;
+    float alpha, beta;
+    int mode;
+};
+cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count);
 
 // ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------
 // Device look-up and set-up, workspace and descriptors are one library-wide
@@ -239,6 +261,12 @@ struct CallState {
 };
 std::mutex& api_mutex();
 int call_state(cudaStream_t stream, CallState* out);
+// at least `bytes` for the device and stream; the first
+// kWorkspaceCounterBytes are the in-kernel reductions'
+int call_workspace(const CallState& c, cudaStream_t stream, size_t bytes, unsigned char** out);
+// a 2-D tensor map: dim0 contiguous elements, dim1 rows ld_bytes apart
+int call_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long dim0,
+                    long long dim1, long long ld_bytes, int box0, int box1);
 
 // gemm_f32_noalloc's fault word on device `dev` (0 if that entry point has
 // not set the device up); blocking read, zeroed afterwards when `clear`.

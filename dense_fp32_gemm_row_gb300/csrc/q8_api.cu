@@ -102,6 +102,48 @@ bool same_shape(const gemm_f32_q8* a, const gemm_f32_q8* b) {
 Q8In in_of(const gemm_f32_q8* q) { return {q->codes, q->scales, q->ldcodes, q->ldscales}; }
 Q8Out out_of(const gemm_f32_q8* q) { return {q->codes, q->scales, q->ldcodes, q->ldscales}; }
 
+long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
+
+// How the tensor-core kernel would run a weight gradient.
+struct WgradPlan {
+    int splits, kb_per_split, chunk;
+    int copy;                // dY goes through a padded copy
+    long long ldy;           // row stride of what the kernel reads
+    long long ldw;           // row stride of the split partials
+    size_t off_copy, off_parts, bytes;
+};
+
+WgradPlan plan_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
+    const Q8WgradTile tile = q8_wgrad_tile();
+    WgradPlan p = {};
+    const long long tiles = ((a.cols - 1LL) / tile.features + 1) * ((a.N - 1LL) / tile.columns + 1);
+    const int kb_total = (a.rows - 1) / tile.tokens + 1;
+    const int clusters = sm_count / 2;
+    long long s = splits;
+    if (s == 0) {
+        // spread few tiles over the clusters, at least four stages each
+        s = 2 * tiles <= clusters ? clusters / tiles : 1;
+        if (s > kb_total / 4) s = kb_total / 4;
+    }
+    if (s > kb_total) s = kb_total;
+    if (s < 1) s = 1;
+    p.kb_per_split = static_cast<int>((kb_total + s - 1) / s);
+    p.splits = (kb_total + p.kb_per_split - 1) / p.kb_per_split;  // none of them empty
+    p.chunk = 4;
+    // TMA reads rows that start on 16-byte boundaries
+    p.ldy = a.rows == 1 ? round_up(a.N, 4) : a.lddy;
+    p.copy = (reinterpret_cast<uintptr_t>(a.dy) & 15u) || (p.ldy & 3);
+    if (p.copy) p.ldy = round_up(a.N, 4);
+    p.ldw = round_up(a.N, 4);
+    size_t off = kWorkspaceCounterBytes;
+    p.off_copy = off;
+    if (p.copy) off += static_cast<size_t>(round_up(p.ldy * a.rows * 4, 256));
+    p.off_parts = off;
+    if (p.splits > 1) off += static_cast<size_t>(p.ldw * a.cols * 4) * p.splits;
+    p.bytes = p.copy || p.splits > 1 ? off : 0;
+    return p;
+}
+
 int status(cudaError_t e) { return e == cudaSuccess ? GEMM_F32_SUCCESS : static_cast<int>(e); }
 
 }  // namespace
@@ -211,9 +253,12 @@ int gemm_f32_q8_gated_backward(int act, const gemm_f32_q8* gq, const gemm_f32_q8
 }
 
 int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int N, float alpha,
-                      float beta, float* dW, long long lddw, cudaStream_t stream) {
+                      float beta, float* dW, long long lddw, int algo, int splits,
+                      cudaStream_t stream) {
     Q8_TRY(check_shape(x));
-    if (N < 0) return GEMM_F32_ERR_INVALID_VALUE;
+    if (N < 0 || splits < 0 || splits > GEMM_F32_MAX_SPLITS) return GEMM_F32_ERR_INVALID_VALUE;
+    if (algo != GEMM_F32_ALGO_AUTO && algo != GEMM_F32_ALGO_FFMA && algo != GEMM_F32_ALGO_3XBF16)
+        return GEMM_F32_ERR_INVALID_VALUE;
     if (x->cols == 0 || N == 0) return GEMM_F32_SUCCESS;
     Q8_TRY(check_matrix(dW, x->cols, N, lddw, 4));
     const bool reads = x->rows > 0 && alpha != 0.0f;
@@ -230,7 +275,47 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     if (!reads) return status(launch_scale_c(dW, lddw, x->cols, N, beta, stream));
     Q8WgradArgs a = {in_of(x), dY, dW, lddy, lddw, x->rows, x->cols, N, x->format, alpha, beta,
                      beta != 0.0f ? 2 : alpha == 1.0f ? 0 : 1};
-    return status(launch_q8_wgrad_ffma(a, stream));
+    if (algo == GEMM_F32_ALGO_AUTO)
+        algo = 1.0 * x->rows * x->cols * N < 5e7 ? GEMM_F32_ALGO_FFMA : GEMM_F32_ALGO_3XBF16;
+    if (algo == GEMM_F32_ALGO_FFMA) return status(launch_q8_wgrad_ffma(a, stream));
+
+    const WgradPlan p = plan_wgrad(a, splits, c.sm_count);
+    unsigned char* ws = nullptr;
+    if (p.bytes) Q8_TRY(call_workspace(c, stream, p.bytes, &ws));
+    const float* dy = dY;
+    if (p.copy) dy = reinterpret_cast<const float*>(ws + p.off_copy);
+    const Q8WgradTile tile = q8_wgrad_tile();
+    Q8WgradPairArgs k = {};
+    Q8_TRY(call_tensor_map(&k.tmY, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dy, N, x->rows, 4 * p.ldy,
+                           tile.columns / 2, tile.tokens));
+    Q8_TRY(call_tensor_map(&k.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->codes, x->cols, x->rows,
+                           x->ldcodes, tile.features / 2, tile.tokens));
+    Q8_TRY(call_tensor_map(&k.tmS, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->scales, blocks_of(x->cols),
+                           x->rows, x->ldscales, 16, tile.tokens));
+    if (p.copy)
+        Q8_TRY(status(launch_pad_copy(dY, lddy, x->rows, N,
+                                      reinterpret_cast<float*>(ws + p.off_copy), p.ldy, stream)));
+    float* parts = reinterpret_cast<float*>(ws + p.off_parts);
+    const long long part_stride = p.ldw * x->cols;
+    k.out = p.splits > 1 ? parts : dW;
+    k.ldo = p.splits > 1 ? p.ldw : lddw;
+    k.split_stride = part_stride;
+    k.rows = x->rows;
+    k.cols = x->cols;
+    k.N = N;
+    k.format = x->format;
+    k.kb_per_split = p.kb_per_split;
+    k.splits = p.splits;
+    k.chunk = p.chunk;
+    k.fault = c.fault;
+    k.timeout_ns = kDefaultTimeoutNs;
+    k.alpha = alpha;
+    k.beta = beta;
+    k.mode = p.splits > 1 ? 0 : a.mode;
+    Q8_TRY(status(launch_q8_wgrad_pair(k, stream, c.dev, c.sm_count)));
+    if (p.splits == 1) return GEMM_F32_SUCCESS;
+    return status(launch_splitk_reduce(parts, part_stride, p.ldw, p.splits, dW, lddw, x->cols, N,
+                                       alpha, beta, a.mode, stream));
 }
 
 }  // extern "C"

@@ -28,7 +28,7 @@ import dense_fp32_gemm_row_gb300 as _g
 
 __all__ = [
     "Q8", "Q8Struct", "Q8_INT8", "Q8_E4M3", "Q8_FORMATS", "Q8_BLOCK", "Q8_TO_F32", "Q8_TO_BF16",
-    "ACT_SILU", "ACT_GELU", "ACTS", "gemm_f32_q8_store", "gemm_f32_q8_restore",
+    "ACT_SILU", "ACT_GELU", "ACTS", "ALGO_3XBF16", "Q8_ALGOS", "gemm_f32_q8_store", "gemm_f32_q8_restore",
     "gemm_f32_q8_wgrad", "gemm_f32_q8_gated", "gemm_f32_q8_gated_backward", "q8_empty",
     "q8_store", "q8_restore", "q8_wgrad", "q8_gated", "q8_gated_backward",
 ]
@@ -41,6 +41,8 @@ Q8_TO_F32 = 0
 Q8_TO_BF16 = 1
 ACT_SILU = 0
 ACT_GELU = 1
+ALGO_3XBF16 = 3
+Q8_ALGOS = {"auto": 0, "ffma": 1, "3xbf16": ALGO_3XBF16}
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 
 
@@ -63,9 +65,9 @@ def gemm_f32_q8_restore(q, X, ldx, type=Q8_TO_F32, stream=0) -> int:
     return _g.load().gemm_f32_q8_restore(q, _g._p(X), ldx, type, _g._p(stream))
 
 
-def gemm_f32_q8_wgrad(x, dY, lddy, N, alpha, beta, dW, lddw, stream=0) -> int:
-    return _g.load().gemm_f32_q8_wgrad(x, _g._p(dY), lddy, N, alpha, beta, _g._p(dW), lddw,
-                                       _g._p(stream))
+def gemm_f32_q8_wgrad(x, dY, lddy, N, alpha, beta, dW, lddw, algo=0, splits=0, stream=0) -> int:
+    return _g.load().gemm_f32_q8_wgrad(x, _g._p(dY), lddy, N, alpha, beta, _g._p(dW), lddw, algo,
+                                       splits, _g._p(stream))
 
 
 def gemm_f32_q8_gated(act, G, ldg, U, ldu, H, ldh, gq, uq, stream=0) -> int:
@@ -84,7 +86,7 @@ def _declare(lib) -> None:
     q = ctypes.POINTER(Q8Struct)
     lib.gemm_f32_q8_store.argtypes = [vp, ll, q, vp]
     lib.gemm_f32_q8_restore.argtypes = [q, vp, ll, i, vp]
-    lib.gemm_f32_q8_wgrad.argtypes = [q, vp, ll, i, f, f, vp, ll, vp]
+    lib.gemm_f32_q8_wgrad.argtypes = [q, vp, ll, i, f, f, vp, ll, i, i, vp]
     lib.gemm_f32_q8_gated.argtypes = [i, vp, ll, vp, ll, vp, ll, q, q, vp]
     lib.gemm_f32_q8_gated_backward.argtypes = [i, q, q, vp, ll, vp, ll, vp, ll, q, vp]
     for name in ("store", "restore", "wgrad", "gated", "gated_backward"):
@@ -276,15 +278,18 @@ def q8_restore(q, out=None, dtype=None, stream=None):
     return x
 
 
-def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, stream=None):
+def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream=None):
     """``out = alpha * x_hat.T @ dy + beta * out`` from the checkpoint ``q`` of x.
 
     ``dy`` is (q.rows, N); ``out`` (q.cols, N) is allocated if not given, and
-    must be given for ``beta`` other than 0 (gradient accumulation).
+    must be given for ``beta`` other than 0 (gradient accumulation).  ``algo``
+    is "auto", "ffma" or "3xbf16" (the tensor-core kernel), ``splits`` the
+    number of ranges the latter splits the tokens into (0: chosen by size).
     """
     import torch
 
     ldy = _ld(dy, "dy")
+    code = _name(Q8_ALGOS, algo, "algo")
     N = dy.shape[1]
     _shape(dy, (q.rows, N), "dy")
     _same_device(q.codes.device, dy, out)
@@ -294,7 +299,7 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, stream=None):
         dw = torch.empty((q.cols, N), dtype=torch.float32, device=dy.device) if out is None else out
         _shape(dw, (q.cols, N), "out")
         st = gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(),
-                               _ld(dw, "out"), c.stream.cuda_stream)
+                               _ld(dw, "out"), code, splits, c.stream.cuda_stream)
         c.uses(q, dy, out)
     _g.check(st, "q8_wgrad")
     return dw

@@ -411,14 +411,20 @@ int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
  *     dW = alpha * x^T * dY + beta * dW
  *
  * dY is x->rows x N (row stride lddy), dW x->cols x N (row stride lddw).
- * x's values enter exactly and products are summed in fp32 (see the accuracy
- * note in q8_wgrad.cu).  With beta == 0 the old dW is not read; with alpha ==
+ * x's values enter exactly and products are summed in fp32.  algo:
+ * GEMM_F32_ALGO_FFMA, the CUDA-core kernel; GEMM_F32_ALGO_3XBF16 (this entry
+ * point's alone), the tensor-core kernel, which splits each float of dY
+ * exactly into three bf16 parts; GEMM_F32_ALGO_AUTO, chosen by size.  splits:
+ * for the tensor-core kernel, over how many ranges the tokens are split, as
+ * for gemm_f32_algo_splitk (0: the library chooses).  With beta == 0 the old dW is not read; with alpha ==
  * 0 or no rows, x and dY are not read and dW = beta * dW.  A NaN or infinity
  * in dY or a block of x that restores to NaN gives non-finite outputs in the
  * columns or rows of dW it enters.
  */
+#define GEMM_F32_ALGO_3XBF16 3
 int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int N, float alpha,
-                      float beta, float* dW, long long lddw, cudaStream_t stream);
+                      float beta, float* dW, long long lddw, int algo, int splits,
+                      cudaStream_t stream);
 
 /*
  * gemm_f32_q8_gated -- the forward pass of a gated unit, H = act(G) * U

@@ -333,11 +333,60 @@ WGRAD_SHAPES = [(1, 1, 1), (1, 40, 5), (2, 32, 4), (15, 33, 3), (16, 64, 64), (1
                 (255, 260, 4), (256, 4, 260), (257, 300, 516), (1000, 333, 77), (1025, 1000, 24)]
 
 
+ALGOS = ("ffma", "3xbf16")
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("T", [33, 700])
+def test_wgrad_of_exact_sums_is_exact(T, algo):
+    """Small integers: every product and partial sum fits fp32, so every path gives the same bits."""
+    rng = np.random.default_rng(T)
+    x = rng.integers(-127, 128, (T, 200)).astype(np.float32)
+    x[:, ::32] = 127  # exponent byte 133: the codes are the integers
+    dy = rng.integers(-64, 65, (T, 130)).astype(np.float32) + 0.0
+    q = g.q8_store(matrix(x)[0])
+    assert np.array_equal(g.q8_wgrad(q, matrix(dy)[0], algo=algo).double().cpu().numpy(),
+                          x.astype(np.float64).T @ dy.astype(np.float64))
+
+
+@pytest.mark.parametrize("algo", ALGOS)
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,D,N", WGRAD_SHAPES)
-def test_wgrad(fmt, T, D, N):
+def test_wgrad(fmt, T, D, N, algo):
     q, x, dy = wgrad_case(np.random.default_rng(T + D + N), T, D, N, fmt)
-    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0]), x, dy)
+    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0], algo=algo), x, dy)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,D,N,splits", [(100, 40, 50, 1), (100, 40, 50, 2), (100, 40, 50, 4),
+                                          (100, 40, 50, 256), (1000, 300, 301, 7),
+                                          (5000, 257, 100, 33), (5000, 257, 100, 256)])
+def test_wgrad_split_over_tokens(fmt, T, D, N, splits):
+    q, x, dy = wgrad_case(np.random.default_rng(T + splits), T, D, N, fmt)
+    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0], algo="3xbf16", splits=splits), x, dy)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_wgrad_of_every_code_and_exponent(fmt, algo):
+    """All codes the format has under exponents over its whole range, one token at a time in effect
+    (dY a one-hot row), so that every output is one exact value."""
+    torch = t()
+    least = 7 if fmt == "int8" else 10
+    exps = np.concatenate([np.arange(least, 248, 12), [least, 133, 127, 247]]).astype(np.uint8)
+    code = np.array([c for c in range(256) if fmt == "int8" or c & 127 != 127], dtype=np.uint8)
+    code = np.resize(code, 256)
+    T, D = len(exps), 256
+    q = g.q8_empty(T, D, fmt)
+    q.codes[:, :D] = torch.from_numpy(np.tile(code, (T, 1))).cuda()
+    q.scales[:, :8] = torch.from_numpy(np.tile(exps[:, None], (1, 8))).cuda()
+    got = g.q8_wgrad(q, torch.eye(T, device="cuda"), algo=algo).cpu().numpy()
+    want = _q8.values(np.tile(code, (T, 1)), np.tile(exps[:, None], (1, 8)), fmt).T
+    # 448 * 2^120 is beyond fp32: an infinity, which times the other columns' zeros is NaN
+    over = np.abs(want).max(axis=1) > np.finfo(np.float32).max
+    assert over.any() == (fmt == "e4m3")
+    assert np.array_equal(got[~over], want[~over].astype(np.float32))
+    assert not np.isfinite(got[over]).any()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -419,18 +468,6 @@ def test_wgrad_runs_alike_every_time(T, D, N):
     first = g.q8_wgrad(q, dev)
     for _ in range(5):
         assert bool((g.q8_wgrad(q, dev) == first).all())
-
-
-@pytest.mark.parametrize("T", [33, 700])
-def test_wgrad_of_exact_sums_is_exact(T):
-    """Small integers: every product and partial sum fits fp32, so every path gives the same bits."""
-    rng = np.random.default_rng(T)
-    x = rng.integers(-127, 128, (T, 200)).astype(np.float32)
-    x[:, ::32] = 127  # exponent byte 133: the codes are the integers
-    dy = rng.integers(-64, 65, (T, 130)).astype(np.float32) + 0.0
-    q = g.q8_store(matrix(x)[0])
-    assert np.array_equal(g.q8_wgrad(q, matrix(dy)[0]).double().cpu().numpy(),
-                          x.astype(np.float64).T @ dy.astype(np.float64))
 
 
 def test_wgrad_against_differences_of_the_product():
