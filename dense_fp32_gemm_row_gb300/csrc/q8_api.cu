@@ -129,7 +129,7 @@ WgradPlan plan_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
     if (s < 1) s = 1;
     p.kb_per_split = static_cast<int>((kb_total + s - 1) / s);
     p.splits = (kb_total + p.kb_per_split - 1) / p.kb_per_split;  // none of them empty
-    p.chunk = 4;
+    p.chunk = 8;
     // TMA reads rows that start on 16-byte boundaries
     p.ldy = a.rows == 1 ? round_up(a.N, 4) : a.lddy;
     p.copy = (reinterpret_cast<uintptr_t>(a.dy) & 15u) || (p.ldy & 3);

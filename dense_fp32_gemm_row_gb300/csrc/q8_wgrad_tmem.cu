@@ -29,20 +29,31 @@
 // its share; dY in shared memory as well (both operands, three parts) would
 // take more than the whole.
 //
-// 512 threads per CTA, registers rebalanced at start (launched at 128 each):
-//   warp 0      one lane: TMA loads of a 32-token stage (dY 128 columns x 32,
-//               codes 128 x 32, exponents 16 x 32), five stages deep;
-//   warp 1      tensor-memory allocation for the pair; in the leader one lane
-//               issues the MMAs; in the peer one lane relays its decoder's
-//               and splitters' arrivals to the leader, one a stage;
-//   warps 2-3   decode x^ to bf16 in shared memory, half of a stage each;
-//   warps 4-7   split dY into tensor memory (warp 4 + q: lanes 32 q ..);
-//   warps 8-15  per chunk add the accumulator (warp 8 + e: lanes 32 (e % 4)
-//               .., columns 128 (e / 4) ..) into 128 registers a thread; at
-//               the end of a unit store them: a warp writes 32 consecutive
-//               columns of one row of dW.
+// 640 threads per CTA, registers rebalanced at start (launched at 96 each):
+//   warp 0       one lane: TMA loads of a 32-token stage (dY 128 columns x 32,
+//                codes 128 x 32, exponents 16 x 32), eight stages deep;
+//   warp 1       tensor-memory allocation for the pair; in the leader one lane
+//                issues the MMAs and commits;
+//   warps 1-3 of the peer  relay: one lane each tells the leader, in turn, that
+//                the peer's operands of a stage are written;
+//   warps 4-7    split dY into tensor memory (warp 4 + q: lanes 32 q ..);
+//   warps 8-11   decode x^ to bf16 in shared memory, eight tokens each;
+//   warps 12-19  per chunk add the accumulator (warp 12 + e: lanes 32 (e % 4)
+//                .., columns 128 (e / 4) ..) into 128 registers a thread; at
+//                the end of a unit store them: a warp writes 32 consecutive
+//                columns of one row of dW.
 // Tensor memory: 256 accumulator columns, then five operand stages of 48 (three
-// parts of 32 tokens, two to a column).
+// parts of 32 tokens, two to a column).  Copies and operands are separate
+// rings, so that DRAM and L2 latency is not part of the operand loop (MMA,
+// commit, conversion, relay: ~1.5 us of the five stages' 2.0).
+//
+// What set the speed, 8192 x 8192 x 8192 (INT8): one relay lane for the peer,
+// whose release at cluster scope takes ~650 ns against 400 ns of MMAs a stage,
+// 2.69 ms; three relays and the separate rings 2.19; four decoder warps
+// instead of two, each of whose stores fills all banks, 1.89.  With operands
+// that are never rewritten the same MMAs and copies take 1.70 ms (three bf16
+// products at the burst rate of the library product: 1.72 ms; at its sustained
+// rate, which the power limit sets, 1.91).
 //
 // Few tiles and many tokens: the tokens are split over clusters into partial
 // sums, added in split order by the GEMM's reduction kernel.
@@ -66,7 +77,8 @@ struct WgradCfg {
     static constexpr int HALF = 128;          // of each, per CTA
     static constexpr int KT = 32;             // tokens a stage
     static constexpr int UK = 16;             // tokens an MMA
-    static constexpr int STAGES = 5;
+    static constexpr int RAW = 8;     // stages of copies
+    static constexpr int STAGES = 5;  // stages of MMA operands
     static constexpr int XB_BYTES = HALF * KT * 2;   // x^ in bf16: two 64-feature groups
     static constexpr int GROUP_BYTES = 64 * KT * 2;  // rows of 128 bytes, a token each
     static constexpr int Y_BYTES = HALF * KT * 4;
@@ -74,25 +86,29 @@ struct WgradCfg {
     static constexpr int S_BYTES = 16 * KT;
     // the swizzled x^ stages first: each 1024-byte aligned
     static constexpr int Y_OFF = STAGES * XB_BYTES;
-    static constexpr int C_OFF = Y_OFF + STAGES * Y_BYTES;
-    static constexpr int S_OFF = C_OFF + STAGES * C_BYTES;
-    static constexpr int BAR_OFF = S_OFF + STAGES * S_BYTES;
-    // full, empty, ready, splitters converted (peer), acc_full, acc_empty, drain
-    static constexpr int NBARS = 4 * STAGES + 3;
+    static constexpr int C_OFF = Y_OFF + RAW * Y_BYTES;
+    static constexpr int S_OFF = C_OFF + RAW * C_BYTES;
+    static constexpr int BAR_OFF = S_OFF + RAW * S_BYTES;
+    static constexpr int CONV_WARPS = 4 + 4;  // splitters, decoders
+    // full, free (per copy stage), empty, ready (per operand stage), acc_full, acc_empty, drain
+    static constexpr int NBARS = 2 * RAW + 2 * STAGES + 3;
     static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;
-    static constexpr int THREADS = 512;
+    static constexpr int THREADS = 640;
     static constexpr int TMEM_COLS = 512;
     static constexpr int OP_COL0 = TD;               // operand stage s at OP_COL0 + 48 s
     static constexpr int PART_COLS = KT / 2;
     static constexpr int OP_COLS = 3 * PART_COLS;
+    static constexpr int RELAYS = 3;
     static constexpr int EPI_WARPS = 8;
-    static constexpr int REGS_LOW = 56, REGS_HIGH = 200;
-    static constexpr int DRAIN_BATCH = 4;
+    static constexpr int REGS_LAUNCH = 96;
+    static constexpr int REGS_CONTROL = 40, REGS_SPLIT = 48, REGS_DECODE = 56, REGS_EPI = 168;
+    static constexpr int DRAIN_BATCH = 2;
     // D fp32, A and B bf16, B with its N axis contiguous, M = 256, N = 256
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
                                       (static_cast<uint32_t>(TD >> 3) << 17) |
                                       (static_cast<uint32_t>(TN >> 4) << 24);
-    static_assert(2 * 128 * REGS_LOW + 2 * 128 * REGS_HIGH == 65536, "register shares");
+    static_assert(REGS_CONTROL + REGS_SPLIT + REGS_DECODE + 2 * REGS_EPI <= 5 * REGS_LAUNCH,
+                  "register shares");
     static_assert(OP_COL0 + STAGES * OP_COLS <= TMEM_COLS, "tensor-memory columns");
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
@@ -121,9 +137,9 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-__device__ __forceinline__ void lds_u32x4(uint32_t addr, uint32_t (&v)[4]) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+__device__ __forceinline__ void lds_u32x2(uint32_t addr, uint32_t (&v)[2]) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(v[0]), "=r"(v[1])
                  : "r"(addr)
                  : "memory");
 }
@@ -148,9 +164,31 @@ __device__ __forceinline__ void drop_upper(float& a, float& b) {
         : "f"(na), "f"(nb));
 }
 
-// Four codes as two words of two bf16 values each, exact.
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Four codes as two words of two bf16 values each, exact.  INT8: the low
+// seven bits of a code below the upper byte of 128 are the bf16 number 128 +
+// low, and its sign bit alone there is 128 or 256, so their difference is the
+// code; five instructions for two codes against 7.5 through fp32.
 template <int FMT>
 __device__ __forceinline__ void decode_bf16(uint32_t w, float scale, uint32_t& lo, uint32_t& hi) {
+    if (FMT == kQ8Int8) {
+        const uint32_t s2 = upper_halves(scale, scale);
+        const uint32_t p = __byte_perm(w, 0x43434343u, 0x4140);
+        const uint32_t q = __byte_perm(w, 0x43434343u, 0x4342);
+        lo = mul_bf16x2(sub_bf16x2(p & 0xFF7FFF7Fu, p & 0xFF80FF80u), s2);
+        hi = mul_bf16x2(sub_bf16x2(q & 0xFF7FFF7Fu, q & 0xFF80FF80u), s2);
+        return;
+    }
     const float4 v = q8_decode4<FMT>(w);
     lo = upper_halves(v.x * scale, v.y * scale);
     hi = upper_halves(v.z * scale, v.w * scale);
@@ -181,11 +219,11 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_addr(smem);
-    const uint32_t full0 = sbase + C::BAR_OFF;      // own: the stage's copies
-    const uint32_t empty0 = full0 + 8 * STAGES;     // own, multicast commit
-    const uint32_t ready0 = empty0 + 8 * STAGES;    // decoder (leader: and splitters, relay)
-    const uint32_t split0 = ready0 + 8 * STAGES;    // peer: its four splitter warps
-    const uint32_t accf = split0 + 8 * STAGES;      // own, multicast commit
+    const uint32_t full0 = sbase + C::BAR_OFF;      // own: a copy stage has landed
+    const uint32_t free0 = full0 + 8 * C::RAW;      // own: its readers are done
+    const uint32_t empty0 = free0 + 8 * C::RAW;     // own, multicast commit: operands read
+    const uint32_t ready0 = empty0 + 8 * STAGES;    // operands written
+    const uint32_t accf = ready0 + 8 * STAGES;      // own, multicast commit
     const uint32_t acce = accf + 8;                 // leader: 8 warps x 2 CTAs
     const uint32_t drain = acce + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + C::NBARS * 8);
@@ -205,13 +243,14 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
         prefetch_tmap(&tmY);
         prefetch_tmap(&tmC);
         prefetch_tmap(&tmS);
+        for (int r = 0; r < C::RAW; ++r) {
+            mbar_init(full0 + 8 * r, 1);
+            mbar_init(free0 + 8 * r, C::CONV_WARPS);
+        }
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
-            // in the leader every arrival the MMA lane needs: two decoder
-            // warps, four splitter warps, the peer's relay
-            mbar_init(ready0 + 8 * s, rank == 0 ? 2 + 4 + 1 : 2);
-            mbar_init(split0 + 8 * s, 4);
+            // in the leader also the relay of the peer's
+            mbar_init(ready0 + 8 * s, C::CONV_WARPS + (rank == 0 ? 1 : 0));
         }
         mbar_init(accf, 1);
         mbar_init(acce, 2 * C::EPI_WARPS);
@@ -230,8 +269,26 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
     pdl_wait();
     pdl_trigger();
 
-    if (warp < 8) {
-        regs_dec<C::REGS_LOW>();
+    // The peer's arrivals on its ready barriers, passed on to the leader's: relay
+    // i of kRelays takes every kRelays-th stage.  A release at cluster scope
+    // takes ~650 ns on this part, more than the MMAs of a stage (400 ns), so
+    // several warps have one each in flight.
+    auto relay = [&](int i) {
+        const uint32_t ready_leader = map_to_cta(ready0, 0);
+        int total = 0;
+        for (int u = cluster; u < units; u += nclusters)
+            total += decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD).nkb;
+        for (int it = i; it < total; it += C::RELAYS) {
+            const int s = it % STAGES;
+            if (!role_wait(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault, kFaultFullBarrier,
+                           abort_flag))
+                break;
+            mbar_arrive_cluster(ready_leader + 8 * s);
+        }
+    };
+
+    if (warp < 4) {
+        regs_dec<C::REGS_CONTROL>();
         if (warp == 0) {
             if (lane == 0) {
                 // -------------------------- TMA producer (both CTAs) ------------------
@@ -244,28 +301,28 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
                     // exponents: the aligned 16 blocks that hold this CTA's four
                     const int bc = (dc / kQ8Block) & ~15;
                     for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                        const int s = it % STAGES;
-                        if (it >= STAGES &&
-                            !role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns, fault,
+                        const int r = it % C::RAW;
+                        if (it >= C::RAW &&
+                            !role_wait(free0 + 8 * r, ((it / C::RAW) & 1) ^ 1, timeout_ns, fault,
                                        kFaultEmptyBarrier, abort_flag)) {
                             ok = false;
                             break;
                         }
                         const int t0 = (w.kb_begin + kb) * C::KT;
-                        const uint32_t fb = full0 + 8 * s;
+                        const uint32_t fb = full0 + 8 * r;
                         mbar_arrive_expect_tx(fb, C::Y_BYTES + C::C_BYTES + C::S_BYTES);
-                        tma_load_2d(sbase + C::Y_OFF + s * C::Y_BYTES, &tmY, fb, nc, t0);
-                        tma_load_2d(sbase + C::C_OFF + s * C::C_BYTES, &tmC, fb, dc, t0);
-                        tma_load_2d(sbase + C::S_OFF + s * C::S_BYTES, &tmS, fb, bc, t0);
+                        tma_load_2d(sbase + C::Y_OFF + r * C::Y_BYTES, &tmY, fb, nc, t0);
+                        tma_load_2d(sbase + C::C_OFF + r * C::C_BYTES, &tmC, fb, dc, t0);
+                        tma_load_2d(sbase + C::S_OFF + r * C::S_BYTES, &tmS, fb, bc, t0);
                     }
                 }
-                // wind down: this CTA's copies have landed and its stages have
-                // been released by the MMAs
+                // wind down: this CTA's copies have landed, and the MMAs' commits
+                // have reached its operand stages
                 const long long tail = ok ? timeout_ns : timeout_ns / 8 + 1000;
-                for (int j = (it > STAGES ? it - STAGES : 0); j < it; ++j) {
-                    mbar_wait(full0 + 8 * (j % STAGES), (j / STAGES) & 1, tail, fault, kFaultDrain);
+                for (int j = (it > C::RAW ? it - C::RAW : 0); j < it; ++j)
+                    mbar_wait(full0 + 8 * (j % C::RAW), (j / C::RAW) & 1, tail, fault, kFaultDrain);
+                for (int j = (it > STAGES ? it - STAGES : 0); j < it; ++j)
                     mbar_wait(empty0 + 8 * (j % STAGES), (j / STAGES) & 1, tail, fault, kFaultDrain);
-                }
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -287,7 +344,7 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
                         const int c1 = min(w.nkb, c0 + chunk);
                         for (int kb = c0; kb < c1; ++kb, ++it) {
                             const int s = it % STAGES;
-                            if (!role_wait(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault,
+                            if (!role_wait<true>(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault,
                                            kFaultFullBarrier, abort_flag)) {
                                 ok = false;
                                 break;
@@ -316,131 +373,132 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
                 mma_commit_pair(drain);
                 mbar_wait(drain, 0, ok ? timeout_ns : timeout_ns / 8 + 1000, fault, kFaultDrain);
             } else if (lane == 0) {
-                // -------------------------- relay (peer CTA) --------------------------
-                const uint32_t ready_leader = map_to_cta(ready0, 0);
-                int it = 0;
-                bool ok = true;
-                for (int u = cluster; u < units && ok; u += nclusters) {
-                    const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
-                    for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                        const int s = it % STAGES;
-                        const uint32_t par = (it / STAGES) & 1;
-                        if (!role_wait(ready0 + 8 * s, par, timeout_ns, fault, kFaultFullBarrier,
-                                       abort_flag) ||
-                            !role_wait(split0 + 8 * s, par, timeout_ns, fault, kFaultFullBarrier,
-                                       abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_cluster(ready_leader + 8 * s);
-                    }
-                }
+                relay(0);
             }
             __syncwarp();
-        } else if (warp < 4) {
-            // ------------------------------ x^ decoders (warps 2-3, both CTAs) --------
-            // A lane takes 16 codes (features 16 c .. 16 c + 15 of a token row, c =
-            // lane % 8) and writes them as two 16-byte chunks of the row of group
-            // c / 4.  Lanes of the second group write their odd chunk first, so that
-            // the eight lanes of a store pass cover all banks.
-            const int c = lane & 7;
-            const int odd = c >> 2;
-            const int row0 = 16 * (warp - 2) + (lane >> 3);
-            int it = 0;
-            bool ok = true;
-            for (int u = cluster; u < units && ok; u += nclusters) {
-                const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
-                const int dc = w.m0 + static_cast<int>(rank) * C::HALF;
-                const uint32_t sc = static_cast<uint32_t>(((dc / kQ8Block) & 15) + (c >> 1));
-                for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    const bool got = role_wait(full0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault,
-                                               kFaultFullBarrier, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t codes = sbase + C::C_OFF + s * C::C_BYTES;
-                    const uint32_t exps = sbase + C::S_OFF + s * C::S_BYTES + sc;
-                    const uint32_t dst = sbase + s * C::XB_BYTES + odd * C::GROUP_BYTES;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t r = static_cast<uint32_t>(row0 + 4 * i);
-                        uint32_t q[4], v[8];
-                        lds_u32x4(codes + r * C::HALF + 16 * c, q);
-                        const float scale = q8_scale<FMT>(lds_u8(exps + 16 * r));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            decode_bf16<FMT>(q[j], scale, v[2 * j], v[2 * j + 1]);
-                        const uint32_t row = dst + r * 128u;
-                        const uint32_t k0 = static_cast<uint32_t>(2 * (c & 3));
-                        const uint32_t at0 = row + ((k0 ^ (r & 7u)) << 4);
-                        const uint32_t at1 = row + (((k0 + 1u) ^ (r & 7u)) << 4);
-                        if (odd) {
-                            sts_u32x4(at1, v[4], v[5], v[6], v[7]);
-                            sts_u32x4(at0, v[0], v[1], v[2], v[3]);
-                        } else {
-                            sts_u32x4(at0, v[0], v[1], v[2], v[3]);
-                            sts_u32x4(at1, v[4], v[5], v[6], v[7]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ready0 + 8 * s);
-                }
-            }
-            __syncwarp();
-        } else {
-            // ------------------------------ dY splitters (warps 4-7, both CTAs) -------
-            const int q = warp & 3;
-            const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-            int it = 0;
-            bool ok = true;
-            for (int u = cluster; u < units && ok; u += nclusters) {
-                const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
-                for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    const bool got = role_wait(full0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault,
-                                               kFaultFullBarrier, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t src = sbase + C::Y_OFF + s * C::Y_BYTES +
-                                         static_cast<uint32_t>(4 * (32 * q + lane));
-                    const uint32_t col =
-                        lane_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
-                    // 16 tokens at a time: this warpgroup runs on 56 registers
-#pragma unroll
-                    for (int h = 0; h < C::KT / 16; ++h) {
-                        float y[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            y[i] = lds_f32(src + static_cast<uint32_t>(16 * h + i) * (4 * C::HALF));
-#pragma unroll
-                        for (int part = 0; part < 3; ++part) {
-                            uint32_t p[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                p[i] = upper_halves(y[2 * i], y[2 * i + 1]);
-                                if (part < 2) drop_upper(y[2 * i], y[2 * i + 1]);
-                            }
-                            tmem_st_32x32b_x8(col + static_cast<uint32_t>(part * C::PART_COLS + 8 * h),
-                                              p);
-                        }
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive((rank == 0 ? ready0 : split0) + 8 * s);
-                }
-            }
-            __syncwarp();
+        } else if (rank == 1 && lane == 0) {
+            // ------------------------------ relays (warps 2-3 of the peer) ------------
+            relay(warp - 1);
         }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------ dY splitters (warps 4-7, both CTAs) -----------
+        regs_dec<C::REGS_SPLIT>();
+        const int q = warp & 3;
+        const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+        int it = 0;
+        bool ok = true;
+        for (int u = cluster; u < units && ok; u += nclusters) {
+            const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+            for (int kb = 0; kb < w.nkb; ++kb, ++it) {
+                const int s = it % STAGES, raw = it % C::RAW;
+                bool got = role_wait(full0 + 8 * raw, (it / C::RAW) & 1, timeout_ns, fault,
+                                     kFaultFullBarrier, abort_flag);
+                if (got && it >= STAGES)
+                    got = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns, fault,
+                                    kFaultEmptyBarrier, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                // the MMAs that read this stage before are done
+                tc_fence_after();
+                const uint32_t src = sbase + C::Y_OFF + raw * C::Y_BYTES +
+                                     static_cast<uint32_t>(4 * (32 * q + lane));
+                const uint32_t col =
+                    lane_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
+                // 16 tokens at a time: this warpgroup runs on 56 registers
+#pragma unroll
+                for (int h = 0; h < C::KT / 16; ++h) {
+                    float y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        y[i] = lds_f32(src + static_cast<uint32_t>(16 * h + i) * (4 * C::HALF));
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        uint32_t p[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            p[i] = upper_halves(y[2 * i], y[2 * i + 1]);
+                            if (part < 2) drop_upper(y[2 * i], y[2 * i + 1]);
+                        }
+                        tmem_st_32x32b_x8(col + static_cast<uint32_t>(part * C::PART_COLS + 8 * h),
+                                          p);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(ready0 + 8 * s);
+                    mbar_arrive(free0 + 8 * raw);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < 12) {
+        // ------------------------------ x^ decoders (warps 8-11, both CTAs) -----------
+        // A lane takes eight codes of a token row: with 16 lanes a row, loads are
+        // 128 contiguous bytes, and each eight lanes store the eight 16-byte
+        // chunks of one row of one 64-feature group.
+        regs_dec<C::REGS_DECODE>();
+        const int c = lane & 15;
+        const int row0 = 8 * (warp - 8) + (lane >> 4);
+        int it = 0;
+        bool ok = true;
+        for (int u = cluster; u < units && ok; u += nclusters) {
+            const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+            const int dc = w.m0 + static_cast<int>(rank) * C::HALF;
+            const uint32_t sc = static_cast<uint32_t>(((dc / kQ8Block) & 15) + (c >> 2));
+            for (int kb = 0; kb < w.nkb; ++kb, ++it) {
+                const int s = it % STAGES, raw = it % C::RAW;
+                const bool got = role_wait(full0 + 8 * raw, (it / C::RAW) & 1, timeout_ns, fault,
+                                           kFaultFullBarrier, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t codes = sbase + C::C_OFF + raw * C::C_BYTES + 8 * c;
+                const uint32_t exps = sbase + C::S_OFF + raw * C::S_BYTES + sc;
+                const uint32_t dst = sbase + s * C::XB_BYTES + (c >> 3) * C::GROUP_BYTES;
+                uint32_t q[4][2], ex[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t r = static_cast<uint32_t>(row0 + 2 * i);
+                    lds_u32x2(codes + r * C::HALF, q[i]);
+                    ex[i] = lds_u8(exps + 16u * r);
+                }
+                if (it >= STAGES) {
+                    const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns,
+                                               fault, kFaultEmptyBarrier, abort_flag);
+                    if (!__all_sync(0xffffffffu, can)) {
+                        ok = false;
+                        break;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t r = static_cast<uint32_t>(row0 + 2 * i);
+                    uint32_t v[4];
+                    const float scale = q8_scale<FMT>(ex[i]);
+                    decode_bf16<FMT>(q[i][0], scale, v[0], v[1]);
+                    decode_bf16<FMT>(q[i][1], scale, v[2], v[3]);
+                    const uint32_t chunk = static_cast<uint32_t>(c & 7) ^ (r & 7u);
+                    sts_u32x4(dst + r * 128u + (chunk << 4), v[0], v[1], v[2], v[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(ready0 + 8 * s);
+                    mbar_arrive(free0 + 8 * raw);
+                }
+            }
+        }
+        __syncwarp();
     } else {
-        // ------------------------------ epilogue (warps 8-15, both CTAs) --------------
-        regs_inc<C::REGS_HIGH>();
-        const int e = warp - 8;
+        // ------------------------------ epilogue (warps 12-19, both CTAs) -------------
+        regs_inc<C::REGS_EPI>();
+        const int e = warp - 12;
         const int q = warp & 3;                  // lanes 32 q .. 32 q + 31
         const int col0 = (e >> 2) * EPI_COLS;    // accumulator columns: features
         const int nl = static_cast<int>(rank) * C::HALF + 32 * q + lane;
@@ -522,7 +580,7 @@ cudaError_t configure(int dev) {
     cudaFuncAttributes attr;
     cudaError_t e = cudaFuncGetAttributes(&attr, q8_wgrad_pair_kernel<FMT>);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs * WgradCfg::THREADS < 65536) return cudaErrorInvalidConfiguration;
+    if (attr.numRegs < WgradCfg::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(q8_wgrad_pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              WgradCfg::SMEM_BYTES);
     if (e == cudaSuccess) done[dev] = true;
