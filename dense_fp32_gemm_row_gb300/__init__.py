@@ -106,6 +106,8 @@ def library_path() -> str:
 def load():
     """Load libgemmf32.so (built in-tree); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -58,27 +58,27 @@ class Q8Struct(ctypes.Structure):
 
 
 def gemm_f32_q8_store(X, ldx, q, stream=0) -> int:
-    return _g.load().gemm_f32_q8_store(_g._p(X), ldx, q, _g._p(stream))
+    return _g.load().gemm_f32_q8_store(X or None, ldx, q, stream or None)
 
 
 def gemm_f32_q8_restore(q, X, ldx, type=Q8_TO_F32, stream=0) -> int:
-    return _g.load().gemm_f32_q8_restore(q, _g._p(X), ldx, type, _g._p(stream))
+    return _g.load().gemm_f32_q8_restore(q, X or None, ldx, type, stream or None)
 
 
 def gemm_f32_q8_wgrad(x, dY, lddy, N, alpha, beta, dW, lddw, algo=0, splits=0, stream=0) -> int:
-    return _g.load().gemm_f32_q8_wgrad(x, _g._p(dY), lddy, N, alpha, beta, _g._p(dW), lddw, algo,
-                                       splits, _g._p(stream))
+    return _g.load().gemm_f32_q8_wgrad(x, dY or None, lddy, N, alpha, beta, dW or None, lddw, algo,
+                                       splits, stream or None)
 
 
 def gemm_f32_q8_gated(act, G, ldg, U, ldu, H, ldh, gq, uq, stream=0) -> int:
-    return _g.load().gemm_f32_q8_gated(act, _g._p(G), ldg, _g._p(U), ldu, _g._p(H), ldh, gq, uq,
-                                       _g._p(stream))
+    return _g.load().gemm_f32_q8_gated(act, G or None, ldg, U or None, ldu, H or None, ldh, gq, uq,
+                                       stream or None)
 
 
 def gemm_f32_q8_gated_backward(act, gq, uq, dH, lddh, dG, lddg, dU, lddu, hq=None,
                                stream=0) -> int:
-    return _g.load().gemm_f32_q8_gated_backward(act, gq, uq, _g._p(dH), lddh, _g._p(dG), lddg,
-                                                _g._p(dU), lddu, hq, _g._p(stream))
+    return _g.load().gemm_f32_q8_gated_backward(act, gq, uq, dH or None, lddh, dG or None, lddg,
+                                                dU or None, lddu, hq, stream or None)
 
 
 def _declare(lib) -> None:
@@ -94,12 +94,31 @@ def _declare(lib) -> None:
 
 
 # ---- tensors ---------------------------------------------------------------------------------
+#
+# A small call takes the GPU a few microseconds, so what the binding spends on the host is most
+# of it: a call looks at each tensor once, makes one allocation for each result, and takes the
+# slower ways (another stream, another device) only where they are needed.
+
+_torch = None  # set on first use: importing the package does not import torch
+_stream_of = None
+_one_device = True
+
+
+def _load_torch():
+    global _torch, _stream_of, _one_device
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _stream_of = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _one_device = torch.cuda.device_count() <= 1
+    _torch = torch
+    return torch
 
 
 def _name(table, value, what):
     try:
         return table[value]
-    except KeyError:
+    except (KeyError, TypeError):
         raise ValueError(f"{what} is one of {', '.join(table)}, not {value!r}") from None
 
 
@@ -111,170 +130,192 @@ class Q8:
     that are multiples of 16.  ``format`` is "int8" or "e4m3".
     """
 
-    __slots__ = ("codes", "scales", "rows", "cols", "format", "struct")
+    __slots__ = ("_codes", "_scales", "_buffer", "device", "rows", "cols", "format", "struct")
 
     def __init__(self, codes, scales, cols, format="int8"):
-        import torch
-
+        torch = _torch or _load_torch()
         fmt = _name(Q8_FORMATS, format, "format")
         rows, cols = codes.shape[0], int(cols)
-        blocks = (cols + Q8_BLOCK - 1) // Q8_BLOCK
-        for t, width in ((codes, cols), (scales, blocks)):
-            if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_cuda:
-                raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
-            if t.shape[0] != rows or t.shape[1] < width:
-                raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
-        if codes.device != scales.device:
+        if cols < 0:
+            raise ValueError("cols must not be negative")
+        self.struct = Q8Struct(codes.data_ptr(), scales.data_ptr(),
+                               _bytes_ld(torch, codes, rows, cols),
+                               _bytes_ld(torch, scales, rows, (cols + 31) >> 5), rows, cols, fmt)
+        self.device = codes.get_device()
+        if scales.get_device() != self.device:
             raise ValueError("codes and scales must be on one device")
-        ldc, lds = _bytes_ld(codes), _bytes_ld(scales)
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales, self._buffer = codes, scales, None
         self.rows, self.cols, self.format = rows, cols, format
-        self.struct = Q8Struct(codes.data_ptr(), scales.data_ptr(), ldc, lds, rows, cols, fmt)
+
+    @property
+    def codes(self):
+        """The code bytes, (rows, cols rounded up to 16) for a checkpoint made here."""
+        if self._codes is None:
+            ld = self.struct.ldcodes
+            self._codes = self._buffer[:self.rows * ld].view(self.rows, ld)
+        return self._codes
+
+    @property
+    def scales(self):
+        """The exponent bytes, one for each block of 32 columns."""
+        if self._scales is None:
+            s = self.struct
+            self._scales = self._buffer[self.rows * s.ldcodes:].view(self.rows, s.ldscales)
+        return self._scales
 
     @property
     def nbytes(self) -> int:
         """Bytes that the two tensors hold."""
         return self.codes.numel() + self.scales.numel()
 
+    def record_stream(self, stream) -> None:
+        """As ``torch.Tensor.record_stream`` of the tensors behind it."""
+        for t in (self._buffer,) if self._buffer is not None else (self._codes, self._scales):
+            t.record_stream(stream)
+
     def __repr__(self):
         return f"Q8({self.rows} x {self.cols}, {self.format})"
 
 
-def _bytes_ld(t) -> int:
-    rows, width = t.shape
-    if rows and width and (t.stride(1) != 1 or t.data_ptr() & 15):
+def _bytes_ld(torch, t, rows, width) -> int:
+    """The row stride of one of a checkpoint's byte tensors, which must hold rows x width."""
+    if t.dtype is not torch.uint8 or not t.is_cuda or t.dim() != 2:
+        raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
+    r, w = t.shape
+    if r != rows or w < width:
+        raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
+    s0, s1 = t.stride()
+    if rows and width and (s1 != 1 or t.data_ptr() & 15):
         raise ValueError("codes and scales must have contiguous rows and 16-byte aligned bases")
-    ld = t.stride(0) if rows > 1 else (width + 15) // 16 * 16
+    ld = s0 if rows > 1 else (w + 15) & ~15
     if ld & 15 or ld < width:
         raise ValueError("row strides of codes and scales must be multiples of 16")
     return ld
 
 
-def _ld(t, what) -> int:
-    """The row stride of a float32 CUDA matrix with contiguous rows."""
-    import torch
+def _make(like, rows, cols, format, fmt) -> Q8:
+    """An uninitialised checkpoint on the device of ``like``: codes, then exponents, in one buffer."""
+    q = Q8.__new__(Q8)
+    ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
+    buf = like.new_empty(rows * (ldc + lds), dtype=_torch.uint8)
+    base = buf.data_ptr()
+    q.struct = Q8Struct(base, base + rows * ldc, ldc, lds, rows, cols, fmt)
+    q._codes = q._scales = None
+    q._buffer = buf
+    q.device = like.get_device()
+    q.rows, q.cols, q.format = rows, cols, format
+    return q
 
-    if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2:
+
+def _matrix(t, what):
+    """(rows, cols, row stride) of a float32 CUDA matrix with contiguous rows."""
+    if t.dtype is not _torch.float32 or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{what} must be a 2-D float32 CUDA tensor")
-    return _row_stride(t, what)
+    return _strides(t, what)
 
 
-def _row_stride(t, what) -> int:
+def _strides(t, what):
     rows, cols = t.shape
-    if cols > 1 and rows and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1 and rows:
         raise ValueError(f"{what} must have contiguous rows")
     if rows <= 1:
-        return max(cols, 1)
-    ld = t.stride(0)
-    if ld < cols:
+        return rows, cols, cols or 1
+    if s0 < cols or s0 < 1:
         raise ValueError(f"{what} must have rows that do not overlap")
+    return rows, cols, s0
+
+
+def _like(t, rows, cols, device, what):
+    """The row stride of a given float32 operand, which must be rows x cols on ``device``."""
+    r, c, ld = _matrix(t, what)
+    if r != rows or c != cols:
+        raise ValueError(f"{what} must be {rows} x {cols}, not {r} x {c}")
+    if t.get_device() != device:
+        raise ValueError("all tensors must be on one device")
     return ld
 
 
-def _shape(t, shape, what) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must be {shape}, not {tuple(t.shape)}")
+def _given(q, rows, cols, format, device, what) -> Q8:
+    """A checkpoint given for a result, or for an operand of this shape."""
+    if q.rows != rows or q.cols != cols:
+        raise ValueError(f"{what} must hold {rows} x {cols}, not {q.rows} x {q.cols}")
+    if q.format != format:
+        raise ValueError(f"{what} must be in {format}, not {q.format}")
+    if q.device != device:
+        raise ValueError("all tensors must be on one device")
+    return q
 
 
-class _Call:
-    """The device and stream of one call: allocations inside the block belong to the stream."""
-
-    __slots__ = ("device", "stream", "current", "guard", "other")
-
-    def __init__(self, device, stream):
-        import torch
-
-        self.device = device
-        self.current = torch.cuda.current_stream(device)
-        self.other = stream is not None and stream != self.current
-        self.stream = stream if self.other else self.current
-        self.guard = None
-
-    def __enter__(self):
-        import torch
-
-        if self.other:
-            self.guard = torch.cuda.stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
-
-    def uses(self, *tensors) -> None:
-        """Tensors made on the current stream that this call reads or writes on another."""
-        if self.other:
-            for t in tensors:
-                if isinstance(t, Q8):
-                    t.codes.record_stream(self.stream)
-                    t.scales.record_stream(self.stream)
-                elif t is not None:
-                    t.record_stream(self.stream)
+def _elsewhere(call, device, stream, tensors):
+    """``call()`` on ``device`` and ``stream``, whose results then belong to that stream, with the
+    tensors it reads or writes kept from reuse until it has run.  None: nothing to switch."""
+    torch = _torch
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        with torch.cuda.stream(stream):
+            result = call()
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return result
+    with torch.cuda.device(device):
+        return call()
 
 
-def _same_device(device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and (t.codes if isinstance(t, Q8) else t).device != device:
-            raise ValueError("all tensors must be on one device")
+def _away(device) -> bool:
+    return not _one_device and device >= 0 and device != _torch.cuda.current_device()
 
 
 def q8_empty(rows, cols, format="int8", device="cuda") -> Q8:
     """An uninitialised checkpoint of a rows x cols matrix."""
-    import torch
-
-    blocks = (cols + Q8_BLOCK - 1) // Q8_BLOCK
-    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    scales = torch.empty((rows, (blocks + 15) // 16 * 16), dtype=torch.uint8, device=device)
-    return Q8(codes, scales, cols, format)
-
-
-def _out_q8(q, rows, cols, format, device, what) -> Q8:
-    if q is None:
-        return q8_empty(rows, cols, format, device)
-    if (q.rows, q.cols) != (rows, cols):
-        raise ValueError(f"{what} must hold {rows} x {cols}, not {q.rows} x {q.cols}")
-    if q.format != format:
-        raise ValueError(f"{what} must be in {format}, not {q.format}")
-    return q
+    torch = _torch or _load_torch()
+    fmt = _name(Q8_FORMATS, format, "format")
+    return _make(torch.empty(0, dtype=torch.uint8, device=device), rows, cols, format, fmt)
 
 
 def q8_store(x, format="int8", out=None, stream=None) -> Q8:
     """The 8-bit checkpoint of ``x`` (rows, cols), in ``out`` if given."""
-    ld = _ld(x, "x")
-    _name(Q8_FORMATS, format, "format")
-    _same_device(x.device, out)
-    with _Call(x.device, stream) as c:
-        q = _out_q8(out, x.shape[0], x.shape[1], format, x.device, "out")
-        st = gemm_f32_q8_store(x.data_ptr(), ld, q.struct, c.stream.cuda_stream)
-        c.uses(x, out)
-    _g.check(st, "q8_store")
+    if _torch is None:
+        _load_torch()
+    rows, cols, ld = _matrix(x, "x")
+    fmt = _name(Q8_FORMATS, format, "format")
+    device = x.get_device()
+    if stream is not None or _away(device):
+        return _elsewhere(lambda: q8_store(x, format, out), device, stream, (x, out))
+    q = _make(x, rows, cols, format, fmt) if out is None else _given(out, rows, cols, format,
+                                                                     device, "out")
+    st = gemm_f32_q8_store(x.data_ptr(), ld, q.struct, _stream_of(device))
+    if st:
+        _g.check(st, "q8_store")
     return q
 
 
 def q8_restore(q, out=None, dtype=None, stream=None):
     """The values ``q`` stands for, as float32 or (``dtype=torch.bfloat16``) bfloat16, both exact."""
-    import torch
-
-    dtype = dtype or (out.dtype if out is not None else torch.float32)
-    if dtype not in (torch.float32, torch.bfloat16):
+    torch = _torch or _load_torch()
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError("dtype is torch.float32 or torch.bfloat16")
-    device = q.codes.device
-    _same_device(device, out)
-    with _Call(device, stream) as c:
-        x = torch.empty((q.rows, q.cols), dtype=dtype, device=device) if out is None else out
-        if x.dtype != dtype or x.dim() != 2:
-            raise ValueError(f"out must be a 2-D {dtype} tensor")
-        _shape(x, (q.rows, q.cols), "out")
-        st = gemm_f32_q8_restore(q.struct, x.data_ptr(), _row_stride(x, "out"),
-                                 Q8_TO_F32 if dtype == torch.float32 else Q8_TO_BF16,
-                                 c.stream.cuda_stream)
-        c.uses(q, out)
-    _g.check(st, "q8_restore")
+    device = q.device
+    if stream is not None or _away(device):
+        return _elsewhere(lambda: q8_restore(q, out, dtype), device, stream, (q, out))
+    if out is None:
+        rows, cols = q.rows, q.cols
+        x = (q._codes if q._buffer is None else q._buffer).new_empty((rows, cols), dtype=dtype)
+        ld = cols or 1
+    else:
+        x = out
+        if x.dtype is not dtype or x.dim() != 2 or x.get_device() != device:
+            raise ValueError(f"out must be a 2-D {dtype} tensor on the checkpoint's device")
+        rows, cols, ld = _strides(x, "out")
+        if rows != q.rows or cols != q.cols:
+            raise ValueError(f"out must be {q.rows} x {q.cols}, not {rows} x {cols}")
+    st = gemm_f32_q8_restore(q.struct, x.data_ptr(), ld,
+                             Q8_TO_F32 if dtype is torch.float32 else Q8_TO_BF16,
+                             _stream_of(device))
+    if st:
+        _g.check(st, "q8_restore")
     return x
 
 
@@ -286,45 +327,55 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     is "auto", "ffma" or "3xbf16" (the tensor-core kernel), ``splits`` the
     number of ranges the latter splits the tokens into (0: chosen by size).
     """
-    import torch
-
-    ldy = _ld(dy, "dy")
+    if _torch is None:
+        _load_torch()
+    rows, N, ldy = _matrix(dy, "dy")
+    if rows != q.rows:
+        raise ValueError(f"dy must have {q.rows} rows, not {rows}")
     code = _name(Q8_ALGOS, algo, "algo")
-    N = dy.shape[1]
-    _shape(dy, (q.rows, N), "dy")
-    _same_device(q.codes.device, dy, out)
-    if out is None and beta != 0.0:
-        raise ValueError("beta needs out, the gradient to add to")
-    with _Call(dy.device, stream) as c:
-        dw = torch.empty((q.cols, N), dtype=torch.float32, device=dy.device) if out is None else out
-        _shape(dw, (q.cols, N), "out")
-        st = gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(),
-                               _ld(dw, "out"), code, splits, c.stream.cuda_stream)
-        c.uses(q, dy, out)
-    _g.check(st, "q8_wgrad")
+    device = q.device
+    if dy.get_device() != device:
+        raise ValueError("all tensors must be on one device")
+    if stream is not None or _away(device):
+        return _elsewhere(lambda: q8_wgrad(q, dy, out, alpha, beta, algo, splits), device, stream,
+                          (q, dy, out))
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta needs out, the gradient to add to")
+        dw, ldw = dy.new_empty((q.cols, N)), N or 1
+    else:
+        dw, ldw = out, _like(out, q.cols, N, device, "out")
+    st = gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(), ldw, code,
+                           splits, _stream_of(device))
+    if st:
+        _g.check(st, "q8_wgrad")
     return dw
 
 
 def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=None, stream=None):
     """``h = act(gate) * up`` and the checkpoints of gate and up: ``(h, gate_q, up_q)``."""
-    import torch
-
-    ldg, ldu = _ld(gate, "gate"), _ld(up, "up")
+    if _torch is None:
+        _load_torch()
+    rows, cols, ldg = _matrix(gate, "gate")
     code = _name(ACTS, act, "act")
-    _name(Q8_FORMATS, format, "format")
-    rows, cols = gate.shape
-    _shape(up, (rows, cols), "up")
-    device = gate.device
-    _same_device(device, up, out, gate_q, up_q)
-    with _Call(device, stream) as c:
-        h = torch.empty((rows, cols), dtype=torch.float32, device=device) if out is None else out
-        _shape(h, (rows, cols), "out")
-        gq = _out_q8(gate_q, rows, cols, format, device, "gate_q")
-        uq = _out_q8(up_q, rows, cols, format, device, "up_q")
-        st = gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(),
-                               _ld(h, "out"), gq.struct, uq.struct, c.stream.cuda_stream)
-        c.uses(gate, up, out, gate_q, up_q)
-    _g.check(st, "q8_gated")
+    fmt = _name(Q8_FORMATS, format, "format")
+    device = gate.get_device()
+    ldu = _like(up, rows, cols, device, "up")
+    if stream is not None or _away(device):
+        return _elsewhere(lambda: q8_gated(gate, up, act, format, out, gate_q, up_q), device,
+                          stream, (gate, up, out, gate_q, up_q))
+    if out is None:
+        h, ldh = gate.new_empty((rows, cols)), cols or 1
+    else:
+        h, ldh = out, _like(out, rows, cols, device, "out")
+    gq = _make(gate, rows, cols, format, fmt) if gate_q is None else _given(
+        gate_q, rows, cols, format, device, "gate_q")
+    uq = _make(gate, rows, cols, format, fmt) if up_q is None else _given(
+        up_q, rows, cols, format, device, "up_q")
+    st = gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(), ldh,
+                           gq.struct, uq.struct, _stream_of(device))
+    if st:
+        _g.check(st, "q8_gated")
     return h, gq, uq
 
 
@@ -337,28 +388,32 @@ def q8_gated_backward(gate_q, up_q, dh, act="silu", dgate=None, dup=None, h_q=No
     false.  ``dgate`` and ``dup`` may be given, for instance as the halves of
     one buffer.
     """
-    import torch
-
-    ldh = _ld(dh, "dh")
+    if _torch is None:
+        _load_torch()
+    rows, cols, format, device = gate_q.rows, gate_q.cols, gate_q.format, gate_q.device
     code = _name(ACTS, act, "act")
-    rows, cols = gate_q.rows, gate_q.cols
-    _shape(dh, (rows, cols), "dh")
-    if (up_q.rows, up_q.cols, up_q.format) != (rows, cols, gate_q.format):
-        raise ValueError("gate_q and up_q must have one shape and one format")
+    _given(up_q, rows, cols, format, device, "up_q")
+    ldh = _like(dh, rows, cols, device, "dh")
     if h_q is not None and not want_h:
         raise ValueError("h_q given, and want_h false")
-    device = dh.device
-    _same_device(device, gate_q, up_q, dgate, dup, h_q)
-    with _Call(device, stream) as c:
-        dg = torch.empty((rows, cols), dtype=torch.float32, device=device) if dgate is None else dgate
-        du = torch.empty((rows, cols), dtype=torch.float32, device=device) if dup is None else dup
-        _shape(dg, (rows, cols), "dgate")
-        _shape(du, (rows, cols), "dup")
-        hq = _out_q8(h_q, rows, cols, gate_q.format, device, "h_q") if want_h else None
-        st = gemm_f32_q8_gated_backward(code, gate_q.struct, up_q.struct, dh.data_ptr(), ldh,
-                                        dg.data_ptr(), _ld(dg, "dgate"), du.data_ptr(),
-                                        _ld(du, "dup"), hq.struct if want_h else None,
-                                        c.stream.cuda_stream)
-        c.uses(gate_q, up_q, dh, dgate, dup, h_q)
-    _g.check(st, "q8_gated_backward")
-    return dg, du, hq
+    if stream is not None or _away(device):
+        return _elsewhere(lambda: q8_gated_backward(gate_q, up_q, dh, act, dgate, dup, h_q, want_h),
+                          device, stream, (gate_q, up_q, dh, dgate, dup, h_q))
+    if dgate is None:
+        dg, ldg = dh.new_empty((rows, cols)), cols or 1
+    else:
+        dg, ldg = dgate, _like(dgate, rows, cols, device, "dgate")
+    if dup is None:
+        du, ldu = dh.new_empty((rows, cols)), cols or 1
+    else:
+        du, ldu = dup, _like(dup, rows, cols, device, "dup")
+    if h_q is not None:
+        _given(h_q, rows, cols, format, device, "h_q")
+    elif want_h:
+        h_q = _make(dh, rows, cols, format, gate_q.struct.format)
+    st = gemm_f32_q8_gated_backward(code, gate_q.struct, up_q.struct, dh.data_ptr(), ldh,
+                                    dg.data_ptr(), ldg, du.data_ptr(), ldu,
+                                    None if h_q is None else h_q.struct, _stream_of(device))
+    if st:
+        _g.check(st, "q8_gated_backward")
+    return dg, du, h_q
