@@ -66,18 +66,26 @@ __device__ __forceinline__ float q8_scale(unsigned e) {
 
 // Codes of four values (inv = q8_inverse_scale(e)), value 0 in the low byte.
 // INT8: adding 1.5 * 2^23 leaves the integer nearest to the value (ties to
-// even) in the low bits of the sum; the clamp matters only where E is held
-// at 254.
+// even) in the low bits of the sum, and as the product with a power of two
+// is exact one fused multiply-add rounds alike.  Only where E is held at 254
+// can a value round to 128, and be clamped.
 template <int FMT>
 __device__ __forceinline__ unsigned q8_encode4(float a, float b, float c, float d, float inv,
                                                unsigned e) {
     unsigned w;
     if (FMT == kQ8Int8) {
         const float magic = 12582912.0f;
-        const unsigned qa = __float_as_uint(fminf(fmaxf(a * inv, -127.0f), 127.0f) + magic);
-        const unsigned qb = __float_as_uint(fminf(fmaxf(b * inv, -127.0f), 127.0f) + magic);
-        const unsigned qc = __float_as_uint(fminf(fmaxf(c * inv, -127.0f), 127.0f) + magic);
-        const unsigned qd = __float_as_uint(fminf(fmaxf(d * inv, -127.0f), 127.0f) + magic);
+        if (e >= 254u) {
+            const float top = 127.0f * __uint_as_float((e - 6u) << 23);  // 127 * 2^121
+            a = fminf(fmaxf(a, -top), top);
+            b = fminf(fmaxf(b, -top), top);
+            c = fminf(fmaxf(c, -top), top);
+            d = fminf(fmaxf(d, -top), top);
+        }
+        const unsigned qa = __float_as_uint(fmaf(a, inv, magic));
+        const unsigned qb = __float_as_uint(fmaf(b, inv, magic));
+        const unsigned qc = __float_as_uint(fmaf(c, inv, magic));
+        const unsigned qd = __float_as_uint(fmaf(d, inv, magic));
         w = __byte_perm(__byte_perm(qa, qb, 0x0040), __byte_perm(qc, qd, 0x0040), 0x5410);
     } else {
         unsigned short lo, hi;

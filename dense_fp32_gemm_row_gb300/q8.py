@@ -193,18 +193,23 @@ def _bytes_ld(torch, t, rows, width) -> int:
     return ld
 
 
-def _make(like, rows, cols, format, fmt) -> Q8:
-    """An uninitialised checkpoint on the device of ``like``: codes, then exponents, in one buffer."""
+def _make(device, rows, cols, format, fmt) -> Q8:
+    """An uninitialised checkpoint on a device: codes, then exponents, in one buffer."""
     q = Q8.__new__(Q8)
     ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
-    buf = like.new_empty(rows * (ldc + lds), dtype=_torch.uint8)
+    q._buffer = buf = _torch.empty(rows * (ldc + lds), dtype=_torch.uint8, device=device)
     base = buf.data_ptr()
     q.struct = Q8Struct(base, base + rows * ldc, ldc, lds, rows, cols, fmt)
     q._codes = q._scales = None
-    q._buffer = buf
-    q.device = like.get_device()
-    q.rows, q.cols, q.format = rows, cols, format
+    q.device = device
+    q.rows = rows
+    q.cols = cols
+    q.format = format
     return q
+
+
+def _floats(rows, cols, device):
+    return _torch.empty((rows, cols), dtype=_torch.float32, device=device)
 
 
 def _matrix(t, what):
@@ -270,7 +275,11 @@ def q8_empty(rows, cols, format="int8", device="cuda") -> Q8:
     """An uninitialised checkpoint of a rows x cols matrix."""
     torch = _torch or _load_torch()
     fmt = _name(Q8_FORMATS, format, "format")
-    return _make(torch.empty(0, dtype=torch.uint8, device=device), rows, cols, format, fmt)
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("a checkpoint is made on a CUDA device")
+    return _make(torch.cuda.current_device() if device.index is None else device.index, rows, cols,
+                 format, fmt)
 
 
 def q8_store(x, format="int8", out=None, stream=None) -> Q8:
@@ -282,7 +291,7 @@ def q8_store(x, format="int8", out=None, stream=None) -> Q8:
     device = x.get_device()
     if stream is not None or _away(device):
         return _elsewhere(lambda: q8_store(x, format, out), device, stream, (x, out))
-    q = _make(x, rows, cols, format, fmt) if out is None else _given(out, rows, cols, format,
+    q = _make(device, rows, cols, format, fmt) if out is None else _given(out, rows, cols, format,
                                                                      device, "out")
     st = gemm_f32_q8_store(x.data_ptr(), ld, q.struct, _stream_of(device))
     if st:
@@ -302,7 +311,7 @@ def q8_restore(q, out=None, dtype=None, stream=None):
         return _elsewhere(lambda: q8_restore(q, out, dtype), device, stream, (q, out))
     if out is None:
         rows, cols = q.rows, q.cols
-        x = (q._codes if q._buffer is None else q._buffer).new_empty((rows, cols), dtype=dtype)
+        x = torch.empty((rows, cols), dtype=dtype, device=device)
         ld = cols or 1
     else:
         x = out
@@ -342,7 +351,7 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs out, the gradient to add to")
-        dw, ldw = dy.new_empty((q.cols, N)), N or 1
+        dw, ldw = _floats(q.cols, N, device), N or 1
     else:
         dw, ldw = out, _like(out, q.cols, N, device, "out")
     st = gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(), ldw, code,
@@ -365,12 +374,12 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
         return _elsewhere(lambda: q8_gated(gate, up, act, format, out, gate_q, up_q), device,
                           stream, (gate, up, out, gate_q, up_q))
     if out is None:
-        h, ldh = gate.new_empty((rows, cols)), cols or 1
+        h, ldh = _floats(rows, cols, device), cols or 1
     else:
         h, ldh = out, _like(out, rows, cols, device, "out")
-    gq = _make(gate, rows, cols, format, fmt) if gate_q is None else _given(
+    gq = _make(device, rows, cols, format, fmt) if gate_q is None else _given(
         gate_q, rows, cols, format, device, "gate_q")
-    uq = _make(gate, rows, cols, format, fmt) if up_q is None else _given(
+    uq = _make(device, rows, cols, format, fmt) if up_q is None else _given(
         up_q, rows, cols, format, device, "up_q")
     st = gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(), ldh,
                            gq.struct, uq.struct, _stream_of(device))
@@ -400,17 +409,17 @@ def q8_gated_backward(gate_q, up_q, dh, act="silu", dgate=None, dup=None, h_q=No
         return _elsewhere(lambda: q8_gated_backward(gate_q, up_q, dh, act, dgate, dup, h_q, want_h),
                           device, stream, (gate_q, up_q, dh, dgate, dup, h_q))
     if dgate is None:
-        dg, ldg = dh.new_empty((rows, cols)), cols or 1
+        dg, ldg = _floats(rows, cols, device), cols or 1
     else:
         dg, ldg = dgate, _like(dgate, rows, cols, device, "dgate")
     if dup is None:
-        du, ldu = dh.new_empty((rows, cols)), cols or 1
+        du, ldu = _floats(rows, cols, device), cols or 1
     else:
         du, ldu = dup, _like(dup, rows, cols, device, "dup")
     if h_q is not None:
         _given(h_q, rows, cols, format, device, "h_q")
     elif want_h:
-        h_q = _make(dh, rows, cols, format, gate_q.struct.format)
+        h_q = _make(device, rows, cols, format, gate_q.struct.format)
     st = gemm_f32_q8_gated_backward(code, gate_q.struct, up_q.struct, dh.data_ptr(), ldh,
                                     dg.data_ptr(), ldg, du.data_ptr(), ldu,
                                     None if h_q is None else h_q.struct, _stream_of(device))
