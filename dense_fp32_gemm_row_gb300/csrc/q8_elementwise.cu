@@ -38,13 +38,35 @@ constexpr int kThreads = 256;
 constexpr int kActSilu = 0;
 constexpr int kActGelu = 1;
 
-// act(z) and act'(z) in fp32.  erfc keeps P's relative accuracy in the
-// lower tail, where 1 + erf cancels.
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if (ACT == kActSilu) return z * (1.0f / (1.0f + expf(-z)));
-    return z * (0.5f * erfcf(-0.70710678118654752f * z));
+// The normal distribution function below zero, P(-a) = e^(-a^2/2) F(a), with
+// F(a) = erfc(a / sqrt 2) e^(a^2/2) / 2 as a polynomial in t = 1 / (1 + 0.35 a)
+// without constant term (the form of Hastings, "Approximations for Digital
+// Computers", 1955).  The ten coefficients are a weighted least-squares fit
+// made for 0 <= a <= 14.5, refined towards equal relative errors: 2.2e-8
+// there, 2.5e-7 evaluated in fp32.  The derivative of gelu needs the same
+// exponential.  (erfcf and expf instead: 8192 x 8192 forward 164 us, backward
+// 193, bound by instructions.)
+__device__ __forceinline__ void normal(float z, float* p, float* bell) {
+    const float a = fabsf(z);
+    float t;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.35f, a, 1.0f)));
+    const float e = expf(-0.5f * a * a);
+    float f = 0.0030903539154678583f;
+    f = fmaf(f, t, -0.04539582133293152f);
+    f = fmaf(f, t, 0.18077702820301056f);
+    f = fmaf(f, t, -0.3026995360851288f);
+    f = fmaf(f, t, 0.19630774855613708f);
+    f = fmaf(f, t, -0.04188587889075279f);
+    f = fmaf(f, t, 0.11156046390533447f);
+    f = fmaf(f, t, 0.1186375617980957f);
+    f = fmaf(f, t, 0.13999271392822266f);
+    f = fmaf(f, t, 0.13961537182331085f);
+    const float below = f * t * e;
+    *p = z < 0.0f ? below : 1.0f - below;
+    *bell = e;
 }
+
+// act(z) and act'(z) in fp32.
 template <int ACT>
 __device__ __forceinline__ void act_both(float z, float* value, float* slope) {
     if (ACT == kActSilu) {
@@ -52,10 +74,17 @@ __device__ __forceinline__ void act_both(float z, float* value, float* slope) {
         *value = z * s;
         *slope = s * fmaf(z, 1.0f - s, 1.0f);
     } else {
-        const float p = 0.5f * erfcf(-0.70710678118654752f * z);
+        float p, bell;
+        normal(z, &p, &bell);
         *value = z * p;
-        *slope = fmaf(z * expf(-0.5f * z * z), 0.39894228040143268f, p);
+        *slope = fmaf(z * bell, 0.39894228040143268f, p);
     }
+}
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+    float value, slope;
+    act_both<ACT>(z, &value, &slope);
+    return value;
 }
 
 constexpr int kBlocksPerSm = 64;
@@ -295,6 +324,8 @@ __device__ __forceinline__ Lane values(const Held& h) {
 // gated forward 137.6 against 164.3).
 #define Q8_FOR_EACH_PLACE(p)                                                       \
     const int lane = threadIdx.x & 31;                                             \
+    pdl_wait();                                                                    \
+    pdl_trigger();                                                                 \
     for (Walk walk(cols); walk.row < rows; walk.next())                            \
         if (const Place p = place(walk, cols, lane); true)
 
@@ -374,77 +405,82 @@ unsigned vectors_bf16(const void* p, long long ld, int rows) {
     return a % 16 == 0 ? kVec16 : kVecNone;
 }
 
+// Launched as programmatic dependents: a kernel's launch overlaps the end of
+// the one before it, whose outputs it waits for.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int rows, int cols, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.gridDim = dim3(grid_for(rows, cols));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int FMT, typename T>
-void restore(const Q8In& q, int rows, int cols, void* x, long long ldx, unsigned vec,
-             cudaStream_t s) {
-    const auto kernel = vec ? q8_restore_kernel<FMT, T, true> : q8_restore_kernel<FMT, T, false>;
-    kernel<<<grid_for(rows, cols), kThreads, 0, s>>>(q, rows, cols, static_cast<T*>(x), ldx, vec);
+cudaError_t restore(const Q8In& q, int rows, int cols, void* x, long long ldx, unsigned vec,
+                    cudaStream_t s) {
+    return launch(vec ? q8_restore_kernel<FMT, T, true> : q8_restore_kernel<FMT, T, false>, rows,
+                  cols, s, q, rows, cols, static_cast<T*>(x), ldx, vec);
 }
 template <int FMT>
-void store(const float* x, long long ldx, int rows, int cols, const Q8Out& q, cudaStream_t s) {
+cudaError_t store(const float* x, long long ldx, int rows, int cols, const Q8Out& q,
+                  cudaStream_t s) {
     const unsigned vec = vectors(x, ldx, rows);
-    const auto kernel = vec ? q8_store_kernel<FMT, true> : q8_store_kernel<FMT, false>;
-    kernel<<<grid_for(rows, cols), kThreads, 0, s>>>(x, ldx, vec, rows, cols, q);
+    return launch(vec ? q8_store_kernel<FMT, true> : q8_store_kernel<FMT, false>, rows, cols, s, x,
+                  ldx, vec, rows, cols, q);
 }
 template <int FMT, int ACT>
-void gated(const GatedArgs& a, cudaStream_t s) {
+cudaError_t gated(const GatedArgs& a, cudaStream_t s) {
     const unsigned vg = vectors(a.g, a.ldg, a.rows), vu = vectors(a.u, a.ldu, a.rows),
                    vh = vectors(a.h, a.ldh, a.rows);
-    const auto kernel =
-        vg && vu && vh ? q8_gated_kernel<FMT, ACT, true> : q8_gated_kernel<FMT, ACT, false>;
-    kernel<<<grid_for(a.rows, a.cols), kThreads, 0, s>>>(a.g, a.ldg, vg, a.u, a.ldu, vu, a.rows,
-                                                         a.cols, a.h, a.ldh, vh, a.gq, a.uq);
+    return launch(
+        vg && vu && vh ? q8_gated_kernel<FMT, ACT, true> : q8_gated_kernel<FMT, ACT, false>, a.rows,
+        a.cols, s, a.g, a.ldg, vg, a.u, a.ldu, vu, a.rows, a.cols, a.h, a.ldh, vh, a.gq, a.uq);
 }
 template <int FMT, int ACT>
-void gated_backward(const GatedBackwardArgs& a, cudaStream_t s) {
+cudaError_t gated_backward(const GatedBackwardArgs& a, cudaStream_t s) {
     const unsigned vd = vectors(a.dh, a.lddh, a.rows), vg = vectors(a.dg, a.lddg, a.rows),
                    vu = vectors(a.du, a.lddu, a.rows);
-    const auto kernel = vd && vg && vu ? q8_gated_backward_kernel<FMT, ACT, true>
-                                       : q8_gated_backward_kernel<FMT, ACT, false>;
-    kernel<<<grid_for(a.rows, a.cols), kThreads, 0, s>>>(a.gq, a.uq, a.dh, a.lddh, vd, a.rows,
-                                                         a.cols, a.dg, a.lddg, vg, a.du, a.lddu,
-                                                         vu, a.hq);
+    return launch(vd && vg && vu ? q8_gated_backward_kernel<FMT, ACT, true>
+                                 : q8_gated_backward_kernel<FMT, ACT, false>,
+                  a.rows, a.cols, s, a.gq, a.uq, a.dh, a.lddh, vd, a.rows, a.cols, a.dg, a.lddg,
+                  vg, a.du, a.lddu, vu, a.hq);
 }
 
 }  // namespace
 
 cudaError_t launch_q8_store(const float* x, long long ldx, int rows, int cols, int format,
                             const Q8Out& q, cudaStream_t s) {
-    if (format == kQ8Int8)
-        store<kQ8Int8>(x, ldx, rows, cols, q, s);
-    else
-        store<kQ8E4m3>(x, ldx, rows, cols, q, s);
-    return cudaGetLastError();
+    return format == kQ8Int8 ? store<kQ8Int8>(x, ldx, rows, cols, q, s)
+                             : store<kQ8E4m3>(x, ldx, rows, cols, q, s);
 }
 
 cudaError_t launch_q8_restore(const Q8In& q, int rows, int cols, int format, void* x,
                               long long ldx, int bf16, cudaStream_t s) {
     const unsigned vec = bf16 ? vectors_bf16(x, ldx, rows) : vectors(x, ldx, rows);
     if (format == kQ8Int8)
-        bf16 ? restore<kQ8Int8, __nv_bfloat16>(q, rows, cols, x, ldx, vec, s)
-             : restore<kQ8Int8, float>(q, rows, cols, x, ldx, vec, s);
-    else
-        bf16 ? restore<kQ8E4m3, __nv_bfloat16>(q, rows, cols, x, ldx, vec, s)
-             : restore<kQ8E4m3, float>(q, rows, cols, x, ldx, vec, s);
-    return cudaGetLastError();
+        return bf16 ? restore<kQ8Int8, __nv_bfloat16>(q, rows, cols, x, ldx, vec, s)
+                    : restore<kQ8Int8, float>(q, rows, cols, x, ldx, vec, s);
+    return bf16 ? restore<kQ8E4m3, __nv_bfloat16>(q, rows, cols, x, ldx, vec, s)
+                : restore<kQ8E4m3, float>(q, rows, cols, x, ldx, vec, s);
 }
 
 cudaError_t launch_q8_gated(const GatedArgs& a, cudaStream_t s) {
     if (a.format == kQ8Int8)
-        a.act == kActSilu ? gated<kQ8Int8, kActSilu>(a, s) : gated<kQ8Int8, kActGelu>(a, s);
-    else
-        a.act == kActSilu ? gated<kQ8E4m3, kActSilu>(a, s) : gated<kQ8E4m3, kActGelu>(a, s);
-    return cudaGetLastError();
+        return a.act == kActSilu ? gated<kQ8Int8, kActSilu>(a, s) : gated<kQ8Int8, kActGelu>(a, s);
+    return a.act == kActSilu ? gated<kQ8E4m3, kActSilu>(a, s) : gated<kQ8E4m3, kActGelu>(a, s);
 }
 
 cudaError_t launch_q8_gated_backward(const GatedBackwardArgs& a, cudaStream_t s) {
     if (a.format == kQ8Int8)
-        a.act == kActSilu ? gated_backward<kQ8Int8, kActSilu>(a, s)
-                          : gated_backward<kQ8Int8, kActGelu>(a, s);
-    else
-        a.act == kActSilu ? gated_backward<kQ8E4m3, kActSilu>(a, s)
-                          : gated_backward<kQ8E4m3, kActGelu>(a, s);
-    return cudaGetLastError();
+        return a.act == kActSilu ? gated_backward<kQ8Int8, kActSilu>(a, s)
+                                 : gated_backward<kQ8Int8, kActGelu>(a, s);
+    return a.act == kActSilu ? gated_backward<kQ8E4m3, kActSilu>(a, s)
+                             : gated_backward<kQ8E4m3, kActGelu>(a, s);
 }
 
 }  // namespace gemm_f32_impl
