@@ -229,16 +229,26 @@ struct Q8WgradArgs {
     int mode;  // epilogue.cuh
 };
 cudaError_t launch_q8_wgrad_ffma(const Q8WgradArgs& a, cudaStream_t s);
-// The tensor-core form: CTA pairs, 256 x 256 tiles.  tmY is dY as {N, T}
-// floats, box 128 x 32; tmC the codes as {cols, T} bytes, box 128 x 32; tmS
-// the exponents as {ceil(cols / 32), T} bytes, box 16 x 32; none swizzled.
-// out is dW, or with splits > 1 the partials (alpha, beta by mode).
+// The tensor-core form: CTA pairs, 256 x 256 tiles.  tmC is the codes as
+// {cols, T} bytes, box 128 x 32; tmS the exponents as {ceil(cols / 32), T}
+// bytes, box 16 x 32; dY is tmY.map[0], {N, T} floats, box 128 x 32, where its
+// rows start on 16-byte boundaries.  Otherwise (shifted) map[c] holds rows c,
+// c + 4, ... from the 16-byte boundary at or before the first of them: {N +
+// shift, rows} floats, box 132 x 8, shift c of 0 .. 3 floats in bits 2 c of
+// shifts; residues without rows take any map.  None is swizzled.  out is dW,
+// or with splits > 1 the partials (alpha, beta by mode).
+struct Q8WgradMaps {
+    CUtensorMap map[4];
+};
 struct Q8WgradTile {
     int features, columns, tokens;  // of a tile; of a pipeline stage
 };
 Q8WgradTile q8_wgrad_tile();
 struct Q8WgradPairArgs {
-    CUtensorMap tmY, tmC, tmS;
+    Q8WgradMaps tmY;
+    CUtensorMap tmC, tmS;
+    int shifted;
+    unsigned shifts;
     float* out;
     long long ldo, split_stride;
     int rows, cols, N, format;

@@ -12,6 +12,12 @@
 
 using namespace gemm_f32_impl;
 
+#define Q8_TRY(expr)                                  \
+    do {                                              \
+        const int st_ = (expr);                       \
+        if (st_ != GEMM_F32_SUCCESS) return st_;      \
+    } while (0)
+
 namespace {
 
 // A matrix in memory, in bytes: `rows` rows of `width` bytes, `stride` apart.
@@ -107,10 +113,8 @@ long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
 // How the tensor-core kernel would run a weight gradient.
 struct WgradPlan {
     int splits, kb_per_split, chunk;
-    int copy;                // dY goes through a padded copy
-    long long ldy;           // row stride of what the kernel reads
-    long long ldw;           // row stride of the split partials
-    size_t off_copy, off_parts, bytes;
+    long long ldw;  // row stride of the split partials
+    size_t off_parts, bytes;
 };
 
 WgradPlan plan_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
@@ -130,29 +134,38 @@ WgradPlan plan_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
     p.kb_per_split = static_cast<int>((kb_total + s - 1) / s);
     p.splits = (kb_total + p.kb_per_split - 1) / p.kb_per_split;  // none of them empty
     p.chunk = 8;
-    // TMA reads rows that start on 16-byte boundaries
-    p.ldy = a.rows == 1 ? round_up(a.N, 4) : a.lddy;
-    p.copy = (reinterpret_cast<uintptr_t>(a.dy) & 15u) || (p.ldy & 3);
-    if (p.copy) p.ldy = round_up(a.N, 4);
     p.ldw = round_up(a.N, 4);
-    size_t off = kWorkspaceCounterBytes;
-    p.off_copy = off;
-    if (p.copy) off += static_cast<size_t>(round_up(p.ldy * a.rows * 4, 256));
-    p.off_parts = off;
-    if (p.splits > 1) off += static_cast<size_t>(p.ldw * a.cols * 4) * p.splits;
-    p.bytes = p.copy || p.splits > 1 ? off : 0;
+    p.off_parts = kWorkspaceCounterBytes;
+    if (p.splits > 1) p.bytes = p.off_parts + static_cast<size_t>(p.ldw * a.cols * 4) * p.splits;
     return p;
+}
+
+// The tensor maps of dY (rows x N, row stride ld): see q8_wgrad_tmem.cu.
+int map_dy(const float* dy, long long ld, int rows, int N, Q8WgradPairArgs* k) {
+    const Q8WgradTile tile = q8_wgrad_tile();
+    const int box = tile.columns / 2;
+    const uintptr_t base = reinterpret_cast<uintptr_t>(dy);
+    if (rows == 1) ld = round_up(N, 4);  // never used
+    if (base % 16 == 0 && ld % 4 == 0)
+        return call_tensor_map(&k->tmY.map[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dy, N, rows, 4 * ld,
+                               box, tile.tokens);
+    k->shifted = 1;
+    for (int c = 0; c < 4; ++c) {
+        const int row = c < rows ? c : 0;
+        const uintptr_t first = base + static_cast<uintptr_t>(row * ld) * 4;
+        const unsigned shift = static_cast<unsigned>(first % 16 / 4);
+        k->shifts |= shift << (2 * c);
+        Q8_TRY(call_tensor_map(&k->tmY.map[c], CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                               reinterpret_cast<const void*>(first - 4 * shift),
+                               static_cast<long long>(N) + shift, (rows - 1 - row) / 4 + 1, 16 * ld,
+                               box + 4, tile.tokens / 4));
+    }
+    return GEMM_F32_SUCCESS;
 }
 
 int status(cudaError_t e) { return e == cudaSuccess ? GEMM_F32_SUCCESS : static_cast<int>(e); }
 
 }  // namespace
-
-#define Q8_TRY(expr)                                  \
-    do {                                              \
-        const int st_ = (expr);                       \
-        if (st_ != GEMM_F32_SUCCESS) return st_;      \
-    } while (0)
 
 extern "C" {
 
@@ -282,19 +295,13 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     const WgradPlan p = plan_wgrad(a, splits, c.sm_count);
     unsigned char* ws = nullptr;
     if (p.bytes) Q8_TRY(call_workspace(c, stream, p.bytes, &ws));
-    const float* dy = dY;
-    if (p.copy) dy = reinterpret_cast<const float*>(ws + p.off_copy);
     const Q8WgradTile tile = q8_wgrad_tile();
     Q8WgradPairArgs k = {};
-    Q8_TRY(call_tensor_map(&k.tmY, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dy, N, x->rows, 4 * p.ldy,
-                           tile.columns / 2, tile.tokens));
+    Q8_TRY(map_dy(dY, lddy, x->rows, N, &k));
     Q8_TRY(call_tensor_map(&k.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->codes, x->cols, x->rows,
                            x->ldcodes, tile.features / 2, tile.tokens));
     Q8_TRY(call_tensor_map(&k.tmS, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->scales, blocks_of(x->cols),
                            x->rows, x->ldscales, 16, tile.tokens));
-    if (p.copy)
-        Q8_TRY(status(launch_pad_copy(dY, lddy, x->rows, N,
-                                      reinterpret_cast<float*>(ws + p.off_copy), p.ldy, stream)));
     float* parts = reinterpret_cast<float*>(ws + p.off_parts);
     const long long part_stride = p.ldw * x->cols;
     k.out = p.splits > 1 ? parts : dW;

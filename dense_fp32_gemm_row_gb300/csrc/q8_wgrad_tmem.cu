@@ -82,11 +82,15 @@ struct WgradCfg {
     static constexpr int XB_BYTES = HALF * KT * 2;   // x^ in bf16: two 64-feature groups
     static constexpr int GROUP_BYTES = 64 * KT * 2;  // rows of 128 bytes, a token each
     static constexpr int Y_BYTES = HALF * KT * 4;
+    // dY by rows of one residue modulo 4, four columns wider (see the kernel)
+    static constexpr int SHIFT_PITCH = (HALF + 4) * 4;
+    static constexpr int SHIFT_GROUP = KT / 4 * SHIFT_PITCH;
+    static constexpr int Y_SLOT = 4 * SHIFT_GROUP;
     static constexpr int C_BYTES = HALF * KT;
     static constexpr int S_BYTES = 16 * KT;
     // the swizzled x^ stages first: each 1024-byte aligned
     static constexpr int Y_OFF = STAGES * XB_BYTES;
-    static constexpr int C_OFF = Y_OFF + RAW * Y_BYTES;
+    static constexpr int C_OFF = Y_OFF + RAW * Y_SLOT;
     static constexpr int S_OFF = C_OFF + RAW * C_BYTES;
     static constexpr int BAR_OFF = S_OFF + RAW * S_BYTES;
     static constexpr int CONV_WARPS = 4 + 4;  // splitters, decoders
@@ -110,6 +114,7 @@ struct WgradCfg {
     static_assert(REGS_CONTROL + REGS_SPLIT + REGS_DECODE + 2 * REGS_EPI <= 5 * REGS_LAUNCH,
                   "register shares");
     static_assert(OP_COL0 + STAGES * OP_COLS <= TMEM_COLS, "tensor-memory columns");
+    static_assert(SHIFT_GROUP % 128 == 0 && Y_SLOT >= Y_BYTES, "dY stages");
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -205,9 +210,16 @@ __device__ __forceinline__ void mma_bf16_pair_tmem_a(uint32_t d_tmem, uint32_t a
         : "memory");
 }
 
-template <int FMT>
+// SHIFTED: rows of dY that do not start on 16-byte boundaries, as TMA loads
+// must.  Four row strides are a multiple of 16 bytes whatever the stride, so
+// the rows t = 4 i + c of each residue c form a matrix that a tensor map can
+// describe, from the 16-byte boundary at or before its first element: its
+// columns then lie shifts[c] (0 .. 3 floats, two bits each) further right, and
+// a box four columns wider holds the tile's.  Such a stage is four boxes of 8
+// rows, and the splitter adds the shift; no padded copy of dY is made.
+template <int FMT, bool SHIFTED>
 __global__ void __launch_bounds__(WgradCfg::THREADS, 1)
-q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
+q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                      const __grid_constant__ CUtensorMap tmC,
                      const __grid_constant__ CUtensorMap tmS, float* __restrict__ out,
                      long long ldo, long long split_stride, int D, int N, int T, int kb_per_split,
@@ -240,7 +252,7 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
     const int kb_total = (T - 1) / C::KT + 1;
 
     if (threadIdx.x == 0) {
-        prefetch_tmap(&tmY);
+        for (int c = 0; c < (SHIFTED ? 4 : 1); ++c) prefetch_tmap(&tmY.map[c]);
         prefetch_tmap(&tmC);
         prefetch_tmap(&tmS);
         for (int r = 0; r < C::RAW; ++r) {
@@ -310,8 +322,18 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
                         }
                         const int t0 = (w.kb_begin + kb) * C::KT;
                         const uint32_t fb = full0 + 8 * r;
-                        mbar_arrive_expect_tx(fb, C::Y_BYTES + C::C_BYTES + C::S_BYTES);
-                        tma_load_2d(sbase + C::Y_OFF + r * C::Y_BYTES, &tmY, fb, nc, t0);
+                        const uint32_t yb = sbase + C::Y_OFF + r * C::Y_SLOT;
+                        mbar_arrive_expect_tx(
+                            fb, (SHIFTED ? C::Y_SLOT : C::Y_BYTES) + C::C_BYTES + C::S_BYTES);
+                        if (SHIFTED) {
+                            // a residue without rows (T < 4) reads beyond its map: zeros
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                tma_load_2d(yb + c * C::SHIFT_GROUP, &tmY.map[c], fb, nc,
+                                            c < T ? t0 / 4 : C::KT);
+                        } else {
+                            tma_load_2d(yb, &tmY.map[0], fb, nc, t0);
+                        }
                         tma_load_2d(sbase + C::C_OFF + r * C::C_BYTES, &tmC, fb, dc, t0);
                         tma_load_2d(sbase + C::S_OFF + r * C::S_BYTES, &tmS, fb, bc, t0);
                     }
@@ -385,6 +407,10 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
         // ------------------------------ dY splitters (warps 4-7, both CTAs) -----------
         regs_dec<C::REGS_SPLIT>();
         const int q = warp & 3;
+        uint32_t at[4];  // SHIFTED: a residue's rows in a stage, and their shift
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            at[c] = static_cast<uint32_t>(c * C::SHIFT_GROUP) + 4u * ((shifts >> (2 * c)) & 3u);
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         int it = 0;
         bool ok = true;
@@ -403,17 +429,20 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
                 }
                 // the MMAs that read this stage before are done
                 tc_fence_after();
-                const uint32_t src = sbase + C::Y_OFF + raw * C::Y_BYTES +
+                const uint32_t src = sbase + C::Y_OFF + raw * C::Y_SLOT +
                                      static_cast<uint32_t>(4 * (32 * q + lane));
                 const uint32_t col =
                     lane_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
-                // 16 tokens at a time: this warpgroup runs on 56 registers
+                // 16 tokens at a time: this warpgroup runs on 48 registers
 #pragma unroll
                 for (int h = 0; h < C::KT / 16; ++h) {
                     float y[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        y[i] = lds_f32(src + static_cast<uint32_t>(16 * h + i) * (4 * C::HALF));
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t t = static_cast<uint32_t>(16 * h + i);
+                        y[i] = lds_f32(SHIFTED ? src + at[i & 3] + (t >> 2) * C::SHIFT_PITCH
+                                               : src + t * (4 * C::HALF));
+                    }
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
                         uint32_t p[8];
@@ -571,29 +600,26 @@ q8_wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmY,
 // mutex is held).  The register rebalancing waits for ever unless the block
 // was launched with the whole register file, so a build in which the
 // compiler took fewer than 128 registers a thread is refused here.
-template <int FMT>
+template <int FMT, bool SHIFTED>
 cudaError_t configure(int dev) {
     constexpr int kDevices = 64;
     static bool done[kDevices] = {};
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, q8_wgrad_pair_kernel<FMT>);
+    cudaError_t e = cudaFuncGetAttributes(&attr, q8_wgrad_pair_kernel<FMT, SHIFTED>);
     if (e != cudaSuccess) return e;
     if (attr.numRegs < WgradCfg::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(q8_wgrad_pair_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             WgradCfg::SMEM_BYTES);
+    e = cudaFuncSetAttribute(q8_wgrad_pair_kernel<FMT, SHIFTED>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, WgradCfg::SMEM_BYTES);
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
 
-}  // namespace
-
-Q8WgradTile q8_wgrad_tile() { return {WgradCfg::TD, WgradCfg::TN, WgradCfg::KT}; }
-
-cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count) {
+template <int FMT, bool SHIFTED>
+cudaError_t launch(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count) {
     using C = WgradCfg;
-    cudaError_t e = a.format == kQ8Int8 ? configure<kQ8Int8>(dev) : configure<kQ8E4m3>(dev);
+    cudaError_t e = configure<FMT, SHIFTED>(dev);
     if (e != cudaSuccess) return e;
     const int tiles = ((a.cols - 1) / C::TD + 1) * ((a.N - 1) / C::TN + 1);
     const int units = tiles * a.splits;
@@ -611,14 +637,22 @@ cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int d
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg,
-                           a.format == kQ8Int8 ? q8_wgrad_pair_kernel<kQ8Int8>
-                                               : q8_wgrad_pair_kernel<kQ8E4m3>,
-                           a.tmY, a.tmC, a.tmS, a.out, a.ldo, a.split_stride, a.cols, a.N, a.rows,
-                           a.kb_per_split, a.splits, a.chunk, a.fault, a.timeout_ns, a.alpha,
-                           a.beta, a.mode);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, q8_wgrad_pair_kernel<FMT, SHIFTED>, a.tmY, a.shifts, a.tmC, a.tmS,
+                           a.out, a.ldo, a.split_stride, a.cols, a.N, a.rows, a.kb_per_split,
+                           a.splits, a.chunk, a.fault, a.timeout_ns, a.alpha, a.beta, a.mode);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+Q8WgradTile q8_wgrad_tile() { return {WgradCfg::TD, WgradCfg::TN, WgradCfg::KT}; }
+
+cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count) {
+    if (a.format == kQ8Int8)
+        return a.shifted ? launch<kQ8Int8, true>(a, s, dev, sm_count)
+                         : launch<kQ8Int8, false>(a, s, dev, sm_count);
+    return a.shifted ? launch<kQ8E4m3, true>(a, s, dev, sm_count)
+                     : launch<kQ8E4m3, false>(a, s, dev, sm_count);
 }
 
 }  // namespace gemm_f32_impl
