@@ -235,8 +235,7 @@ cudaError_t launch_q8_wgrad_ffma(const Q8WgradArgs& a, cudaStream_t s);
 // rows start on 16-byte boundaries.  Otherwise (shifted) map[c] holds rows c,
 // c + 4, ... from the 16-byte boundary at or before the first of them: {N +
 // shift, rows} floats, box 132 x 8, shift c of 0 .. 3 floats in bits 2 c of
-// shifts; residues without rows take any map.  None is swizzled.  out is dW,
-// or with splits > 1 the partials (alpha, beta by mode).
+// shifts; residues without rows take any map.  None is swizzled.
 struct Q8WgradMaps {
     CUtensorMap map[4];
 };
@@ -244,17 +243,47 @@ struct Q8WgradTile {
     int features, columns, tokens;  // of a tile; of a pipeline stage
 };
 Q8WgradTile q8_wgrad_tile();
+// How the tiles are shared out: the first `whole` are a unit each; the stages
+// of the `shared` ones behind them, laid end to end, are cut into `runs`, a
+// unit each.  They are cut group by group, of group_stages stages (one tile's,
+// or all of them) into group_runs runs of `per` or, the first `extra`, per + 1
+// stages.  All stages of the shared tiles together are below 2^31.
+struct Q8WgradShare {
+    int tiles_d, tiles_n;  // tiles of dW
+    int stages;            // of one tile
+    int whole, shared, runs;
+    int group_stages, group_runs, per, extra;
+};
+#ifdef __CUDACC__
+#define Q8_HOST_DEVICE __host__ __device__
+#else
+#define Q8_HOST_DEVICE
+#endif
+// first stage of run i, counted through the shared tiles (i == runs: the end)
+Q8_HOST_DEVICE inline int q8_wgrad_cut(const Q8WgradShare& s, int i) {
+    const int g = i / s.group_runs, j = i - g * s.group_runs;
+    return g * s.group_stages + j * s.per + (j < s.extra ? j : s.extra);
+}
+// the run that holds a stage
+Q8_HOST_DEVICE inline int q8_wgrad_run(const Q8WgradShare& s, int stage) {
+    const int g = stage / s.group_stages, k = stage - g * s.group_stages;
+    const int longer = s.extra * (s.per + 1);
+    const int j = k < longer ? k / (s.per + 1) : s.extra + (k - longer) / s.per;
+    return g * s.group_runs + j;
+}
+// bytes of the partial sums
+size_t q8_wgrad_parts_bytes(const Q8WgradShare& s);
 struct Q8WgradPairArgs {
     Q8WgradMaps tmY;
     CUtensorMap tmC, tmS;
     int shifted;
     unsigned shifts;
-    float* out;
-    long long ldo, split_stride;
+    float* dw;
+    long long lddw;
+    float* parts;  // partial sums of the shared tiles
     int rows, cols, N, format;
-    int kb_per_split;  // stages per split; every split has at least one
-    int splits;
-    int chunk;         // stages per tensor-core sum
+    Q8WgradShare share;
+    int chunk;  // stages per tensor-core sum
     unsigned* fault;
     long long timeout_ns;
     float alpha, beta;

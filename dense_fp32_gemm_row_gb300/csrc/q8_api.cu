@@ -4,6 +4,7 @@
 // process.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <limits>
 
@@ -110,34 +111,83 @@ Q8Out out_of(const gemm_f32_q8* q) { return {q->codes, q->scales, q->ldcodes, q-
 
 long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
 
-// How the tensor-core kernel would run a weight gradient.
-struct WgradPlan {
-    int splits, kb_per_split, chunk;
-    long long ldw;  // row stride of the split partials
-    size_t off_parts, bytes;
-};
+// The tensor-core weight gradient's times in microseconds, fitted to calls
+// with both forms forced (a stage is 32 tokens of a tile): a stage of clusters
+// that run through the tokens side by side and share operands in L2; of
+// clusters that are all at different tokens, with operands that fit L2 and
+// beyond it; the second kernel, and writing and adding one partial sum.
+// Measured, shared against whole: 4096 x 1280 x 2048 (40 tiles on 76 pairs)
+// 55.4 against 75.5 us, 4096 x 1536 x 2304 (54) 70.4 against 76.2, 4096 x 2048
+// x 2048 (64) 79.3 against 76.5, 16384 x 1280 x 2048 178 against 275, 16384 x
+// 2048 x 2048 287 against 277.
+constexpr double kWgradStageUs = 0.53, kWgradApartUs = 0.57, kWgradFarUs = 0.65;
+constexpr double kWgradSumUs = 4.0, kWgradPartUs = 0.05;
+constexpr double kWgradL2Bytes = 64e6;
+// what sharing has to save of the whole call: back to back the largest calls
+// are at the power limit and gain nothing from a shorter last round (8192 x
+// 8192 x 8192, 36 of 1024 tiles in halves: 2.00 against 1.93 ms)
+constexpr double kWgradLeastGain = 0.05;
 
-WgradPlan plan_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
+// The CUDA-core kernel, which has no pipeline to fill, for a few tokens and
+// small outputs (measured, against the tensor-core kernel, in microseconds:
+// 16 x 512 x 512 5.8 and 7.3, 16 x 1024 x 1024 5.9 and 7.4, 32 x 512 x 512 6.2
+// and 7.3; but 64 x 64 x 64 8.2 and 6.8, 32 x 2048 x 2048 18.4 and 8.9, 8 x
+// 8192 x 8192 115 and 50).
+constexpr int kFfmaTokens = 32;
+constexpr double kFfmaProducts = 2e7;
+
+// Shares out the last `shared` tiles in groups of `group` tiles, `runs` a group.
+void cut_tiles(Q8WgradShare* s, int shared, int group, int runs) {
+    s->whole -= shared;
+    s->shared = shared;
+    s->group_stages = group * s->stages;
+    s->group_runs = runs;
+    s->per = s->group_stages / runs;
+    s->extra = s->group_stages % runs;
+    s->runs = shared / group * runs;
+}
+
+// How the tiles of a weight gradient are shared out over the CTA pairs.
+// Requested splits: every tile in that many runs.  Otherwise whole tiles for
+// as many rounds as they fill, and the rest shared by all pairs where that
+// shortens the last round by more than the partial sums cost.
+Q8WgradShare share_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
     const Q8WgradTile tile = q8_wgrad_tile();
-    WgradPlan p = {};
-    const long long tiles = ((a.cols - 1LL) / tile.features + 1) * ((a.N - 1LL) / tile.columns + 1);
-    const int kb_total = (a.rows - 1) / tile.tokens + 1;
-    const int clusters = sm_count / 2;
-    long long s = splits;
-    if (s == 0) {
-        // spread few tiles over the clusters, at least four stages each
-        s = 2 * tiles <= clusters ? clusters / tiles : 1;
-        if (s > kb_total / 4) s = kb_total / 4;
+    Q8WgradShare s = {};
+    s.tiles_d = (a.cols - 1) / tile.features + 1;
+    s.tiles_n = (a.N - 1) / tile.columns + 1;
+    s.stages = (a.rows - 1) / tile.tokens + 1;
+    s.whole = s.tiles_d * s.tiles_n;
+    const int pairs = sm_count / 2;
+    const int rest = splits > 0 ? s.whole : s.whole % pairs;
+    const long long all = static_cast<long long>(rest) * s.stages;
+    if (all == 0 || all > std::numeric_limits<int>::max()) return s;
+    if (splits > 0) {
+        const int n = splits < s.stages ? splits : s.stages;
+        if (n > 1) cut_tiles(&s, rest, 1, n);
+        return s;
     }
-    if (s > kb_total) s = kb_total;
-    if (s < 1) s = 1;
-    p.kb_per_split = static_cast<int>((kb_total + s - 1) / s);
-    p.splits = (kb_total + p.kb_per_split - 1) / p.kb_per_split;  // none of them empty
-    p.chunk = 8;
-    p.ldw = round_up(a.N, 4);
-    p.off_parts = kWorkspaceCounterBytes;
-    if (p.splits > 1) p.bytes = p.off_parts + static_cast<size_t>(p.ldw * a.cols * 4) * p.splits;
-    return p;
+    // the same number of runs for every tile, which start side by side; or as
+    // many as there are pairs, over tile boundaries
+    const double whole_us = kWgradStageUs * s.stages;
+    const double least = whole_us * (1.0 - kWgradLeastGain * ((s.whole - 1) / pairs + 1));
+    const int each = std::min(pairs / rest, s.stages / 4);
+    const int through = static_cast<int>(std::min<long long>(pairs, all / 4));
+    double each_us = whole_us, through_us = whole_us;
+    if (each > 1)
+        each_us = kWgradStageUs * ((s.stages - 1) / each + 1) + kWgradSumUs +
+                  kWgradPartUs * each * rest;
+    if (through > rest) {
+        const bool far = a.rows * (4.0 * a.N + a.cols) > kWgradL2Bytes;
+        through_us = (far ? kWgradFarUs : kWgradApartUs) *
+                         static_cast<double>((all - 1) / through + 1) +
+                     kWgradSumUs + kWgradPartUs * (through + rest);
+    }
+    if (each_us < least && each_us <= through_us)
+        cut_tiles(&s, rest, 1, each);
+    else if (through_us < least)
+        cut_tiles(&s, rest, rest, through);
+    return s;
 }
 
 // The tensor maps of dY (rows x N, row stride ld): see q8_wgrad_tmem.cu.
@@ -289,40 +339,36 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     Q8WgradArgs a = {in_of(x), dY, dW, lddy, lddw, x->rows, x->cols, N, x->format, alpha, beta,
                      beta != 0.0f ? 2 : alpha == 1.0f ? 0 : 1};
     if (algo == GEMM_F32_ALGO_AUTO)
-        algo = 1.0 * x->rows * x->cols * N < 5e7 ? GEMM_F32_ALGO_FFMA : GEMM_F32_ALGO_3XBF16;
+        algo = x->rows <= kFfmaTokens && 1.0 * x->rows * x->cols * N <= kFfmaProducts
+                   ? GEMM_F32_ALGO_FFMA
+                   : GEMM_F32_ALGO_3XBF16;
     if (algo == GEMM_F32_ALGO_FFMA) return status(launch_q8_wgrad_ffma(a, stream));
 
-    const WgradPlan p = plan_wgrad(a, splits, c.sm_count);
-    unsigned char* ws = nullptr;
-    if (p.bytes) Q8_TRY(call_workspace(c, stream, p.bytes, &ws));
     const Q8WgradTile tile = q8_wgrad_tile();
     Q8WgradPairArgs k = {};
+    k.share = share_wgrad(a, splits, c.sm_count);
+    unsigned char* ws = nullptr;
+    if (k.share.shared)
+        Q8_TRY(call_workspace(c, stream, kWorkspaceCounterBytes + q8_wgrad_parts_bytes(k.share), &ws));
     Q8_TRY(map_dy(dY, lddy, x->rows, N, &k));
     Q8_TRY(call_tensor_map(&k.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->codes, x->cols, x->rows,
                            x->ldcodes, tile.features / 2, tile.tokens));
     Q8_TRY(call_tensor_map(&k.tmS, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->scales, blocks_of(x->cols),
                            x->rows, x->ldscales, 16, tile.tokens));
-    float* parts = reinterpret_cast<float*>(ws + p.off_parts);
-    const long long part_stride = p.ldw * x->cols;
-    k.out = p.splits > 1 ? parts : dW;
-    k.ldo = p.splits > 1 ? p.ldw : lddw;
-    k.split_stride = part_stride;
+    k.dw = dW;
+    k.lddw = lddw;
+    k.parts = k.share.shared ? reinterpret_cast<float*>(ws + kWorkspaceCounterBytes) : nullptr;
     k.rows = x->rows;
     k.cols = x->cols;
     k.N = N;
     k.format = x->format;
-    k.kb_per_split = p.kb_per_split;
-    k.splits = p.splits;
-    k.chunk = p.chunk;
+    k.chunk = 8;
     k.fault = c.fault;
     k.timeout_ns = kDefaultTimeoutNs;
     k.alpha = alpha;
     k.beta = beta;
-    k.mode = p.splits > 1 ? 0 : a.mode;
-    Q8_TRY(status(launch_q8_wgrad_pair(k, stream, c.dev, c.sm_count)));
-    if (p.splits == 1) return GEMM_F32_SUCCESS;
-    return status(launch_splitk_reduce(parts, part_stride, p.ldw, p.splits, dW, lddw, x->cols, N,
-                                       alpha, beta, a.mode, stream));
+    k.mode = a.mode;
+    return status(launch_q8_wgrad_pair(k, stream, c.dev, c.sm_count));
 }
 
 }  // extern "C"

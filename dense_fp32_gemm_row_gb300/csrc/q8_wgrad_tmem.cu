@@ -31,7 +31,7 @@
 //
 // 640 threads per CTA, registers rebalanced at start (launched at 96 each):
 //   warp 0       one lane: TMA loads of a 32-token stage (dY 128 columns x 32,
-//                codes 128 x 32, exponents 16 x 32), eight stages deep;
+//                codes 128 x 32, exponents 16 x 32), six stages deep;
 //   warp 1       tensor-memory allocation for the pair; in the leader one lane
 //                issues the MMAs and commits;
 //   warps 1-3 of the peer  relay: one lane each tells the leader, in turn, that
@@ -55,8 +55,9 @@
 // products at the burst rate of the library product: 1.72 ms; at its sustained
 // rate, which the power limit sets, 1.91).
 //
-// Few tiles and many tokens: the tokens are split over clusters into partial
-// sums, added in split order by the GEMM's reduction kernel.
+// Where the tiles do not fill the clusters evenly, the last of them are shared:
+// their stages, end to end, are cut into equal runs, whose partial sums a
+// second kernel adds in order.
 // Waits are bounded and wind down as in the GEMM kernels.
 #include <cstdint>
 
@@ -77,7 +78,7 @@ struct WgradCfg {
     static constexpr int HALF = 128;          // of each, per CTA
     static constexpr int KT = 32;             // tokens a stage
     static constexpr int UK = 16;             // tokens an MMA
-    static constexpr int RAW = 8;     // stages of copies
+    static constexpr int RAW = 6;     // stages of copies
     static constexpr int STAGES = 5;  // stages of MMA operands
     static constexpr int XB_BYTES = HALF * KT * 2;   // x^ in bf16: two 64-feature groups
     static constexpr int GROUP_BYTES = 64 * KT * 2;  // rows of 128 bytes, a token each
@@ -210,6 +211,145 @@ __device__ __forceinline__ void mma_bf16_pair_tmem_a(uint32_t d_tmem, uint32_t a
         : "memory");
 }
 
+// First feature and column of a tile: neighbouring tiles run down groups of 8
+// rows of tiles, so that the clusters at work share operands in L2.
+__device__ __forceinline__ void tile_at(const Q8WgradShare& sh, int tile, int& d0, int& n0) {
+    const int per_group = GROUP_M * sh.tiles_n;
+    const int group = tile / per_group, within = tile - group * per_group;
+    const int rows = min(sh.tiles_d - group * GROUP_M, GROUP_M);
+    const int column = within / rows;
+    d0 = (group * GROUP_M + within - column * rows) * WgradCfg::TD;
+    n0 = column * WgradCfg::TN;
+}
+
+// The work of one cluster, piece by piece: a whole tile, or a run of stages of
+// a shared tile.  A run may cover parts of several tiles; a part of a tile goes to slot (run + tile) of the partial sums, so that the slots of
+// one tile follow one another in the order of its stages.
+struct Pieces {
+    int u;          // next unit
+    int run, b, e;  // the current run, its stages left
+
+    __device__ __forceinline__ Pieces() : u(blockIdx.x >> 1), run(0), b(0), e(0) {}
+
+    __device__ __forceinline__ bool next(const Q8WgradShare& sh, Unit& w) {
+        int tile = u;
+        w.kb_begin = 0;
+        w.nkb = sh.stages;
+        w.slot = -1;
+        if (b >= e) {
+            if (u >= sh.whole + sh.runs) return false;
+            if (u >= sh.whole) {
+                run = u - sh.whole;
+                b = q8_wgrad_cut(sh, run);
+                e = q8_wgrad_cut(sh, run + 1);
+            }
+            u += gridDim.x >> 1;
+        }
+        if (b < e) {
+            const int t = b / sh.stages;
+            tile = sh.whole + t;
+            w.kb_begin = b - t * sh.stages;
+            w.nkb = min(sh.stages - w.kb_begin, e - b);
+            b += w.nkb;
+            if (w.nkb < sh.stages) w.slot = run + t;
+        }
+        tile_at(sh, tile, w.m0, w.n0);
+        return true;
+    }
+};
+
+// Adds the partial sums of the shared tiles, in the order of their stages, and
+// writes dW, 256 threads a block.
+//   Q = 1: a thread adds four columns of G rows at once, B partials of each in
+//   flight, and a block takes 4 G rows of a tile;
+//   Q = 4: for few outputs with many partials, each bound by the latency of
+//   its loads: four lanes share a group of four columns, each adding a
+//   contiguous quarter of the partials, B in flight, and their sums are added
+//   in order; a block takes one row of a tile.
+template <int Q, int G, int B>
+__global__ void __launch_bounds__(256)
+q8_wgrad_sum_kernel(const float* __restrict__ parts, Q8WgradShare sh, float* __restrict__ dw,
+                    long long lddw, bool vec, int D, int N, float alpha, float beta, int mode) {
+    using C = WgradCfg;
+    constexpr int kPart = C::TD * C::TN;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int q = Q == 1 ? 0 : lane / (32 / Q);
+    const int group = warp * (32 / Q) + lane % (32 / Q);  // of 256 / Q groups of four columns
+    const int col = 4 * (group % (C::TN / 4));
+    const int row0 = (256 / Q / (C::TN / 4)) * G * static_cast<int>(blockIdx.x) + group / (C::TN / 4);
+    for (int t = blockIdx.y; t < sh.shared; t += gridDim.y) {
+        // the runs that hold the tile's first and last stage
+        int first = t * sh.group_runs, n = sh.group_runs;
+        if (sh.group_stages != sh.stages) {
+            first = q8_wgrad_run(sh, t * sh.stages);
+            n = q8_wgrad_run(sh, (t + 1) * sh.stages - 1) - first + 1;
+        }
+        if (n == 1) continue;  // written by its cluster
+        int d0, n0;
+        tile_at(sh, sh.whole + t, d0, n0);
+        const int per = (n + Q - 1) / Q;
+        const int i1 = n0 + col < N ? min(n, (q + 1) * per) : 0;
+        const float* src = parts + static_cast<long long>(first + t) * kPart + col;
+        pdl_wait();  // the partial sums; only indices before it
+        float4 sum[G];
+        int row[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            sum[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            row[g] = row0 + g * (256 / Q / (C::TN / 4));
+        }
+        for (int i0 = q * per; i0 < i1; i0 += B) {
+            float4 v[G][B];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (i0 + k < i1 && d0 + row[g] < D)
+                        v[g][k] = __ldcg(reinterpret_cast<const float4*>(
+                            src + static_cast<long long>(i0 + k) * kPart + row[g] * C::TN));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (i0 + k < i1 && d0 + row[g] < D) {
+                        sum[g].x += v[g][k].x;
+                        sum[g].y += v[g][k].y;
+                        sum[g].z += v[g][k].z;
+                        sum[g].w += v[g][k].w;
+                    }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            // lanes of the first quarter gather the others' sums, in order
+            float4 all = sum[g];
+#pragma unroll
+            for (int k = 1; k < Q; ++k) {
+                const int from = lane % (32 / Q) + k * (32 / Q);
+                all.x += __shfl_sync(0xffffffffu, sum[g].x, from);
+                all.y += __shfl_sync(0xffffffffu, sum[g].y, from);
+                all.z += __shfl_sync(0xffffffffu, sum[g].z, from);
+                all.w += __shfl_sync(0xffffffffu, sum[g].w, from);
+            }
+            if (q == 0 && i1 > 0 && d0 + row[g] < D)
+                store4(dw + static_cast<long long>(d0 + row[g]) * lddw, n0 + col, N, all, vec,
+                       alpha, beta, mode);
+        }
+    }
+}
+
+// A thread's accumulators to the rows below one another at p.
+__device__ __forceinline__ void store_columns(const float (&acc)[EPI_COLS], float* p, long long ld,
+                                              int rows) {
+    if (rows >= EPI_COLS) {
+#pragma unroll
+        for (int j = 0; j < EPI_COLS; ++j) p[j * ld] = acc[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPI_COLS; ++j)
+            if (j < rows) p[j * ld] = acc[j];
+    }
+}
+
 // SHIFTED: rows of dY that do not start on 16-byte boundaries, as TMA loads
 // must.  Four row strides are a multiple of 16 bytes whatever the stride, so
 // the rows t = 4 i + c of each residue c form a matrix that a tensor map can
@@ -221,10 +361,10 @@ template <int FMT, bool SHIFTED>
 __global__ void __launch_bounds__(WgradCfg::THREADS, 1)
 q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                      const __grid_constant__ CUtensorMap tmC,
-                     const __grid_constant__ CUtensorMap tmS, float* __restrict__ out,
-                     long long ldo, long long split_stride, int D, int N, int T, int kb_per_split,
-                     int splits, int chunk, unsigned* fault, long long timeout_ns, float alpha,
-                     float beta, int scale_mode) {
+                     const __grid_constant__ CUtensorMap tmS, float* __restrict__ dw,
+                     long long lddw, float* __restrict__ parts, int D, int N, int T,
+                     Q8WgradShare share, int chunk, unsigned* fault, long long timeout_ns,
+                     float alpha, float beta, int scale_mode) {
     using C = WgradCfg;
     constexpr int STAGES = C::STAGES;
     extern __shared__ unsigned char smem_raw[];
@@ -244,12 +384,6 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int cluster = blockIdx.x >> 1;
-    const int nclusters = gridDim.x >> 1;
-    const int tiles_d = (D - 1) / C::TD + 1;
-    const int tiles_n = (N - 1) / C::TN + 1;
-    const int units = tiles_d * tiles_n * splits;
-    const int kb_total = (T - 1) / C::KT + 1;
 
     if (threadIdx.x == 0) {
         for (int c = 0; c < (SHIFTED ? 4 : 1); ++c) prefetch_tmap(&tmY.map[c]);
@@ -288,8 +422,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
     auto relay = [&](int i) {
         const uint32_t ready_leader = map_to_cta(ready0, 0);
         int total = 0;
-        for (int u = cluster; u < units; u += nclusters)
-            total += decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD).nkb;
+        Unit w;
+        for (Pieces todo; todo.next(share, w);) total += w.nkb;
         for (int it = i; it < total; it += C::RELAYS) {
             const int s = it % STAGES;
             if (!role_wait(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault, kFaultFullBarrier,
@@ -306,8 +440,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                 // -------------------------- TMA producer (both CTAs) ------------------
                 int it = 0;
                 bool ok = true;
-                for (int u = cluster; u < units && ok; u += nclusters) {
-                    const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+                Unit w;
+                    for (Pieces todo; ok && todo.next(share, w);) {
                     const int dc = w.m0 + static_cast<int>(rank) * C::HALF;
                     const int nc = w.n0 + static_cast<int>(rank) * C::HALF;
                     // exponents: the aligned 16 blocks that hold this CTA's four
@@ -353,8 +487,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                 int it = 0;
                 int g = 0;  // chunks issued
                 bool ok = true;
-                for (int u = cluster; u < units && ok; u += nclusters) {
-                    const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+                Unit w;
+                    for (Pieces todo; ok && todo.next(share, w);) {
                     for (int c0 = 0; c0 < w.nkb && ok; c0 += chunk, ++g) {
                         // the single accumulator: both epilogues have drained chunk g - 1
                         if (g >= 1 && !role_wait(acce, (g - 1) & 1, timeout_ns, fault,
@@ -414,8 +548,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
         int it = 0;
         bool ok = true;
-        for (int u = cluster; u < units && ok; u += nclusters) {
-            const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+        Unit w;
+            for (Pieces todo; ok && todo.next(share, w);) {
             for (int kb = 0; kb < w.nkb; ++kb, ++it) {
                 const int s = it % STAGES, raw = it % C::RAW;
                 bool got = role_wait(full0 + 8 * raw, (it / C::RAW) & 1, timeout_ns, fault,
@@ -475,8 +609,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         const int row0 = 8 * (warp - 8) + (lane >> 4);
         int it = 0;
         bool ok = true;
-        for (int u = cluster; u < units && ok; u += nclusters) {
-            const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+        Unit w;
+            for (Pieces todo; ok && todo.next(share, w);) {
             const int dc = w.m0 + static_cast<int>(rank) * C::HALF;
             const uint32_t sc = static_cast<uint32_t>(((dc / kQ8Block) & 15) + (c >> 2));
             for (int kb = 0; kb < w.nkb; ++kb, ++it) {
@@ -537,8 +671,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         float acc[EPI_COLS];
         int g = 0;
         bool ok = true;
-        for (int u = cluster; u < units && ok; u += nclusters) {
-            const Unit w = decode(u, tiles_d, tiles_n, kb_per_split, kb_total, C::TN, C::TD);
+        Unit w;
+            for (Pieces todo; ok && todo.next(share, w);) {
             for (int c0 = 0; c0 < w.nkb; c0 += chunk, ++g) {
                 const bool got = role_wait(accf, g & 1, timeout_ns, fault, kFaultAccumBarrier,
                                            abort_flag);
@@ -574,13 +708,23 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
             }
             if (!ok) break;
             const int n = w.n0 + nl;
-            if (n < N) {
-                float* p = out + static_cast<long long>(w.split) * split_stride +
-                           static_cast<long long>(w.m0 + col0) * ldo + n;
-                const int rows = D - (w.m0 + col0);
+            const int rows = D - (w.m0 + col0);
+            // Code that runs once a tile is bound by the fetching of its
+            // instructions: the usual stores are as few as can be.
+            if (n >= N) {
+            } else if (w.slot >= 0) {
+                float* p = parts + static_cast<long long>(w.slot) * (C::TD * C::TN) +
+                           col0 * C::TN + nl;
+                store_columns(acc, p, C::TN, rows);
+            } else {
+                float* p = dw + static_cast<long long>(w.m0 + col0) * lddw + n;
+                if (scale_mode == kStorePlain) {
+                    store_columns(acc, p, lddw, rows);
+                } else {
 #pragma unroll
-                for (int j = 0; j < EPI_COLS; ++j, p += ldo)
-                    if (j < rows) *p = scale1(acc[j], p, alpha, beta, scale_mode);
+                    for (int j = 0; j < EPI_COLS; ++j, p += lddw)
+                        if (j < rows) *p = scale1(acc[j], p, alpha, beta, scale_mode);
+                }
             }
         }
         __syncwarp();
@@ -621,9 +765,8 @@ cudaError_t launch(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_cou
     using C = WgradCfg;
     cudaError_t e = configure<FMT, SHIFTED>(dev);
     if (e != cudaSuccess) return e;
-    const int tiles = ((a.cols - 1) / C::TD + 1) * ((a.N - 1) / C::TN + 1);
-    const int units = tiles * a.splits;
-    const int clusters = units < sm_count / 2 ? units : sm_count / 2;
+    const long long units = static_cast<long long>(a.share.whole) + a.share.runs;
+    const int clusters = static_cast<int>(units < sm_count / 2 ? units : sm_count / 2);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -638,8 +781,29 @@ cudaError_t launch(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_cou
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, q8_wgrad_pair_kernel<FMT, SHIFTED>, a.tmY, a.shifts, a.tmC, a.tmS,
-                           a.out, a.ldo, a.split_stride, a.cols, a.N, a.rows, a.kb_per_split,
-                           a.splits, a.chunk, a.fault, a.timeout_ns, a.alpha, a.beta, a.mode);
+                           a.dw, a.lddw, a.parts, a.cols, a.N, a.rows, a.share, a.chunk, a.fault,
+                           a.timeout_ns, a.alpha, a.beta, a.mode);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+constexpr int kSumRows = 2;
+// The kernel that adds the shared tiles' partial sums.
+cudaError_t launch_sum(const Q8WgradPairArgs& a, cudaStream_t s) {
+    using C = WgradCfg;
+    const bool vec = a.lddw % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % 16 == 0;
+    // four lanes an output group where a tile has many partials
+    const bool quarters = a.share.runs >= 8LL * a.share.shared;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.gridDim = dim3(quarters ? C::TD : C::TD / (4 * kSumRows), a.share.shared < 65535 ? a.share.shared : 65535);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, quarters ? q8_wgrad_sum_kernel<4, 1, 8> : q8_wgrad_sum_kernel<1, kSumRows, 4>,
+        static_cast<const float*>(a.parts), a.share, a.dw, a.lddw, vec, a.cols, a.N, a.alpha,
+        a.beta, a.mode);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -647,12 +811,21 @@ cudaError_t launch(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_cou
 
 Q8WgradTile q8_wgrad_tile() { return {WgradCfg::TD, WgradCfg::TN, WgradCfg::KT}; }
 
+size_t q8_wgrad_parts_bytes(const Q8WgradShare& sh) {
+    if (!sh.shared) return 0;
+    return (static_cast<size_t>(sh.runs) + sh.shared) * (WgradCfg::TD * WgradCfg::TN * 4);
+}
+
 cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count) {
+    cudaError_t e;
     if (a.format == kQ8Int8)
-        return a.shifted ? launch<kQ8Int8, true>(a, s, dev, sm_count)
-                         : launch<kQ8Int8, false>(a, s, dev, sm_count);
-    return a.shifted ? launch<kQ8E4m3, true>(a, s, dev, sm_count)
-                     : launch<kQ8E4m3, false>(a, s, dev, sm_count);
+        e = a.shifted ? launch<kQ8Int8, true>(a, s, dev, sm_count)
+                      : launch<kQ8Int8, false>(a, s, dev, sm_count);
+    else
+        e = a.shifted ? launch<kQ8E4m3, true>(a, s, dev, sm_count)
+                      : launch<kQ8E4m3, false>(a, s, dev, sm_count);
+    if (e != cudaSuccess || !a.share.shared) return e;
+    return launch_sum(a, s);
 }
 
 }  // namespace gemm_f32_impl

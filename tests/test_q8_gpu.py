@@ -391,7 +391,10 @@ def test_wgrad_of_every_code_and_exponent(fmt, algo):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,D,N", [(4096, 256, 256), (5000, 300, 500), (20000, 256, 40),
-                                   (65536, 64, 96), (2048, 2048, 1024), (600, 4100, 1500)])
+                                   (65536, 64, 96), (2048, 2048, 1024), (600, 4100, 1500),
+                                   # tiles of 256 x 256 shared by the 76 CTA pairs: 45 and, after
+                                   # a round of whole tiles, 14 of 90, over tile boundaries or not
+                                   (2100, 1283, 2049), (2100, 2305, 2303)])
 def test_wgrad_large(fmt, T, D, N):
     q, x, dy = wgrad_case(np.random.default_rng(T + D + N), T, D, N, fmt)
     assert_wgrad(g.q8_wgrad(q, matrix(dy)[0]), x, dy)
@@ -409,7 +412,8 @@ def test_wgrad_strides_and_alignment(fmt, T, D, N, pad, offset):
     assert outside_is_nan(out, buf)
 
 
-@pytest.mark.parametrize("T,D,N", [(20, 40, 50), (500, 260, 300), (8192, 128, 260)])
+@pytest.mark.parametrize("T,D,N", [(20, 40, 50), (500, 260, 300), (8192, 128, 260),
+                                   (4100, 1281, 2049)])
 @pytest.mark.parametrize("alpha,beta", [(1.0, 1.0), (0.5, 0.0), (-2.0, 0.25), (1.0, -1.0)])
 def test_wgrad_alpha_beta(T, D, N, alpha, beta):
     rng = np.random.default_rng(T)
