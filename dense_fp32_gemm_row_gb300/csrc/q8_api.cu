@@ -128,6 +128,12 @@ constexpr double kWgradL2Bytes = 64e6;
 // 8192 x 8192, 36 of 1024 tiles in halves: 2.00 against 1.93 ms)
 constexpr double kWgradLeastGain = 0.05;
 
+// Stages per tensor-core sum, 256 tokens: relative error 7e-7 (2-norm; an fp32
+// product in one running sum has 1.6e-6 at 8192 tokens).  Each sum costs the
+// MMAs a wait of ~0.23 us: 128 tokens, 4e-7, were 2.2 % slower at 8192 x 8192
+// x 8192, 512 tokens, 1.4e-6, 0.8 % faster.
+constexpr int kWgradChunk = 8;
+
 // The CUDA-core kernel, which has no pipeline to fill, for a few tokens and
 // small outputs (measured, against the tensor-core kernel, in microseconds:
 // 16 x 512 x 512 5.8 and 7.3, 16 x 1024 x 1024 5.9 and 7.4, 32 x 512 x 512 6.2
@@ -323,6 +329,8 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     if (algo != GEMM_F32_ALGO_AUTO && algo != GEMM_F32_ALGO_FFMA && algo != GEMM_F32_ALGO_3XBF16)
         return GEMM_F32_ERR_INVALID_VALUE;
     if (x->cols == 0 || N == 0) return GEMM_F32_SUCCESS;
+    // more tiles of dW than an index holds: no memory does either
+    if (1.0 * x->cols * N > 1e13) return GEMM_F32_ERR_INVALID_VALUE;
     Q8_TRY(check_matrix(dW, x->cols, N, lddw, 4));
     const bool reads = x->rows > 0 && alpha != 0.0f;
     if (x->rows > 0) {
@@ -362,7 +370,7 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     k.cols = x->cols;
     k.N = N;
     k.format = x->format;
-    k.chunk = 8;
+    k.chunk = kWgradChunk;
     k.fault = c.fault;
     k.timeout_ns = kDefaultTimeoutNs;
     k.alpha = alpha;

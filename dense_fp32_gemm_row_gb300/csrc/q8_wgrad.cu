@@ -11,6 +11,8 @@
 // each, 16 tokens a step through shared memory; sums over 256 tokens are
 // added into a second accumulator, so that the rounding error of a long sum
 // grows with the number of such chunks and not with the number of tokens.
+// It is for small calls (a few tokens, small outputs), which are bound by the
+// launch: 16 x 512 x 512 takes 5.8 us against 7.3 on the tensor core.
 #include <cstdint>
 
 #include "device_sync.cuh"
@@ -39,56 +41,57 @@ q8_wgrad_ffma_kernel(Q8In x, int rows, int cols, const float* __restrict__ dy, l
     const int tx = tid & 15, ty = tid >> 4;
     // loads: token tid / 16 of the step, four columns from 4 (tid % 16)
     const int lt = tid >> 4, lc = 4 * (tid & 15);
-    for (int d0 = blockIdx.y * kTile; d0 < cols; d0 += gridDim.y * kTile) {
-    float sum[4][4] = {}, acc[4][4];
-    for (long long t0 = 0; t0 < rows; t0 += kChunk) {
+    for (long long d0 = blockIdx.y * kTile; d0 < cols; d0 += gridDim.y * kTile) {
+        float sum[4][4] = {}, acc[4][4];
+        for (long long t0 = 0; t0 < rows; t0 += kChunk) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        const long long t1 = min(static_cast<long long>(rows), t0 + kChunk);
-        for (long long tb = t0; tb < t1; tb += kStep) {
-            const long long t = tb + lt;
-            const bool in = t < rows;
+                for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+            const long long t1 = min(static_cast<long long>(rows), t0 + kChunk);
+            for (long long tb = t0; tb < t1; tb += kStep) {
+                const long long t = tb + lt;
+                const bool in = t < rows;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int d = d0 + lc + i, n = n0 + lc + i;
-                float v = 0.0f;
-                if (in && d < cols)
-                    v = q8_decode4<FMT>(x.codes[t * x.ldcodes + d]).x *
-                        q8_scale<FMT>(x.scales[t * x.ldscales + d / kQ8Block]);
-                xs[lt][lc + i] = v;
-                ys[lt][lc + i] = in && n < N ? dy[t * lddy + n] : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    const long long d = d0 + lc + i;
+                    const int n = n0 + lc + i;
+                    float v = 0.0f;
+                    if (in && d < cols)
+                        v = q8_decode4<FMT>(x.codes[t * x.ldcodes + d]).x *
+                            q8_scale<FMT>(x.scales[t * x.ldscales + d / kQ8Block]);
+                    xs[lt][lc + i] = v;
+                    ys[lt][lc + i] = in && n < N ? dy[t * lddy + n] : 0.0f;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < kStep; ++k) {
+                    const float4 a = *reinterpret_cast<const float4*>(&xs[k][4 * ty]);
+                    const float4 b = *reinterpret_cast<const float4*>(&ys[k][4 * tx]);
+                    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+                }
+                __syncthreads();
             }
-            __syncthreads();
 #pragma unroll
-            for (int k = 0; k < kStep; ++k) {
-                const float4 a = *reinterpret_cast<const float4*>(&xs[k][4 * ty]);
-                const float4 b = *reinterpret_cast<const float4*>(&ys[k][4 * tx]);
-                const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-            }
-            __syncthreads();
+                for (int j = 0; j < 4; ++j) sum[i][j] += acc[i][j];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            const long long d = d0 + 4 * ty + i;
+            if (d >= cols) break;
+            float* row = dw + d * lddw;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[i][j] += acc[i][j];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = d0 + 4 * ty + i;
-        if (d >= cols) break;
-        float* row = dw + static_cast<long long>(d) * lddw;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + 4 * tx + j;
-            if (n < N) row[n] = scale1(sum[i][j], row + n, alpha, beta, mode);
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + 4 * tx + j;
+                if (n < N) row[n] = scale1(sum[i][j], row + n, alpha, beta, mode);
+            }
         }
-    }
     }
 }
 

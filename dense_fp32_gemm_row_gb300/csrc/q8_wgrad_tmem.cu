@@ -10,7 +10,9 @@
 // addition (an error of about 2^-24 * 0.7 of the sum, always towards zero),
 // so a tensor-memory sum covers one chunk of tokens and is then added, with
 // rounding, into fp32 registers.  (Two bf16 parts would leave 2^-17 of each
-// product; TF32 parts need two MMAs at half the rate.)
+// product; TF32 parts need two MMAs at half the rate.)  Parts of dY below
+// 2^-126 are at the tensor core's mercy; an infinity in dY leaves a NaN part,
+// as in the 3xTF32 kernels, so it comes back as NaN.
 //
 // Shape.  Both operands have the summed index, the token, as their slow
 // axis.  The MMA's A operand comes from tensor memory, one row per lane, and
@@ -284,13 +286,13 @@ q8_wgrad_sum_kernel(const float* __restrict__ parts, Q8WgradShare sh, float* __r
             first = q8_wgrad_run(sh, t * sh.stages);
             n = q8_wgrad_run(sh, (t + 1) * sh.stages - 1) - first + 1;
         }
+        pdl_wait();  // the partial sums: only indices before it
         if (n == 1) continue;  // written by its cluster
         int d0, n0;
         tile_at(sh, sh.whole + t, d0, n0);
         const int per = (n + Q - 1) / Q;
         const int i1 = n0 + col < N ? min(n, (q + 1) * per) : 0;
         const float* src = parts + static_cast<long long>(first + t) * kPart + col;
-        pdl_wait();  // the partial sums; only indices before it
         float4 sum[G];
         int row[G];
 #pragma unroll
@@ -795,13 +797,14 @@ cudaError_t launch_sum(const Q8WgradPairArgs& a, cudaStream_t s) {
     const bool quarters = a.share.runs >= 8LL * a.share.shared;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    cfg.gridDim = dim3(quarters ? C::TD : C::TD / (4 * kSumRows), a.share.shared < 65535 ? a.share.shared : 65535);
+    cfg.gridDim = dim3(quarters ? C::TD : C::TD / (4 * kSumRows),
+                       a.share.shared < 65535 ? a.share.shared : 65535);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(
-        &cfg, quarters ? q8_wgrad_sum_kernel<4, 1, 8> : q8_wgrad_sum_kernel<1, kSumRows, 4>,
+        &cfg, quarters ? q8_wgrad_sum_kernel<4, 1, 10> : q8_wgrad_sum_kernel<1, kSumRows, 4>,
         static_cast<const float*>(a.parts), a.share, a.dw, a.lddw, vec, a.cols, a.N, a.alpha,
         a.beta, a.mode);
     return e != cudaSuccess ? e : cudaGetLastError();

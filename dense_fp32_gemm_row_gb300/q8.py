@@ -130,7 +130,7 @@ class Q8:
     that are multiples of 16.  ``format`` is "int8" or "e4m3".
     """
 
-    __slots__ = ("_codes", "_scales", "_buffer", "device", "rows", "cols", "format", "struct")
+    __slots__ = ("_codes", "_scales", "_buffer", "_at", "device", "rows", "cols", "format", "struct")
 
     def __init__(self, codes, scales, cols, format="int8"):
         torch = _torch or _load_torch()
@@ -144,7 +144,7 @@ class Q8:
         self.device = codes.get_device()
         if scales.get_device() != self.device:
             raise ValueError("codes and scales must be on one device")
-        self._codes, self._scales, self._buffer = codes, scales, None
+        self._codes, self._scales, self._buffer, self._at = codes, scales, None, 0
         self.rows, self.cols, self.format = rows, cols, format
 
     @property
@@ -152,15 +152,16 @@ class Q8:
         """The code bytes, (rows, cols rounded up to 16) for a checkpoint made here."""
         if self._codes is None:
             ld = self.struct.ldcodes
-            self._codes = self._buffer[:self.rows * ld].view(self.rows, ld)
+            self._codes = self._buffer[self._at:self._at + self.rows * ld].view(self.rows, ld)
         return self._codes
 
     @property
     def scales(self):
         """The exponent bytes, one for each block of 32 columns."""
         if self._scales is None:
-            s = self.struct
-            self._scales = self._buffer[self.rows * s.ldcodes:].view(self.rows, s.ldscales)
+            ld = self.struct.ldscales
+            at = self._at + self.rows * self.struct.ldcodes
+            self._scales = self._buffer[at:at + self.rows * ld].view(self.rows, ld)
         return self._scales
 
     @property
@@ -198,6 +199,7 @@ def _make(device, rows, cols, format, fmt) -> Q8:
     q = Q8.__new__(Q8)
     ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
     q._buffer = buf = _torch.empty(rows * (ldc + lds), dtype=_torch.uint8, device=device)
+    q._at = 0
     base = buf.data_ptr()
     q.struct = Q8Struct(base, base + rows * ldc, ldc, lds, rows, cols, fmt)
     q._codes = q._scales = None
@@ -206,6 +208,21 @@ def _make(device, rows, cols, format, fmt) -> Q8:
     q.cols = cols
     q.format = format
     return q
+
+
+def _make_two(device, rows, cols, format, fmt):
+    """Two uninitialised checkpoints of one shape, kept for one backward pass, in one buffer."""
+    a, b = Q8.__new__(Q8), Q8.__new__(Q8)
+    ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
+    one = rows * (ldc + lds)
+    both = _torch.empty(2 * one, dtype=_torch.uint8, device=device)
+    base = both.data_ptr()
+    for q, at in ((a, 0), (b, one)):
+        q._buffer, q._at = both, at
+        q.struct = Q8Struct(base + at, base + at + rows * ldc, ldc, lds, rows, cols, fmt)
+        q._codes = q._scales = None
+        q.device, q.rows, q.cols, q.format = device, rows, cols, format
+    return a, b
 
 
 def _floats(rows, cols, device):
@@ -377,10 +394,13 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
         h, ldh = _floats(rows, cols, device), cols or 1
     else:
         h, ldh = out, _like(out, rows, cols, device, "out")
-    gq = _make(device, rows, cols, format, fmt) if gate_q is None else _given(
-        gate_q, rows, cols, format, device, "gate_q")
-    uq = _make(device, rows, cols, format, fmt) if up_q is None else _given(
-        up_q, rows, cols, format, device, "up_q")
+    if gate_q is None and up_q is None:
+        gq, uq = _make_two(device, rows, cols, format, fmt)
+    else:
+        gq = _make(device, rows, cols, format, fmt) if gate_q is None else _given(
+            gate_q, rows, cols, format, device, "gate_q")
+        uq = _make(device, rows, cols, format, fmt) if up_q is None else _given(
+            up_q, rows, cols, format, device, "up_q")
     st = gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(), ldh,
                            gq.struct, uq.struct, _stream_of(device))
     if st:

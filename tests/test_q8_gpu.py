@@ -627,3 +627,49 @@ def test_binding_refuses():
         g.q8_gated(x, x.clone(), out=x)
     with pytest.raises(g.GemmError):
         g.q8_gated_backward(q, g.q8_store(x), x, h_q=q)
+
+
+def test_checkpoints_made_together_are_apart():
+    """The two checkpoints of a gated unit share one allocation: their bytes must not."""
+    torch = t()
+    gate, up = torch.randn(5, 70, device="cuda"), torch.randn(5, 70, device="cuda")
+    _, gq, uq = g.q8_gated(gate, up)
+    assert gq.codes.shape == uq.codes.shape == (5, 80) and gq.scales.shape == (5, 16)
+    for q, x in ((gq, gate), (uq, up)):
+        assert torch.equal(g.q8_restore(q), g.q8_restore(g.q8_store(x)))
+        again = g.Q8(q.codes, q.scales, 70)
+        assert torch.equal(g.q8_restore(again), g.q8_restore(q))
+
+
+@pytest.mark.parametrize("kind,status", [(g.INJECT_WORKSPACE, g.ERR_WORKSPACE),
+                                         (g.INJECT_DESCRIPTOR, g.ERR_DESCRIPTOR)])
+def test_wgrad_reports_a_host_failure_and_recovers(kind, status):
+    """A workspace that cannot be had, a descriptor that is refused: the status, dW as it was."""
+    torch = t()
+    q, x, dy = wgrad_case(np.random.default_rng(1), 4096, 300, 300, "int8")  # shares its tiles
+    dev, _ = matrix(dy)
+    out = torch.full((300, 300), 7.0, device="cuda")
+    g.check(g.gemm_f32_release())
+    g.gemm_f32_inject_host_fault(kind)
+    with pytest.raises(g.GemmError) as e:
+        g.q8_wgrad(q, dev, out=out)
+    assert e.value.status == status
+    assert bool((out == 7.0).all())
+    assert_wgrad(g.q8_wgrad(q, dev, out=out), x, dy)
+
+
+def test_wgrad_needs_its_workspace_before_a_capture():
+    torch = t()
+    q, x, dy = wgrad_case(np.random.default_rng(1), 4096, 300, 300, "int8")
+    dev, _ = matrix(dy)
+    out = torch.empty(300, 300, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g.check(g.gemm_f32_release())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        st = g.gemm_f32_q8_wgrad(q.struct, dev.data_ptr(), 300, 300, 1.0, 0.0, out.data_ptr(), 300,
+                                 stream=torch.cuda.current_stream().cuda_stream)
+        out.zero_()  # a graph of something
+    assert st == g.ERR_CAPTURE
+    assert_wgrad(g.q8_wgrad(q, dev), x, dy)
