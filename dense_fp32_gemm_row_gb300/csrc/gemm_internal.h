@@ -229,7 +229,8 @@ struct Q8WgradArgs {
     int mode;  // epilogue.cuh
 };
 cudaError_t launch_q8_wgrad_ffma(const Q8WgradArgs& a, cudaStream_t s);
-// The tensor-core form: CTA pairs, 256 x 256 tiles.  tmC is the codes as
+// The tensor-core form: CTA pairs with tiles of 256 features x 256 columns, or
+// (pair = 0) single CTAs with 256 x 128.  tmC is the codes as
 // {cols, T} bytes, box 128 x 32; tmS the exponents as {ceil(cols / 32), T}
 // bytes, box 16 x 32; dY is tmY.map[0], {N, T} floats, box 128 x 32, where its
 // rows start on 16-byte boundaries.  Otherwise (shifted) map[c] holds rows c,
@@ -242,7 +243,7 @@ struct Q8WgradMaps {
 struct Q8WgradTile {
     int features, columns, tokens;  // of a tile; of a pipeline stage
 };
-Q8WgradTile q8_wgrad_tile();
+Q8WgradTile q8_wgrad_tile(bool pair);
 // How the tiles are shared out: the first `whole` are a unit each; the stages
 // of the `shared` ones behind them, laid end to end, are cut into `runs`, a
 // unit each.  They are cut group by group, of group_stages stages (one tile's,
@@ -272,8 +273,9 @@ Q8_HOST_DEVICE inline int q8_wgrad_run(const Q8WgradShare& s, int stage) {
     return g * s.group_runs + j;
 }
 // bytes of the partial sums
-size_t q8_wgrad_parts_bytes(const Q8WgradShare& s);
-struct Q8WgradPairArgs {
+size_t q8_wgrad_parts_bytes(const Q8WgradShare& s, bool pair);
+struct Q8WgradTmemArgs {
+    int pair;
     Q8WgradMaps tmY;
     CUtensorMap tmC, tmS;
     int shifted;
@@ -289,7 +291,7 @@ struct Q8WgradPairArgs {
     float alpha, beta;
     int mode;
 };
-cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count);
+cudaError_t launch_q8_wgrad_tmem(const Q8WgradTmemArgs& a, cudaStream_t s, int dev, int sm_count);
 
 // ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------
 // Device look-up and set-up, workspace and descriptors are one library-wide

@@ -112,16 +112,22 @@ Q8Out out_of(const gemm_f32_q8* q) { return {q->codes, q->scales, q->ldcodes, q-
 long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
 
 // The tensor-core weight gradient's times in microseconds, fitted to calls
-// with both forms forced (a stage is 32 tokens of a tile): a stage of clusters
-// that run through the tokens side by side and share operands in L2; of
-// clusters that are all at different tokens, with operands that fit L2 and
-// beyond it; the second kernel, and writing and adding one partial sum.
+// with each choice forced (a stage is 32 tokens of a tile): what a call takes
+// more than one of single CTAs; a stage of units that run through the tokens side by side and share operands in L2; of units
+// that are all at different tokens, with operands that fit L2 and beyond it;
+// the second kernel, and writing and adding one partial sum.
 // Measured, shared against whole: 4096 x 1280 x 2048 (40 tiles on 76 pairs)
 // 55.4 against 75.5 us, 4096 x 1536 x 2304 (54) 70.4 against 76.2, 4096 x 2048
 // x 2048 (64) 79.3 against 76.5, 16384 x 1280 x 2048 178 against 275, 16384 x
-// 2048 x 2048 287 against 277.
-constexpr double kWgradStageUs = 0.53, kWgradApartUs = 0.57, kWgradFarUs = 0.65;
-constexpr double kWgradSumUs = 4.0, kWgradPartUs = 0.05;
+// 2048 x 2048 287 against 277.  Single CTAs against pairs: 8192 x 8192 x 8192
+// 2.18 against 1.96 ms, 4096 x 2048 x 2048 83 against 76 us, 16384 x 8192 x 32
+// 82 against 149, 8192 x 4096 x 384 63 against 75, 64 x 512 x 512 7.0 against
+// 7.6.
+struct WgradTimes {
+    double more, stage, apart, far, sum, part;
+};
+constexpr WgradTimes kWgradPair = {1.5, 0.53, 0.57, 0.65, 4.4, 0.06};
+constexpr WgradTimes kWgradSingle = {0.0, 0.59, 0.62, 0.70, 4.0, 0.02};
 constexpr double kWgradL2Bytes = 64e6;
 // what sharing has to save of the whole call: back to back the largest calls
 // are at the power limit and gain nothing from a shorter last round (8192 x
@@ -134,13 +140,13 @@ constexpr double kWgradLeastGain = 0.05;
 // x 8192, 512 tokens, 1.4e-6, 0.8 % faster.
 constexpr int kWgradChunk = 8;
 
-// The CUDA-core kernel, which has no pipeline to fill, for a few tokens and
-// small outputs (measured, against the tensor-core kernel, in microseconds:
-// 16 x 512 x 512 5.8 and 7.3, 16 x 1024 x 1024 5.9 and 7.4, 32 x 512 x 512 6.2
-// and 7.3; but 64 x 64 x 64 8.2 and 6.8, 32 x 2048 x 2048 18.4 and 8.9, 8 x
-// 8192 x 8192 115 and 50).
+// The CUDA-core kernel, which has no pipeline to fill and no descriptors, for
+// a few tokens and small outputs (measured, against the tensor-core kernel's
+// single CTAs, in microseconds: 16 x 512 x 512 5.6 and 6.3, 16 x 1024 x 1024
+// 5.7 and 6.6, 32 x 512 x 512 5.6 and 6.3, 24 x 300 x 300 6.1 and 6.8; but 4 x
+// 2048 x 2048 10.5 and 8.1, 64 x 512 x 512 8.3 and 7.0, 64 x 64 x 64 8.2 and 6).
 constexpr int kFfmaTokens = 32;
-constexpr double kFfmaProducts = 2e7;
+constexpr double kFfmaOutputs = 1 << 20, kFfmaProducts = 1.7e7;
 
 // Shares out the last `shared` tiles in groups of `group` tiles, `runs` a group.
 void cut_tiles(Q8WgradShare* s, int shared, int group, int runs) {
@@ -153,20 +159,25 @@ void cut_tiles(Q8WgradShare* s, int shared, int group, int runs) {
     s->runs = shared / group * runs;
 }
 
-// How the tiles of a weight gradient are shared out over the CTA pairs.
-// Requested splits: every tile in that many runs.  Otherwise whole tiles for
-// as many rounds as they fill, and the rest shared by all pairs where that
-// shortens the last round by more than the partial sums cost.
-Q8WgradShare share_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
-    const Q8WgradTile tile = q8_wgrad_tile();
+// How the tiles of a weight gradient are shared out over the CTA pairs, or the
+// single CTAs, and the time that should take.  Requested splits: every tile in
+// that many runs.  Otherwise whole tiles for as many rounds as they fill, and
+// the rest shared by all units where that shortens the last round by more than
+// the partial sums cost.
+Q8WgradShare share_wgrad(const Q8WgradArgs& a, bool pair, int splits, int sm_count, double* us) {
+    const Q8WgradTile tile = q8_wgrad_tile(pair);
+    const WgradTimes& time = pair ? kWgradPair : kWgradSingle;
     Q8WgradShare s = {};
     s.tiles_d = (a.cols - 1) / tile.features + 1;
     s.tiles_n = (a.N - 1) / tile.columns + 1;
     s.stages = (a.rows - 1) / tile.tokens + 1;
     s.whole = s.tiles_d * s.tiles_n;
-    const int pairs = sm_count / 2;
-    const int rest = splits > 0 ? s.whole : s.whole % pairs;
+    const int units = pair ? sm_count / 2 : sm_count;
+    const int rounds = (s.whole - 1) / units + 1;
+    const int rest = splits > 0 ? s.whole : s.whole % units;
     const long long all = static_cast<long long>(rest) * s.stages;
+    const double whole_us = time.stage * s.stages;
+    *us = time.more + whole_us * rounds;
     if (all == 0 || all > std::numeric_limits<int>::max()) return s;
     if (splits > 0) {
         const int n = splits < s.stages ? splits : s.stages;
@@ -174,32 +185,32 @@ Q8WgradShare share_wgrad(const Q8WgradArgs& a, int splits, int sm_count) {
         return s;
     }
     // the same number of runs for every tile, which start side by side; or as
-    // many as there are pairs, over tile boundaries
-    const double whole_us = kWgradStageUs * s.stages;
-    const double least = whole_us * (1.0 - kWgradLeastGain * ((s.whole - 1) / pairs + 1));
-    const int each = std::min(pairs / rest, s.stages / 4);
-    const int through = static_cast<int>(std::min<long long>(pairs, all / 4));
+    // many as there are units, over tile boundaries
+    const double least = whole_us * (1.0 - kWgradLeastGain * rounds);
+    const int each = std::min(units / rest, s.stages / 4);
+    const int through = static_cast<int>(std::min<long long>(units, all / 4));
     double each_us = whole_us, through_us = whole_us;
     if (each > 1)
-        each_us = kWgradStageUs * ((s.stages - 1) / each + 1) + kWgradSumUs +
-                  kWgradPartUs * each * rest;
+        each_us = time.stage * ((s.stages - 1) / each + 1) + time.sum + time.part * each * rest;
     if (through > rest) {
         const bool far = a.rows * (4.0 * a.N + a.cols) > kWgradL2Bytes;
-        through_us = (far ? kWgradFarUs : kWgradApartUs) *
-                         static_cast<double>((all - 1) / through + 1) +
-                     kWgradSumUs + kWgradPartUs * (through + rest);
+        through_us = (far ? time.far : time.apart) * static_cast<double>((all - 1) / through + 1) +
+                     time.sum + time.part * (through + rest);
     }
-    if (each_us < least && each_us <= through_us)
+    if (each_us < least && each_us <= through_us) {
         cut_tiles(&s, rest, 1, each);
-    else if (through_us < least)
+        *us += each_us - whole_us;
+    } else if (through_us < least) {
         cut_tiles(&s, rest, rest, through);
+        *us += through_us - whole_us;
+    }
     return s;
 }
 
 // The tensor maps of dY (rows x N, row stride ld): see q8_wgrad_tmem.cu.
-int map_dy(const float* dy, long long ld, int rows, int N, Q8WgradPairArgs* k) {
-    const Q8WgradTile tile = q8_wgrad_tile();
-    const int box = tile.columns / 2;
+int map_dy(const float* dy, long long ld, int rows, int N, Q8WgradTmemArgs* k) {
+    const Q8WgradTile tile = q8_wgrad_tile(false);
+    const int box = tile.columns;
     const uintptr_t base = reinterpret_cast<uintptr_t>(dy);
     if (rows == 1) ld = round_up(N, 4);  // never used
     if (base % 16 == 0 && ld % 4 == 0)
@@ -326,7 +337,8 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
                       cudaStream_t stream) {
     Q8_TRY(check_shape(x));
     if (N < 0 || splits < 0 || splits > GEMM_F32_MAX_SPLITS) return GEMM_F32_ERR_INVALID_VALUE;
-    if (algo != GEMM_F32_ALGO_AUTO && algo != GEMM_F32_ALGO_FFMA && algo != GEMM_F32_ALGO_3XBF16)
+    if (algo != GEMM_F32_ALGO_AUTO && algo != GEMM_F32_ALGO_FFMA &&
+        (algo < GEMM_F32_ALGO_3XBF16 || algo > GEMM_F32_ALGO_3XBF16_SINGLE))
         return GEMM_F32_ERR_INVALID_VALUE;
     if (x->cols == 0 || N == 0) return GEMM_F32_SUCCESS;
     // more tiles of dW than an index holds: no memory does either
@@ -347,20 +359,27 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     Q8WgradArgs a = {in_of(x), dY, dW, lddy, lddw, x->rows, x->cols, N, x->format, alpha, beta,
                      beta != 0.0f ? 2 : alpha == 1.0f ? 0 : 1};
     if (algo == GEMM_F32_ALGO_AUTO)
-        algo = x->rows <= kFfmaTokens && 1.0 * x->rows * x->cols * N <= kFfmaProducts
+        algo = x->rows <= kFfmaTokens && 1.0 * x->cols * N <= kFfmaOutputs &&
+                       1.0 * x->rows * x->cols * N <= kFfmaProducts
                    ? GEMM_F32_ALGO_FFMA
                    : GEMM_F32_ALGO_3XBF16;
     if (algo == GEMM_F32_ALGO_FFMA) return status(launch_q8_wgrad_ffma(a, stream));
 
-    const Q8WgradTile tile = q8_wgrad_tile();
-    Q8WgradPairArgs k = {};
-    k.share = share_wgrad(a, splits, c.sm_count);
+    const Q8WgradTile tile = q8_wgrad_tile(false);
+    Q8WgradTmemArgs k = {};
+    double pair_us, single_us;
+    k.share = share_wgrad(a, true, splits, c.sm_count, &pair_us);
+    const Q8WgradShare single = share_wgrad(a, false, splits, c.sm_count, &single_us);
+    k.pair = algo == GEMM_F32_ALGO_3XBF16 ? pair_us <= single_us
+                                          : algo == GEMM_F32_ALGO_3XBF16_PAIR;
+    if (!k.pair) k.share = single;
     unsigned char* ws = nullptr;
     if (k.share.shared)
-        Q8_TRY(call_workspace(c, stream, kWorkspaceCounterBytes + q8_wgrad_parts_bytes(k.share), &ws));
+        Q8_TRY(call_workspace(
+            c, stream, kWorkspaceCounterBytes + q8_wgrad_parts_bytes(k.share, k.pair), &ws));
     Q8_TRY(map_dy(dY, lddy, x->rows, N, &k));
     Q8_TRY(call_tensor_map(&k.tmC, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->codes, x->cols, x->rows,
-                           x->ldcodes, tile.features / 2, tile.tokens));
+                           x->ldcodes, 128, tile.tokens));
     Q8_TRY(call_tensor_map(&k.tmS, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->scales, blocks_of(x->cols),
                            x->rows, x->ldscales, 16, tile.tokens));
     k.dw = dW;
@@ -376,7 +395,7 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     k.alpha = alpha;
     k.beta = beta;
     k.mode = a.mode;
-    return status(launch_q8_wgrad_pair(k, stream, c.dev, c.sm_count));
+    return status(launch_q8_wgrad_tmem(k, stream, c.dev, c.sm_count));
 }
 
 }  // extern "C"

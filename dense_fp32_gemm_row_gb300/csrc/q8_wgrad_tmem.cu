@@ -23,21 +23,27 @@
 // are stored, so its decoder writes rows as it reads them.  D is the
 // transposed tile: lane n, column d.
 //
-// A cluster of two CTAs computes a tile of 256 features x 256 columns with
-// cta_group::2 MMAs (M = 256 columns n across the pair, N = 256 features, K =
-// 16 tokens), CTA rank r holding columns n0 + 128 r .. in its tensor memory
-// and features d0 + 128 r .. in its shared memory.  Per 16 tokens an SM's
-// tensor core works 3 x 128 cycles and reads 12 KB of shared memory, half
-// its share; dY in shared memory as well (both operands, three parts) would
-// take more than the whole.
+// Two forms.  A cluster of two CTAs computes a tile of 256 features x 256
+// columns with cta_group::2 MMAs (M = 256 columns n across the pair, N = 256
+// features, K = 16 tokens), CTA rank r holding columns n0 + 128 r .. in its
+// tensor memory and half of the features in its shared memory.  Per 16 tokens
+// an SM's tensor core works 3 x 128 cycles and reads 12 KB of shared memory,
+// half its share; dY in shared memory as well (both operands, three parts)
+// would take more than the whole.  Or one CTA computes 256 x 128 (M = 128) and
+// holds all the features: it decodes and reads twice as much of x^ for the
+// same MMAs (8192 x 8192 x 8192 2.14 ms against 1.89), but wastes less of them
+// on few or odd columns, is quicker to start, and has no partner to tell
+// (16384 x 8192 x 32 82 us against 149, 64 x 512 x 512 7.0 against 7.6).  In a
+// tile with fewer features the MMAs are as much narrower.
 //
 // 640 threads per CTA, registers rebalanced at start (launched at 96 each):
 //   warp 0       one lane: TMA loads of a 32-token stage (dY 128 columns x 32,
-//                codes 128 x 32, exponents 16 x 32), six stages deep;
-//   warp 1       tensor-memory allocation for the pair; in the leader one lane
+//                codes 128 x 32 once or twice, exponents 16 x 32), six stages
+//                deep (five in the single form);
+//   warp 1       tensor-memory allocation; one lane (of a pair: the leader's)
 //                issues the MMAs and commits;
-//   warps 1-3 of the peer  relay: one lane each tells the leader, in turn, that
-//                the peer's operands of a stage are written;
+//   warps 1-3 of a pair's peer  relay: one lane each tells the leader, in turn,
+//                that the peer's operands of a stage are written;
 //   warps 4-7    split dY into tensor memory (warp 4 + q: lanes 32 q ..);
 //   warps 8-11   decode x^ to bf16 in shared memory, eight tokens each;
 //   warps 12-19  per chunk add the accumulator (warp 12 + e: lanes 32 (e % 4)
@@ -49,17 +55,21 @@
 // rings, so that DRAM and L2 latency is not part of the operand loop (MMA,
 // commit, conversion, relay: ~1.5 us of the five stages' 2.0).
 //
-// What set the speed, 8192 x 8192 x 8192 (INT8): one relay lane for the peer,
-// whose release at cluster scope takes ~650 ns against 400 ns of MMAs a stage,
-// 2.69 ms; three relays and the separate rings 2.19; four decoder warps
-// instead of two, each of whose stores fills all banks, 1.89.  With operands
-// that are never rewritten the same MMAs and copies take 1.70 ms (three bf16
-// products at the burst rate of the library product: 1.72 ms; at its sustained
-// rate, which the power limit sets, 1.91).
+// What set the speed, 8192 x 8192 x 8192 (INT8), pairs: one relay lane for the
+// peer, whose release at cluster scope takes ~650 ns against 400 ns of MMAs a
+// stage, 2.69 ms; three relays and the separate rings 2.19; four decoder warps
+// instead of two, each of whose stores fills all banks, 1.89 (2.03 back to
+// back at the power limit).  With operands that are never rewritten the same
+// MMAs and copies take 1.70 ms; three bf16 products at the burst rate of the
+// library's product take 1.72, at its sustained rate 1.91.  4096 x 2048 x
+// 2048: 75.5 us, 64 tiles on 76 pairs, the tensor pipe busy 79 % of a CTA's
+// life, a stage 0.53 us.
 //
-// Where the tiles do not fill the clusters evenly, the last of them are shared:
+// Where the tiles do not fill the units evenly, the last of them are shared:
 // their stages, end to end, are cut into equal runs, whose partial sums a
-// second kernel adds in order.
+// second kernel adds in order.  (Adding them in this kernel, by CTAs that
+// wait for one another, took 1000 x 1024 x 1024 20.5 us against 15.2: the
+// second kernel starts as a programmatic dependent.)
 // Waits are bounded and wind down as in the GEMM kernels.
 #include <cstdint>
 
@@ -75,21 +85,26 @@ namespace {
 
 using namespace gemm_f32_dev;
 
+template <bool PAIR_>
 struct WgradCfg {
-    static constexpr int TD = 256, TN = 256;  // features, columns of a tile
-    static constexpr int HALF = 128;          // of each, per CTA
-    static constexpr int KT = 32;             // tokens a stage
-    static constexpr int UK = 16;             // tokens an MMA
-    static constexpr int RAW = 6;     // stages of copies
-    static constexpr int STAGES = 5;  // stages of MMA operands
-    static constexpr int XB_BYTES = HALF * KT * 2;   // x^ in bf16: two 64-feature groups
+    static constexpr bool PAIR = PAIR_;
+    static constexpr int CTAS = PAIR ? 2 : 1;
+    static constexpr int TD = 256, TN = 128 * CTAS;  // features, columns of a tile
+    static constexpr int CTA_D = TD / CTAS;          // per CTA: features in shared memory,
+    static constexpr int CTA_N = 128;                // columns in tensor-memory lanes
+    static constexpr int KT = 32;                    // tokens a stage
+    static constexpr int UK = 16;                    // tokens an MMA
+    static constexpr int RAW = PAIR ? 6 : 5;         // stages of copies
+    static constexpr int STAGES = 5;                 // stages of MMA operands
+    static constexpr int XB_BYTES = CTA_D * KT * 2;  // x^ in bf16: 64-feature groups
     static constexpr int GROUP_BYTES = 64 * KT * 2;  // rows of 128 bytes, a token each
-    static constexpr int Y_BYTES = HALF * KT * 4;
+    static constexpr int Y_BYTES = CTA_N * KT * 4;
     // dY by rows of one residue modulo 4, four columns wider (see the kernel)
-    static constexpr int SHIFT_PITCH = (HALF + 4) * 4;
+    static constexpr int SHIFT_PITCH = (CTA_N + 4) * 4;
     static constexpr int SHIFT_GROUP = KT / 4 * SHIFT_PITCH;
     static constexpr int Y_SLOT = 4 * SHIFT_GROUP;
-    static constexpr int C_BYTES = HALF * KT;
+    static constexpr int C_BOX_BYTES = 128 * KT;     // codes: boxes of 128 features
+    static constexpr int C_BYTES = CTA_D * KT;
     static constexpr int S_BYTES = 16 * KT;
     // the swizzled x^ stages first: each 1024-byte aligned
     static constexpr int Y_OFF = STAGES * XB_BYTES;
@@ -110,9 +125,8 @@ struct WgradCfg {
     static constexpr int REGS_LAUNCH = 96;
     static constexpr int REGS_CONTROL = 40, REGS_SPLIT = 48, REGS_DECODE = 56, REGS_EPI = 168;
     static constexpr int DRAIN_BATCH = 2;
-    // D fp32, A and B bf16, B with its N axis contiguous, M = 256, N = 256
+    // D fp32, A and B bf16, B with its N axis contiguous, M = TN; N is added
     static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
-                                      (static_cast<uint32_t>(TD >> 3) << 17) |
                                       (static_cast<uint32_t>(TN >> 4) << 24);
     static_assert(REGS_CONTROL + REGS_SPLIT + REGS_DECODE + 2 * REGS_EPI <= 5 * REGS_LAUNCH,
                   "register shares");
@@ -128,7 +142,7 @@ struct WgradCfg {
 __device__ __forceinline__ uint64_t xhat_desc(uint32_t addr) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(WgradCfg::GROUP_BYTES >> 4) << 16;
+    d |= static_cast<uint64_t>(WgradCfg<true>::GROUP_BYTES >> 4) << 16;
     d |= static_cast<uint64_t>(1024u >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
@@ -202,36 +216,55 @@ __device__ __forceinline__ void decode_bf16(uint32_t w, float scale, uint32_t& l
     hi = upper_halves(v.z * scale, v.w * scale);
 }
 
-__device__ __forceinline__ void mma_bf16_pair_tmem_a(uint32_t d_tmem, uint32_t a_tmem,
-                                                     uint64_t b_desc, uint32_t idesc,
-                                                     uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+// D += A B^T, A in tensor memory, for one CTA or (leader's thread) the pair.
+template <bool PAIR>
+__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// Arrival on a barrier, in both CTAs of a pair, when the MMAs so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (PAIR)
+        mma_commit_pair_multicast(bar, 0x3);
+    else
+        mma_commit(bar);
 }
 
 // First feature and column of a tile: neighbouring tiles run down groups of 8
 // rows of tiles, so that the clusters at work share operands in L2.
+template <class C>
 __device__ __forceinline__ void tile_at(const Q8WgradShare& sh, int tile, int& d0, int& n0) {
     const int per_group = GROUP_M * sh.tiles_n;
     const int group = tile / per_group, within = tile - group * per_group;
     const int rows = min(sh.tiles_d - group * GROUP_M, GROUP_M);
     const int column = within / rows;
-    d0 = (group * GROUP_M + within - column * rows) * WgradCfg::TD;
-    n0 = column * WgradCfg::TN;
+    d0 = (group * GROUP_M + within - column * rows) * C::TD;
+    n0 = column * C::TN;
 }
 
-// The work of one cluster, piece by piece: a whole tile, or a run of stages of
+// The work of one cluster (or CTA), piece by piece: a whole tile, or a run of stages of
 // a shared tile.  A run may cover parts of several tiles; a part of a tile goes to slot (run + tile) of the partial sums, so that the slots of
 // one tile follow one another in the order of its stages.
+template <class C>
 struct Pieces {
     int u;          // next unit
     int run, b, e;  // the current run, its stages left
 
-    __device__ __forceinline__ Pieces() : u(blockIdx.x >> 1), run(0), b(0), e(0) {}
+    __device__ __forceinline__ Pieces() : u(blockIdx.x / C::CTAS), run(0), b(0), e(0) {}
 
     __device__ __forceinline__ bool next(const Q8WgradShare& sh, Unit& w) {
         int tile = u;
@@ -245,7 +278,7 @@ struct Pieces {
                 b = q8_wgrad_cut(sh, run);
                 e = q8_wgrad_cut(sh, run + 1);
             }
-            u += gridDim.x >> 1;
+            u += gridDim.x / C::CTAS;
         }
         if (b < e) {
             const int t = b / sh.stages;
@@ -255,7 +288,7 @@ struct Pieces {
             b += w.nkb;
             if (w.nkb < sh.stages) w.slot = run + t;
         }
-        tile_at(sh, tile, w.m0, w.n0);
+        tile_at<C>(sh, tile, w.m0, w.n0);
         return true;
     }
 };
@@ -263,22 +296,22 @@ struct Pieces {
 // Adds the partial sums of the shared tiles, in the order of their stages, and
 // writes dW, 256 threads a block.
 //   Q = 1: a thread adds four columns of G rows at once, B partials of each in
-//   flight, and a block takes 4 G rows of a tile;
+//   flight;
 //   Q = 4: for few outputs with many partials, each bound by the latency of
 //   its loads: four lanes share a group of four columns, each adding a
 //   contiguous quarter of the partials, B in flight, and their sums are added
-//   in order; a block takes one row of a tile.
-template <int Q, int G, int B>
+//   in order.
+template <class C, int Q, int G, int B>
 __global__ void __launch_bounds__(256)
 q8_wgrad_sum_kernel(const float* __restrict__ parts, Q8WgradShare sh, float* __restrict__ dw,
                     long long lddw, bool vec, int D, int N, float alpha, float beta, int mode) {
-    using C = WgradCfg;
     constexpr int kPart = C::TD * C::TN;
+    constexpr int kRows = 256 / Q / (C::TN / 4);  // of a block, in each of G passes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int q = Q == 1 ? 0 : lane / (32 / Q);
     const int group = warp * (32 / Q) + lane % (32 / Q);  // of 256 / Q groups of four columns
     const int col = 4 * (group % (C::TN / 4));
-    const int row0 = (256 / Q / (C::TN / 4)) * G * static_cast<int>(blockIdx.x) + group / (C::TN / 4);
+    const int row0 = kRows * G * static_cast<int>(blockIdx.x) + group / (C::TN / 4);
     for (int t = blockIdx.y; t < sh.shared; t += gridDim.y) {
         // the runs that hold the tile's first and last stage
         int first = t * sh.group_runs, n = sh.group_runs;
@@ -289,7 +322,7 @@ q8_wgrad_sum_kernel(const float* __restrict__ parts, Q8WgradShare sh, float* __r
         pdl_wait();  // the partial sums: only indices before it
         if (n == 1) continue;  // written by its cluster
         int d0, n0;
-        tile_at(sh, sh.whole + t, d0, n0);
+        tile_at<C>(sh, sh.whole + t, d0, n0);
         const int per = (n + Q - 1) / Q;
         const int i1 = n0 + col < N ? min(n, (q + 1) * per) : 0;
         const float* src = parts + static_cast<long long>(first + t) * kPart + col;
@@ -298,7 +331,7 @@ q8_wgrad_sum_kernel(const float* __restrict__ parts, Q8WgradShare sh, float* __r
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             sum[g] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            row[g] = row0 + g * (256 / Q / (C::TN / 4));
+            row[g] = row0 + g * kRows;
         }
         for (int i0 = q * per; i0 < i1; i0 += B) {
             float4 v[G][B];
@@ -352,6 +385,15 @@ __device__ __forceinline__ void store_columns(const float (&acc)[EPI_COLS], floa
     }
 }
 
+// Features that each CTA holds of a tile with `left` features from its first
+// to the last of x: all of them, or in a matrix's last tiles as few blocks of
+// 32 as cover the rest, so that the MMAs are no wider than they need to be.
+template <class C>
+__device__ __forceinline__ int cta_features(int left) {
+    const int each = (left + C::CTAS - 1) / C::CTAS;
+    return min(C::CTA_D, (each + 31) & ~31);
+}
+
 // SHIFTED: rows of dY that do not start on 16-byte boundaries, as TMA loads
 // must.  Four row strides are a multiple of 16 bytes whatever the stride, so
 // the rows t = 4 i + c of each residue c form a matrix that a tensor map can
@@ -359,15 +401,15 @@ __device__ __forceinline__ void store_columns(const float (&acc)[EPI_COLS], floa
 // columns then lie shifts[c] (0 .. 3 floats, two bits each) further right, and
 // a box four columns wider holds the tile's.  Such a stage is four boxes of 8
 // rows, and the splitter adds the shift; no padded copy of dY is made.
-template <int FMT, bool SHIFTED>
-__global__ void __launch_bounds__(WgradCfg::THREADS, 1)
-q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
+template <bool PAIR, int FMT, bool SHIFTED>
+__global__ void __launch_bounds__(WgradCfg<PAIR>::THREADS, 1)
+q8_wgrad_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                      const __grid_constant__ CUtensorMap tmC,
                      const __grid_constant__ CUtensorMap tmS, float* __restrict__ dw,
                      long long lddw, float* __restrict__ parts, int D, int N, int T,
                      Q8WgradShare share, int chunk, unsigned* fault, long long timeout_ns,
                      float alpha, float beta, int scale_mode) {
-    using C = WgradCfg;
+    using C = WgradCfg<PAIR>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -378,14 +420,14 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
     const uint32_t empty0 = free0 + 8 * C::RAW;     // own, multicast commit: operands read
     const uint32_t ready0 = empty0 + 8 * STAGES;    // operands written
     const uint32_t accf = ready0 + 8 * STAGES;      // own, multicast commit
-    const uint32_t acce = accf + 8;                 // leader: 8 warps x 2 CTAs
+    const uint32_t acce = accf + 8;                 // leader: 8 warps a CTA
     const uint32_t drain = acce + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + C::NBARS * 8);
     const uint32_t abort_flag = smem_addr(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0;
 
     if (threadIdx.x == 0) {
         for (int c = 0; c < (SHIFTED ? 4 : 1); ++c) prefetch_tmap(&tmY.map[c]);
@@ -398,34 +440,42 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(empty0 + 8 * s, 1);
             // in the leader also the relay of the peer's
-            mbar_init(ready0 + 8 * s, C::CONV_WARPS + (rank == 0 ? 1 : 0));
+            mbar_init(ready0 + 8 * s, C::CONV_WARPS + (PAIR && rank == 0 ? 1 : 0));
         }
         mbar_init(accf, 1);
-        mbar_init(acce, 2 * C::EPI_WARPS);
+        mbar_init(acce, C::CTAS * C::EPI_WARPS);
         mbar_init(drain, 1);
         st_shared_volatile(abort_flag, 0u);
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_addr(tmem_slot), C::TMEM_COLS);
-        tmem_relinquish_pair();
+        if (PAIR) {
+            tmem_alloc_pair(smem_addr(tmem_slot), C::TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_addr(tmem_slot), C::TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    cluster_sync();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
     pdl_trigger();
 
     // The peer's arrivals on its ready barriers, passed on to the leader's: relay
-    // i of kRelays takes every kRelays-th stage.  A release at cluster scope
+    // i of RELAYS takes every RELAYS-th stage.  A release at cluster scope
     // takes ~650 ns on this part, more than the MMAs of a stage (400 ns), so
     // several warps have one each in flight.
     auto relay = [&](int i) {
         const uint32_t ready_leader = map_to_cta(ready0, 0);
         int total = 0;
         Unit w;
-        for (Pieces todo; todo.next(share, w);) total += w.nkb;
+        for (Pieces<C> todo; todo.next(share, w);) total += w.nkb;
         for (int it = i; it < total; it += C::RELAYS) {
             const int s = it % STAGES;
             if (!role_wait(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault, kFaultFullBarrier,
@@ -439,14 +489,14 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         regs_dec<C::REGS_CONTROL>();
         if (warp == 0) {
             if (lane == 0) {
-                // -------------------------- TMA producer (both CTAs) ------------------
+                // -------------------------- TMA producer ------------------------------
                 int it = 0;
                 bool ok = true;
                 Unit w;
-                    for (Pieces todo; ok && todo.next(share, w);) {
-                    const int dc = w.m0 + static_cast<int>(rank) * C::HALF;
-                    const int nc = w.n0 + static_cast<int>(rank) * C::HALF;
-                    // exponents: the aligned 16 blocks that hold this CTA's four
+                for (Pieces<C> todo; ok && todo.next(share, w);) {
+                    const int dc = w.m0 + static_cast<int>(rank) * cta_features<C>(D - w.m0);
+                    const int nc = w.n0 + static_cast<int>(rank) * C::CTA_N;
+                    // exponents: the aligned 16 blocks that hold this CTA's
                     const int bc = (dc / kQ8Block) & ~15;
                     for (int kb = 0; kb < w.nkb; ++kb, ++it) {
                         const int r = it % C::RAW;
@@ -470,7 +520,10 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                         } else {
                             tma_load_2d(yb, &tmY.map[0], fb, nc, t0);
                         }
-                        tma_load_2d(sbase + C::C_OFF + r * C::C_BYTES, &tmC, fb, dc, t0);
+#pragma unroll
+                        for (int c = 0; c < C::CTA_D / 128; ++c)
+                            tma_load_2d(sbase + C::C_OFF + r * C::C_BYTES + c * C::C_BOX_BYTES, &tmC,
+                                        fb, dc + 128 * c, t0);
                         tma_load_2d(sbase + C::S_OFF + r * C::S_BYTES, &tmS, fb, bc, t0);
                     }
                 }
@@ -485,14 +538,17 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
             __syncwarp();
         } else if (warp == 1) {
             if (lane == 0 && rank == 0) {
-                // -------------------------- MMA issuer (leader) -----------------------
+                // -------------------------- MMA issuer (of a pair: the leader) --------
                 int it = 0;
                 int g = 0;  // chunks issued
                 bool ok = true;
                 Unit w;
-                    for (Pieces todo; ok && todo.next(share, w);) {
+                for (Pieces<C> todo; ok && todo.next(share, w);) {
+                    const uint32_t idesc =
+                        C::IDESC |
+                        static_cast<uint32_t>(C::CTAS * cta_features<C>(D - w.m0) / 8) << 17;
                     for (int c0 = 0; c0 < w.nkb && ok; c0 += chunk, ++g) {
-                        // the single accumulator: both epilogues have drained chunk g - 1
+                        // the single accumulator: chunk g - 1 has been drained
                         if (g >= 1 && !role_wait(acce, (g - 1) & 1, timeout_ns, fault,
                                                  kFaultAccumBarrier, abort_flag)) {
                             ok = false;
@@ -502,8 +558,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                         const int c1 = min(w.nkb, c0 + chunk);
                         for (int kb = c0; kb < c1; ++kb, ++it) {
                             const int s = it % STAGES;
-                            if (!role_wait<true>(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns, fault,
-                                           kFaultFullBarrier, abort_flag)) {
+                            if (!role_wait<PAIR>(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns,
+                                                 fault, kFaultFullBarrier, abort_flag)) {
                                 ok = false;
                                 break;
                             }
@@ -518,29 +574,32 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                                 const uint64_t xk = x + static_cast<uint64_t>((k * C::UK * 128) >> 4);
                                 const uint32_t kc = static_cast<uint32_t>(k * C::UK / 2);
                                 const uint32_t acc = (kb > c0 || k > 0) ? 1u : 0u;
-                                mma_bf16_pair_tmem_a(tmem_base, b2 + kc, xk, C::IDESC, acc);
-                                mma_bf16_pair_tmem_a(tmem_base, b1 + kc, xk, C::IDESC, 1u);
-                                mma_bf16_pair_tmem_a(tmem_base, b0 + kc, xk, C::IDESC, 1u);
+                                mma_bf16_tmem_a<PAIR>(tmem_base, b2 + kc, xk, idesc, acc);
+                                mma_bf16_tmem_a<PAIR>(tmem_base, b1 + kc, xk, idesc, 1u);
+                                mma_bf16_tmem_a<PAIR>(tmem_base, b0 + kc, xk, idesc, 1u);
                             }
-                            mma_commit_pair_multicast(empty0 + 8 * s, 0x3);
+                            commit<PAIR>(empty0 + 8 * s);
                         }
                         if (!ok) break;
-                        mma_commit_pair_multicast(accf, 0x3);
+                        commit<PAIR>(accf);
                     }
                 }
-                mma_commit_pair(drain);
+                if (PAIR)
+                    mma_commit_pair(drain);
+                else
+                    mma_commit(drain);
                 mbar_wait(drain, 0, ok ? timeout_ns : timeout_ns / 8 + 1000, fault, kFaultDrain);
-            } else if (lane == 0) {
+            } else if (PAIR && lane == 0) {
                 relay(0);
             }
             __syncwarp();
-        } else if (rank == 1 && lane == 0) {
+        } else if (PAIR && rank == 1 && lane == 0) {
             // ------------------------------ relays (warps 2-3 of the peer) ------------
             relay(warp - 1);
         }
         __syncwarp();
     } else if (warp < 8) {
-        // ------------------------------ dY splitters (warps 4-7, both CTAs) -----------
+        // ------------------------------ dY splitters (warps 4-7) ----------------------
         regs_dec<C::REGS_SPLIT>();
         const int q = warp & 3;
         uint32_t at[4];  // SHIFTED: a residue's rows in a stage, and their shift
@@ -551,7 +610,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         int it = 0;
         bool ok = true;
         Unit w;
-            for (Pieces todo; ok && todo.next(share, w);) {
+        for (Pieces<C> todo; ok && todo.next(share, w);) {
+            const bool columns = w.n0 + static_cast<int>(rank) * C::CTA_N + 32 * q < N;
             for (int kb = 0; kb < w.nkb; ++kb, ++it) {
                 const int s = it % STAGES, raw = it % C::RAW;
                 bool got = role_wait(full0 + 8 * raw, (it / C::RAW) & 1, timeout_ns, fault,
@@ -569,15 +629,16 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                                      static_cast<uint32_t>(4 * (32 * q + lane));
                 const uint32_t col =
                     lane_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
-                // 16 tokens at a time: this warpgroup runs on 48 registers
+                // 16 tokens at a time: this warpgroup runs on 48 registers.  Lanes of
+                // columns beyond dY's last keep what they hold: no output reads them.
 #pragma unroll
-                for (int h = 0; h < C::KT / 16; ++h) {
+                for (int h = 0; h < (columns ? C::KT / 16 : 0); ++h) {
                     float y[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const uint32_t t = static_cast<uint32_t>(16 * h + i);
                         y[i] = lds_f32(SHIFTED ? src + at[i & 3] + (t >> 2) * C::SHIFT_PITCH
-                                               : src + t * (4 * C::HALF));
+                                               : src + t * (4 * C::CTA_N));
                     }
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
@@ -602,18 +663,21 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         }
         __syncwarp();
     } else if (warp < 12) {
-        // ------------------------------ x^ decoders (warps 8-11, both CTAs) -----------
-        // A lane takes eight codes of a token row: with 16 lanes a row, loads are
-        // 128 contiguous bytes, and each eight lanes store the eight 16-byte
-        // chunks of one row of one 64-feature group.
+        // ------------------------------ x^ decoders (warps 8-11) ----------------------
+        // A lane takes eight codes of a token row: 16 lanes load 128 contiguous
+        // bytes, and each eight lanes store the eight 16-byte chunks of one row of
+        // one 64-feature group.
         regs_dec<C::REGS_DECODE>();
-        const int c = lane & 15;
-        const int row0 = 8 * (warp - 8) + (lane >> 4);
+        constexpr int kRowLanes = C::CTA_D / 8;         // 16 or 32
+        constexpr int kStep = 32 / kRowLanes;           // rows a warp takes at once
+        constexpr int kItems = C::KT / 4 / kStep;       // 4 or 8
+        const int c = lane % kRowLanes;
+        const int row0 = C::KT / 4 * (warp - 8) + lane / kRowLanes;
         int it = 0;
         bool ok = true;
         Unit w;
-            for (Pieces todo; ok && todo.next(share, w);) {
-            const int dc = w.m0 + static_cast<int>(rank) * C::HALF;
+        for (Pieces<C> todo; ok && todo.next(share, w);) {
+            const int dc = w.m0 + static_cast<int>(rank) * cta_features<C>(D - w.m0);
             const uint32_t sc = static_cast<uint32_t>(((dc / kQ8Block) & 15) + (c >> 2));
             for (int kb = 0; kb < w.nkb; ++kb, ++it) {
                 const int s = it % STAGES, raw = it % C::RAW;
@@ -623,14 +687,15 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                     ok = false;
                     break;
                 }
-                const uint32_t codes = sbase + C::C_OFF + raw * C::C_BYTES + 8 * c;
+                const uint32_t codes = sbase + C::C_OFF + raw * C::C_BYTES +
+                                       (c >> 4) * C::C_BOX_BYTES + 8 * (c & 15);
                 const uint32_t exps = sbase + C::S_OFF + raw * C::S_BYTES + sc;
                 const uint32_t dst = sbase + s * C::XB_BYTES + (c >> 3) * C::GROUP_BYTES;
-                uint32_t q[4][2], ex[4];
+                uint32_t q[kItems][2], ex[kItems];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t r = static_cast<uint32_t>(row0 + 2 * i);
-                    lds_u32x2(codes + r * C::HALF, q[i]);
+                for (int i = 0; i < kItems; ++i) {
+                    const uint32_t r = static_cast<uint32_t>(row0 + kStep * i);
+                    lds_u32x2(codes + r * 128u, q[i]);
                     ex[i] = lds_u8(exps + 16u * r);
                 }
                 if (it >= STAGES) {
@@ -642,8 +707,8 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t r = static_cast<uint32_t>(row0 + 2 * i);
+                for (int i = 0; i < kItems; ++i) {
+                    const uint32_t r = static_cast<uint32_t>(row0 + kStep * i);
                     uint32_t v[4];
                     const float scale = q8_scale<FMT>(ex[i]);
                     decode_bf16<FMT>(q[i][0], scale, v[0], v[1]);
@@ -661,20 +726,20 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         }
         __syncwarp();
     } else {
-        // ------------------------------ epilogue (warps 12-19, both CTAs) -------------
+        // ------------------------------ epilogue (warps 12-19) ------------------------
         regs_inc<C::REGS_EPI>();
         const int e = warp - 12;
         const int q = warp & 3;                  // lanes 32 q .. 32 q + 31
         const int col0 = (e >> 2) * EPI_COLS;    // accumulator columns: features
-        const int nl = static_cast<int>(rank) * C::HALF + 32 * q + lane;
-        const uint32_t acce_leader = map_to_cta(acce, 0);
+        const int nl = static_cast<int>(rank) * C::CTA_N + 32 * q + lane;
+        const uint32_t acce_leader = PAIR ? map_to_cta(acce, 0) : acce;
         const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                                static_cast<uint32_t>(col0);
         float acc[EPI_COLS];
         int g = 0;
         bool ok = true;
         Unit w;
-            for (Pieces todo; ok && todo.next(share, w);) {
+        for (Pieces<C> todo; ok && todo.next(share, w);) {
             for (int c0 = 0; c0 < w.nkb; c0 += chunk, ++g) {
                 const bool got = role_wait(accf, g & 1, timeout_ns, fault, kFaultAccumBarrier,
                                            abort_flag);
@@ -706,7 +771,12 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                 // the loads have completed: the arrival orders no writes
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(acce_leader);
+                if (lane == 0) {
+                    if (PAIR)
+                        mbar_arrive_remote(acce_leader);
+                    else
+                        mbar_arrive(acce);
+                }
             }
             if (!ok) break;
             const int n = w.n0 + nl;
@@ -732,103 +802,121 @@ q8_wgrad_pair_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         __syncwarp();
     }
 
-    // neither CTA may leave while its partner can still reach its shared or
-    // tensor memory
+    // neither CTA of a pair may leave while the other can still reach its shared
+    // or tensor memory
     tc_fence_before();
-    cluster_sync();
+    if (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
 }
 
 // Shared-memory attribute of the kernel on device `dev`, once (the ABI's
-// mutex is held).  The register rebalancing waits for ever unless the block
-// was launched with the whole register file, so a build in which the
-// compiler took fewer than 128 registers a thread is refused here.
-template <int FMT, bool SHIFTED>
+// mutex is held).  The register rebalancing would wait for ever for registers
+// that the block was not launched with, so a build in which the compiler took
+// fewer than REGS_LAUNCH a thread is refused here.
+template <bool PAIR, int FMT, bool SHIFTED>
 cudaError_t configure(int dev) {
+    using C = WgradCfg<PAIR>;
     constexpr int kDevices = 64;
     static bool done[kDevices] = {};
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, q8_wgrad_pair_kernel<FMT, SHIFTED>);
+    cudaError_t e = cudaFuncGetAttributes(&attr, q8_wgrad_kernel<PAIR, FMT, SHIFTED>);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs < WgradCfg::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(q8_wgrad_pair_kernel<FMT, SHIFTED>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, WgradCfg::SMEM_BYTES);
+    if (attr.numRegs < C::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(q8_wgrad_kernel<PAIR, FMT, SHIFTED>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
 
-template <int FMT, bool SHIFTED>
-cudaError_t launch(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count) {
-    using C = WgradCfg;
-    cudaError_t e = configure<FMT, SHIFTED>(dev);
+template <bool PAIR, int FMT, bool SHIFTED>
+cudaError_t launch(const Q8WgradTmemArgs& a, cudaStream_t s, int dev, int sm_count) {
+    using C = WgradCfg<PAIR>;
+    cudaError_t e = configure<PAIR, FMT, SHIFTED>(dev);
     if (e != cudaSuccess) return e;
     const long long units = static_cast<long long>(a.share.whole) + a.share.runs;
-    const int clusters = static_cast<int>(units < sm_count / 2 ? units : sm_count / 2);
+    const int slots = sm_count / C::CTAS;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1] = pdl_attribute();
-    cfg.gridDim = dim3(2 * clusters);
+    attr[0] = pdl_attribute();
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(C::CTAS * static_cast<int>(units < slots ? units : slots));
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, q8_wgrad_pair_kernel<FMT, SHIFTED>, a.tmY, a.shifts, a.tmC, a.tmS,
+    cfg.numAttrs = PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, q8_wgrad_kernel<PAIR, FMT, SHIFTED>, a.tmY, a.shifts, a.tmC, a.tmS,
                            a.dw, a.lddw, a.parts, a.cols, a.N, a.rows, a.share, a.chunk, a.fault,
                            a.timeout_ns, a.alpha, a.beta, a.mode);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-constexpr int kSumRows = 2;
 // The kernel that adds the shared tiles' partial sums.
-cudaError_t launch_sum(const Q8WgradPairArgs& a, cudaStream_t s) {
-    using C = WgradCfg;
+template <bool PAIR>
+cudaError_t launch_sum(const Q8WgradTmemArgs& a, cudaStream_t s) {
+    using C = WgradCfg<PAIR>;
+    constexpr int kRowsInFlight = 2;
     const bool vec = a.lddw % 4 == 0 && reinterpret_cast<uintptr_t>(a.dw) % 16 == 0;
     // four lanes an output group where a tile has many partials
     const bool quarters = a.share.runs >= 8LL * a.share.shared;
+    const int rows = quarters ? 64 / (C::TN / 4) : kRowsInFlight * 256 / (C::TN / 4);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    cfg.gridDim = dim3(quarters ? C::TD : C::TD / (4 * kSumRows),
-                       a.share.shared < 65535 ? a.share.shared : 65535);
+    cfg.gridDim = dim3(C::TD / rows, a.share.shared < 65535 ? a.share.shared : 65535);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(
-        &cfg, quarters ? q8_wgrad_sum_kernel<4, 1, 10> : q8_wgrad_sum_kernel<1, kSumRows, 4>,
+        &cfg,
+        quarters ? q8_wgrad_sum_kernel<C, 4, 1, 10> : q8_wgrad_sum_kernel<C, 1, kRowsInFlight, 4>,
         static_cast<const float*>(a.parts), a.share, a.dw, a.lddw, vec, a.cols, a.N, a.alpha,
         a.beta, a.mode);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-}  // namespace
-
-Q8WgradTile q8_wgrad_tile() { return {WgradCfg::TD, WgradCfg::TN, WgradCfg::KT}; }
-
-size_t q8_wgrad_parts_bytes(const Q8WgradShare& sh) {
-    if (!sh.shared) return 0;
-    return (static_cast<size_t>(sh.runs) + sh.shared) * (WgradCfg::TD * WgradCfg::TN * 4);
-}
-
-cudaError_t launch_q8_wgrad_pair(const Q8WgradPairArgs& a, cudaStream_t s, int dev, int sm_count) {
+template <bool PAIR>
+cudaError_t launch_form(const Q8WgradTmemArgs& a, cudaStream_t s, int dev, int sm_count) {
     cudaError_t e;
     if (a.format == kQ8Int8)
-        e = a.shifted ? launch<kQ8Int8, true>(a, s, dev, sm_count)
-                      : launch<kQ8Int8, false>(a, s, dev, sm_count);
+        e = a.shifted ? launch<PAIR, kQ8Int8, true>(a, s, dev, sm_count)
+                      : launch<PAIR, kQ8Int8, false>(a, s, dev, sm_count);
     else
-        e = a.shifted ? launch<kQ8E4m3, true>(a, s, dev, sm_count)
-                      : launch<kQ8E4m3, false>(a, s, dev, sm_count);
+        e = a.shifted ? launch<PAIR, kQ8E4m3, true>(a, s, dev, sm_count)
+                      : launch<PAIR, kQ8E4m3, false>(a, s, dev, sm_count);
     if (e != cudaSuccess || !a.share.shared) return e;
-    return launch_sum(a, s);
+    return launch_sum<PAIR>(a, s);
+}
+
+}  // namespace
+
+Q8WgradTile q8_wgrad_tile(bool pair) {
+    using P = WgradCfg<true>;
+    return {P::TD, pair ? P::TN : WgradCfg<false>::TN, P::KT};
+}
+
+size_t q8_wgrad_parts_bytes(const Q8WgradShare& sh, bool pair) {
+    if (!sh.shared) return 0;
+    const Q8WgradTile t = q8_wgrad_tile(pair);
+    return (static_cast<size_t>(sh.runs) + sh.shared) * (t.features * t.columns * 4);
+}
+
+cudaError_t launch_q8_wgrad_tmem(const Q8WgradTmemArgs& a, cudaStream_t s, int dev, int sm_count) {
+    return a.pair ? launch_form<true>(a, s, dev, sm_count) : launch_form<false>(a, s, dev, sm_count);
 }
 
 }  // namespace gemm_f32_impl

@@ -28,7 +28,8 @@ import dense_fp32_gemm_row_gb300 as _g
 
 __all__ = [
     "Q8", "Q8Struct", "Q8_INT8", "Q8_E4M3", "Q8_FORMATS", "Q8_BLOCK", "Q8_TO_F32", "Q8_TO_BF16",
-    "ACT_SILU", "ACT_GELU", "ACTS", "ALGO_3XBF16", "Q8_ALGOS", "gemm_f32_q8_store", "gemm_f32_q8_restore",
+    "ACT_SILU", "ACT_GELU", "ACTS", "ALGO_3XBF16",
+    "ALGO_3XBF16_PAIR", "ALGO_3XBF16_SINGLE", "Q8_ALGOS", "gemm_f32_q8_store", "gemm_f32_q8_restore",
     "gemm_f32_q8_wgrad", "gemm_f32_q8_gated", "gemm_f32_q8_gated_backward", "q8_empty",
     "q8_store", "q8_restore", "q8_wgrad", "q8_gated", "q8_gated_backward",
 ]
@@ -42,7 +43,10 @@ Q8_TO_BF16 = 1
 ACT_SILU = 0
 ACT_GELU = 1
 ALGO_3XBF16 = 3
-Q8_ALGOS = {"auto": 0, "ffma": 1, "3xbf16": ALGO_3XBF16}
+ALGO_3XBF16_PAIR = 4
+ALGO_3XBF16_SINGLE = 5
+Q8_ALGOS = {"auto": 0, "ffma": 1, "3xbf16": ALGO_3XBF16, "3xbf16_pair": ALGO_3XBF16_PAIR,
+            "3xbf16_single": ALGO_3XBF16_SINGLE}
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 
 
@@ -350,8 +354,9 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
 
     ``dy`` is (q.rows, N); ``out`` (q.cols, N) is allocated if not given, and
     must be given for ``beta`` other than 0 (gradient accumulation).  ``algo``
-    is "auto", "ffma" or "3xbf16" (the tensor-core kernel), ``splits`` the
-    number of ranges the latter splits the tokens into (0: chosen by size).
+    is "auto", "ffma" or "3xbf16" (the tensor-core kernel; "3xbf16_pair" and
+    "3xbf16_single" force its tiles), ``splits`` the number of ranges the
+    latter splits the tokens into (0: chosen by size).
     """
     if _torch is None:
         _load_torch()

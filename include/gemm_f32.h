@@ -414,14 +414,18 @@ int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
  * x's values enter exactly and products are summed in fp32.  algo:
  * GEMM_F32_ALGO_FFMA, the CUDA-core kernel; GEMM_F32_ALGO_3XBF16 (this entry
  * point's alone), the tensor-core kernel, which splits each float of dY
- * exactly into three bf16 parts; GEMM_F32_ALGO_AUTO, chosen by size.  splits:
+ * exactly into three bf16 parts, with its tiles (256 x 256 by a CTA pair or
+ * 256 x 128 by one CTA) chosen by size or, _PAIR and _SINGLE, forced;
+ * GEMM_F32_ALGO_AUTO, all of this chosen by size.  splits:
  * for the tensor-core kernel, over how many ranges the tokens are split, as
  * for gemm_f32_algo_splitk (0: the library chooses).  With beta == 0 the old dW is not read; with alpha ==
  * 0 or no rows, x and dY are not read and dW = beta * dW.  A NaN or infinity
  * in dY or a block of x that restores to NaN gives non-finite outputs in the
  * columns or rows of dW it enters.
  */
-#define GEMM_F32_ALGO_3XBF16 3
+#define GEMM_F32_ALGO_3XBF16        3
+#define GEMM_F32_ALGO_3XBF16_PAIR   4
+#define GEMM_F32_ALGO_3XBF16_SINGLE 5
 int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int N, float alpha,
                       float beta, float* dW, long long lddw, int algo, int splits,
                       cudaStream_t stream);

@@ -333,7 +333,8 @@ WGRAD_SHAPES = [(1, 1, 1), (1, 40, 5), (2, 32, 4), (15, 33, 3), (16, 64, 64), (1
                 (255, 260, 4), (256, 4, 260), (257, 300, 516), (1000, 333, 77), (1025, 1000, 24)]
 
 
-ALGOS = ("ffma", "3xbf16")
+ALGOS = ("ffma", "3xbf16_pair", "3xbf16_single")
+TENSOR = ALGOS[1:]
 
 
 @pytest.mark.parametrize("algo", ALGOS)
@@ -357,13 +358,14 @@ def test_wgrad(fmt, T, D, N, algo):
     assert_wgrad(g.q8_wgrad(q, matrix(dy)[0], algo=algo), x, dy)
 
 
+@pytest.mark.parametrize("algo", TENSOR)
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,D,N,splits", [(100, 40, 50, 1), (100, 40, 50, 2), (100, 40, 50, 4),
                                           (100, 40, 50, 256), (1000, 300, 301, 7),
                                           (5000, 257, 100, 33), (5000, 257, 100, 256)])
-def test_wgrad_split_over_tokens(fmt, T, D, N, splits):
+def test_wgrad_split_over_tokens(fmt, T, D, N, splits, algo):
     q, x, dy = wgrad_case(np.random.default_rng(T + splits), T, D, N, fmt)
-    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0], algo="3xbf16", splits=splits), x, dy)
+    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0], algo=algo, splits=splits), x, dy)
 
 
 @pytest.mark.parametrize("algo", ALGOS)
@@ -389,25 +391,27 @@ def test_wgrad_of_every_code_and_exponent(fmt, algo):
     assert not np.isfinite(got[over]).any()
 
 
+@pytest.mark.parametrize("algo", ("auto",) + TENSOR)
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,D,N", [(4096, 256, 256), (5000, 300, 500), (20000, 256, 40),
                                    (65536, 64, 96), (2048, 2048, 1024), (600, 4100, 1500),
                                    # tiles of 256 x 256 shared by the 76 CTA pairs: 45 and, after
                                    # a round of whole tiles, 14 of 90, over tile boundaries or not
                                    (2100, 1283, 2049), (2100, 2305, 2303)])
-def test_wgrad_large(fmt, T, D, N):
+def test_wgrad_large(fmt, T, D, N, algo):
     q, x, dy = wgrad_case(np.random.default_rng(T + D + N), T, D, N, fmt)
-    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0]), x, dy)
+    assert_wgrad(g.q8_wgrad(q, matrix(dy)[0], algo=algo), x, dy)
 
 
+@pytest.mark.parametrize("algo", ("auto",) + TENSOR)
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("T,D,N", [(50, 70, 90), (700, 300, 520), (3000, 512, 512)])
-@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (4, 4), (6, 2), (1000, 0)])
-def test_wgrad_strides_and_alignment(fmt, T, D, N, pad, offset):
+@pytest.mark.parametrize("T,D,N", [(3, 70, 90), (50, 70, 90), (700, 300, 520), (3000, 512, 512)])
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (4, 4), (6, 2), (3, 3), (1000, 0)])
+def test_wgrad_strides_and_alignment(fmt, T, D, N, pad, offset, algo):
     q, x, dy = wgrad_case(np.random.default_rng(pad + offset), T, D, N, fmt)
     view, _ = matrix(dy, pad, offset)
     out, buf = matrix(np.zeros((D, N)), pad, offset)
-    assert g.q8_wgrad(q, view, out=out) is out
+    assert g.q8_wgrad(q, view, out=out, algo=algo) is out
     assert_wgrad(out, x, dy)
     assert outside_is_nan(out, buf)
 
