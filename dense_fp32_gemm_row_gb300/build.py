@@ -6,7 +6,10 @@
 Each ``csrc/*.cu`` translation unit is compiled in parallel into
 ``_build/<name>.o`` (ptxas register/spill report in ``_build/<name>.ptxas.txt``)
 and the objects are linked, with the static CUDA runtime, into
-``dense_fp32_gemm_row_gb300/libgemmf32.so``.
+``dense_fp32_gemm_row_gb300/libgemmf32.so``.  ``csrc/binding/tensors.cpp``, the
+Python binding's fast path for output tensors, is built with g++ against the
+installed torch into ``dense_fp32_gemm_row_gb300/_tensors.so``; the binding works
+without it, so a torch it cannot be built for is only reported.
 """
 
 from __future__ import annotations
@@ -16,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +28,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemmf32.so")
+TENSORS_SRC = os.path.join(CSRC, "binding", "tensors.cpp")
+TENSORS = os.path.join(PKG, "_tensors.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -67,13 +73,44 @@ def _compile(nvcc: str, src: str, force: bool) -> str:
     return obj
 
 
+def _build_tensors(force: bool) -> None:
+    """Build the binding's module for the installed torch, if there is one."""
+    import importlib.util
+
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return
+    torch_dir = os.path.dirname(spec.origin)
+    # the build this module belongs to: another torch's headers are another module
+    version_file = os.path.join(torch_dir, "version.py")
+    if not force and not _stale(TENSORS, [TENSORS_SRC, version_file, __file__]):
+        return
+    include = os.path.join(torch_dir, "include")
+    lib = os.path.join(torch_dir, "lib")
+    tmp = TENSORS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=1",
+           "-I", sysconfig.get_paths()["include"], "-isystem", include,
+           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           TENSORS_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode == 0:
+        os.replace(tmp, TENSORS)
+    else:
+        print(f"{TENSORS} not built, torch.empty is used instead:\n{res.stderr[-2000:]}",
+              file=sys.stderr)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build (if stale) and return the path of libgemmf32.so."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        tensors = ex.submit(_build_tensors, force)
         objs = list(ex.map(lambda s: _compile(nvcc, s, force), srcs))
+        tensors.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp]

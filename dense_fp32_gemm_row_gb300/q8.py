@@ -100,23 +100,80 @@ def _declare(lib) -> None:
 # ---- tensors ---------------------------------------------------------------------------------
 #
 # A small call takes the GPU a few microseconds, so what the binding spends on the host is most
-# of it: a call looks at each tensor once, makes one allocation for each result, and takes the
-# slower ways (another stream, another device) only where they are needed.
+# of it: a call looks at each tensor once and takes the slower ways (another stream, another
+# device) only where they are needed.  Making a tensor by torch.empty costs more than the launch
+# (see csrc/binding/tensors.cpp, which makes the outputs where it is built); memory alone from the
+# same allocator takes 0.6 us, so a checkpoint holds that and makes its two tensors when they are
+# asked for.
 
 _torch = None  # set on first use: importing the package does not import torch
-_stream_of = None
+_stream_of = _alloc = _free = _empty = _lib = None
 _one_device = True
 
 
 def _load_torch():
-    global _torch, _stream_of, _one_device
+    global _torch, _stream_of, _alloc, _free, _empty, _lib, _one_device
     import torch
 
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _stream_of = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    # the functions behind torch.cuda's current_stream, caching_allocator_alloc and _delete
+    _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
+                         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc",
+                     lambda size, stream: torch.cuda.caching_allocator_alloc(size, None, stream))
+    _free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete",
+                    torch.cuda.caching_allocator_delete)
+    try:
+        from dense_fp32_gemm_row_gb300._tensors import empty as _empty
+    except ImportError:  # not built, or for another torch
+        def _empty(rows, cols, bf16, device):
+            return torch.empty((rows, cols), dtype=torch.bfloat16 if bf16 else torch.float32,
+                               device=device)
+    _lib = _g.load()
     _one_device = torch.cuda.device_count() <= 1
     _torch = torch
     return torch
+
+
+class _Memory:
+    """Bytes of torch's caching allocator for the current stream, freed with this object."""
+
+    __slots__ = ("address", "size", "device", "stream", "others", "__weakref__")
+
+    def __init__(self, size, device):
+        self.address, self.size, self.device, self.others = 0, size, device, None
+        self.stream = _stream_of(device)
+        if size:
+            self.address = _alloc(size, self.stream)
+
+    def __del__(self):
+        if self.address and _free is not None:
+            if self.others:
+                self._order()
+            _free(self.address)
+
+    def record_stream(self, stream):
+        """The memory is used on ``stream``: what that holds now comes before its reuse."""
+        self.others = (self.others or []) + [stream]
+
+    def _order(self):
+        # the allocator hands the memory to later work of the stream it was allocated for
+        cuda = _torch.cuda
+        mine = (cuda.ExternalStream(self.stream, device=self.device) if self.stream
+                else cuda.default_stream(self.device))
+        for other in self.others:
+            mine.wait_stream(other)
+
+    @property
+    def __cuda_array_interface__(self):
+        return {"shape": (self.size,), "typestr": "|u1", "data": (self.address, False),
+                "version": 2}
+
+    def tensor(self):
+        """A uint8 tensor of these bytes, which keeps them."""
+        device = f"cuda:{self.device}"
+        if not self.size:
+            return _torch.empty(0, dtype=_torch.uint8, device=device)
+        return _torch.as_tensor(self, device=device)
 
 
 def _name(table, value, what):
@@ -134,7 +191,7 @@ class Q8:
     that are multiples of 16.  ``format`` is "int8" or "e4m3".
     """
 
-    __slots__ = ("_codes", "_scales", "_buffer", "_at", "device", "rows", "cols", "format", "struct")
+    __slots__ = ("_codes", "_scales", "_memory", "device", "rows", "cols", "format", "struct")
 
     def __init__(self, codes, scales, cols, format="int8"):
         torch = _torch or _load_torch()
@@ -148,25 +205,29 @@ class Q8:
         self.device = codes.get_device()
         if scales.get_device() != self.device:
             raise ValueError("codes and scales must be on one device")
-        self._codes, self._scales, self._buffer, self._at = codes, scales, None, 0
+        self._codes, self._scales, self._memory = codes, scales, None
         self.rows, self.cols, self.format = rows, cols, format
 
     @property
     def codes(self):
         """The code bytes, (rows, cols rounded up to 16) for a checkpoint made here."""
         if self._codes is None:
-            ld = self.struct.ldcodes
-            self._codes = self._buffer[self._at:self._at + self.rows * ld].view(self.rows, ld)
+            self._views()
         return self._codes
 
     @property
     def scales(self):
         """The exponent bytes, one for each block of 32 columns."""
         if self._scales is None:
-            ld = self.struct.ldscales
-            at = self._at + self.rows * self.struct.ldcodes
-            self._scales = self._buffer[at:at + self.rows * ld].view(self.rows, ld)
+            self._views()
         return self._scales
+
+    def _views(self):
+        s, all_bytes = self.struct, self._memory.tensor()
+        at = s.codes - self._memory.address if s.codes else 0
+        between, end = at + self.rows * s.ldcodes, at + self.rows * (s.ldcodes + s.ldscales)
+        self._codes = all_bytes[at:between].view(self.rows, s.ldcodes)
+        self._scales = all_bytes[between:end].view(self.rows, s.ldscales)
 
     @property
     def nbytes(self) -> int:
@@ -174,9 +235,12 @@ class Q8:
         return self.codes.numel() + self.scales.numel()
 
     def record_stream(self, stream) -> None:
-        """As ``torch.Tensor.record_stream`` of the tensors behind it."""
-        for t in (self._buffer,) if self._buffer is not None else (self._codes, self._scales):
-            t.record_stream(stream)
+        """As ``torch.Tensor.record_stream``, for a checkpoint used on another stream."""
+        if self._memory is not None:
+            self._memory.record_stream(stream)
+        else:
+            self._codes.record_stream(stream)
+            self._scales.record_stream(stream)
 
     def __repr__(self):
         return f"Q8({self.rows} x {self.cols}, {self.format})"
@@ -198,15 +262,14 @@ def _bytes_ld(torch, t, rows, width) -> int:
     return ld
 
 
-def _make(device, rows, cols, format, fmt) -> Q8:
-    """An uninitialised checkpoint on a device: codes, then exponents, in one buffer."""
+def _place(memory, at, device, rows, cols, format, fmt) -> Q8:
+    """An uninitialised checkpoint in a piece of memory: codes, then exponents."""
     q = Q8.__new__(Q8)
     ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
-    q._buffer = buf = _torch.empty(rows * (ldc + lds), dtype=_torch.uint8, device=device)
-    q._at = 0
-    base = buf.data_ptr()
+    base = memory.address + at
     q.struct = Q8Struct(base, base + rows * ldc, ldc, lds, rows, cols, fmt)
     q._codes = q._scales = None
+    q._memory = memory
     q.device = device
     q.rows = rows
     q.cols = cols
@@ -214,23 +277,20 @@ def _make(device, rows, cols, format, fmt) -> Q8:
     return q
 
 
+def _bytes(rows, cols) -> int:
+    return rows * (((cols + 15) & ~15) + ((((cols + 31) >> 5) + 15) & ~15))
+
+
+def _make(device, rows, cols, format, fmt) -> Q8:
+    return _place(_Memory(_bytes(rows, cols), device), 0, device, rows, cols, format, fmt)
+
+
 def _make_two(device, rows, cols, format, fmt):
-    """Two uninitialised checkpoints of one shape, kept for one backward pass, in one buffer."""
-    a, b = Q8.__new__(Q8), Q8.__new__(Q8)
-    ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
-    one = rows * (ldc + lds)
-    both = _torch.empty(2 * one, dtype=_torch.uint8, device=device)
-    base = both.data_ptr()
-    for q, at in ((a, 0), (b, one)):
-        q._buffer, q._at = both, at
-        q.struct = Q8Struct(base + at, base + at + rows * ldc, ldc, lds, rows, cols, fmt)
-        q._codes = q._scales = None
-        q.device, q.rows, q.cols, q.format = device, rows, cols, format
-    return a, b
-
-
-def _floats(rows, cols, device):
-    return _torch.empty((rows, cols), dtype=_torch.float32, device=device)
+    """Two checkpoints of one shape, kept for one backward pass, in one allocation."""
+    one = _bytes(rows, cols)
+    memory = _Memory(2 * one, device)
+    return (_place(memory, 0, device, rows, cols, format, fmt),
+            _place(memory, one, device, rows, cols, format, fmt))
 
 
 def _matrix(t, what):
@@ -299,8 +359,8 @@ def q8_empty(rows, cols, format="int8", device="cuda") -> Q8:
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError("a checkpoint is made on a CUDA device")
-    return _make(torch.cuda.current_device() if device.index is None else device.index, rows, cols,
-                 format, fmt)
+    with torch.cuda.device(device):
+        return _make(torch.cuda.current_device(), rows, cols, format, fmt)
 
 
 def q8_store(x, format="int8", out=None, stream=None) -> Q8:
@@ -314,7 +374,7 @@ def q8_store(x, format="int8", out=None, stream=None) -> Q8:
         return _elsewhere(lambda: q8_store(x, format, out), device, stream, (x, out))
     q = _make(device, rows, cols, format, fmt) if out is None else _given(out, rows, cols, format,
                                                                      device, "out")
-    st = gemm_f32_q8_store(x.data_ptr(), ld, q.struct, _stream_of(device))
+    st = _lib.gemm_f32_q8_store(x.data_ptr(), ld, q.struct, _stream_of(device))
     if st:
         _g.check(st, "q8_store")
     return q
@@ -332,7 +392,7 @@ def q8_restore(q, out=None, dtype=None, stream=None):
         return _elsewhere(lambda: q8_restore(q, out, dtype), device, stream, (q, out))
     if out is None:
         rows, cols = q.rows, q.cols
-        x = torch.empty((rows, cols), dtype=dtype, device=device)
+        x = _empty(rows, cols, dtype is torch.bfloat16, device)
         ld = cols or 1
     else:
         x = out
@@ -341,9 +401,9 @@ def q8_restore(q, out=None, dtype=None, stream=None):
         rows, cols, ld = _strides(x, "out")
         if rows != q.rows or cols != q.cols:
             raise ValueError(f"out must be {q.rows} x {q.cols}, not {rows} x {cols}")
-    st = gemm_f32_q8_restore(q.struct, x.data_ptr(), ld,
-                             Q8_TO_F32 if dtype is torch.float32 else Q8_TO_BF16,
-                             _stream_of(device))
+    st = _lib.gemm_f32_q8_restore(q.struct, x.data_ptr(), ld,
+                                  Q8_TO_F32 if dtype is torch.float32 else Q8_TO_BF16,
+                                  _stream_of(device))
     if st:
         _g.check(st, "q8_restore")
     return x
@@ -373,11 +433,11 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     if out is None:
         if beta != 0.0:
             raise ValueError("beta needs out, the gradient to add to")
-        dw, ldw = _floats(q.cols, N, device), N or 1
+        dw, ldw = _empty(q.cols, N, 0, device), N or 1
     else:
         dw, ldw = out, _like(out, q.cols, N, device, "out")
-    st = gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(), ldw, code,
-                           splits, _stream_of(device))
+    st = _lib.gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(), ldw,
+                                code, splits, _stream_of(device))
     if st:
         _g.check(st, "q8_wgrad")
     return dw
@@ -396,7 +456,7 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
         return _elsewhere(lambda: q8_gated(gate, up, act, format, out, gate_q, up_q), device,
                           stream, (gate, up, out, gate_q, up_q))
     if out is None:
-        h, ldh = _floats(rows, cols, device), cols or 1
+        h, ldh = _empty(rows, cols, 0, device), cols or 1
     else:
         h, ldh = out, _like(out, rows, cols, device, "out")
     if gate_q is None and up_q is None:
@@ -406,8 +466,8 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
             gate_q, rows, cols, format, device, "gate_q")
         uq = _make(device, rows, cols, format, fmt) if up_q is None else _given(
             up_q, rows, cols, format, device, "up_q")
-    st = gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(), ldh,
-                           gq.struct, uq.struct, _stream_of(device))
+    st = _lib.gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(), ldh,
+                                gq.struct, uq.struct, _stream_of(device))
     if st:
         _g.check(st, "q8_gated")
     return h, gq, uq
@@ -434,20 +494,21 @@ def q8_gated_backward(gate_q, up_q, dh, act="silu", dgate=None, dup=None, h_q=No
         return _elsewhere(lambda: q8_gated_backward(gate_q, up_q, dh, act, dgate, dup, h_q, want_h),
                           device, stream, (gate_q, up_q, dh, dgate, dup, h_q))
     if dgate is None:
-        dg, ldg = _floats(rows, cols, device), cols or 1
+        dg, ldg = _empty(rows, cols, 0, device), cols or 1
     else:
         dg, ldg = dgate, _like(dgate, rows, cols, device, "dgate")
     if dup is None:
-        du, ldu = _floats(rows, cols, device), cols or 1
+        du, ldu = _empty(rows, cols, 0, device), cols or 1
     else:
         du, ldu = dup, _like(dup, rows, cols, device, "dup")
     if h_q is not None:
         _given(h_q, rows, cols, format, device, "h_q")
     elif want_h:
         h_q = _make(device, rows, cols, format, gate_q.struct.format)
-    st = gemm_f32_q8_gated_backward(code, gate_q.struct, up_q.struct, dh.data_ptr(), ldh,
-                                    dg.data_ptr(), ldg, du.data_ptr(), ldu,
-                                    None if h_q is None else h_q.struct, _stream_of(device))
+    st = _lib.gemm_f32_q8_gated_backward(code, gate_q.struct, up_q.struct, dh.data_ptr(), ldh,
+                                         dg.data_ptr(), ldg, du.data_ptr(), ldu,
+                                         None if h_q is None else h_q.struct,
+                                         _stream_of(device))
     if st:
         _g.check(st, "q8_gated_backward")
     return dg, du, h_q

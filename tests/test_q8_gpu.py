@@ -1,5 +1,7 @@
 """8-bit checkpoint operators on the GPU against their 64-bit forms."""
 
+import gc
+
 import numpy as np
 import pytest
 
@@ -677,3 +679,43 @@ def test_wgrad_needs_its_workspace_before_a_capture():
         out.zero_()  # a graph of something
     assert st == g.ERR_CAPTURE
     assert_wgrad(g.q8_wgrad(q, dev), x, dy)
+
+
+def test_checkpoint_memory_lives_as_long_as_it_is_used():
+    """Views keep the memory; dropped checkpoints give it back; empty ones have none."""
+    torch = t()
+    x = torch.randn(1000, 4096, device="cuda")
+    q = g.q8_store(x)
+    want = g.q8_restore(q).clone()
+    codes, scales = q.codes, q.scales
+    del q
+    junk = [g.q8_store(torch.zeros(1000, 4096, device="cuda")) for _ in range(4)]
+    assert torch.equal(g.q8_restore(g.Q8(codes, scales, 4096)), want)
+    del junk, codes, scales
+    torch.cuda.synchronize()
+    gc.collect()
+    before = torch.cuda.memory_allocated()
+    for _ in range(50):
+        g.q8_store(x)
+    assert torch.cuda.memory_allocated() == before
+    none = g.q8_empty(0, 70)
+    assert none.codes.shape == (0, 80) and none.scales.shape == (0, 16) and none.nbytes == 0
+
+
+def test_checkpoint_dropped_while_another_stream_reads_it():
+    """Its memory is not handed out again before that stream is done."""
+    torch = t()
+    x = torch.randn(4096, 4096, device="cuda")
+    want = g.q8_restore(g.q8_store(x)).clone()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        q = g.q8_store(x)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2000000)  # the reader is late
+        back = g.q8_restore(q, stream=side)
+        del q
+        others = [g.q8_store(torch.zeros_like(x)) for _ in range(3)]
+        side.synchronize()
+        assert torch.equal(back, want)
+        del others
