@@ -194,17 +194,27 @@ class Q8:
     __slots__ = ("_codes", "_scales", "_memory", "device", "rows", "cols", "format", "struct")
 
     def __init__(self, codes, scales, cols, format="int8"):
-        torch = _torch or _load_torch()
+        u8 = (_torch or _load_torch()).uint8
         fmt = _name(Q8_FORMATS, format, "format")
-        rows, cols = codes.shape[0], int(cols)
-        if cols < 0:
-            raise ValueError("cols must not be negative")
-        self.struct = Q8Struct(codes.data_ptr(), scales.data_ptr(),
-                               _bytes_ld(torch, codes, rows, cols),
-                               _bytes_ld(torch, scales, rows, (cols + 31) >> 5), rows, cols, fmt)
-        self.device = codes.get_device()
-        if scales.get_device() != self.device:
+        if (codes.dtype is not u8 or scales.dtype is not u8 or codes.dim() != 2
+                or scales.dim() != 2 or not codes.is_cuda):
+            raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
+        self.device = device = codes.get_device()
+        if scales.get_device() != device:
             raise ValueError("codes and scales must be on one device")
+        (rows, width), (rows2, width2) = codes.shape, scales.shape
+        blocks = (cols + 31) >> 5
+        if cols < 0 or rows2 != rows or width < cols or width2 < blocks:
+            raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
+        (ldc, one), (lds, one2) = codes.stride(), scales.stride()
+        at, at2 = codes.data_ptr(), scales.data_ptr()
+        if rows <= 1:
+            ldc, lds = (width + 15) & ~15, (width2 + 15) & ~15
+        if rows and cols and (one != 1 or one2 != 1 or (at | at2 | ldc | lds) & 15
+                              or ldc < cols or lds < blocks):
+            raise ValueError("codes and scales must have contiguous rows, 16-byte aligned bases "
+                             "and row strides that are multiples of 16")
+        self.struct = Q8Struct(at, at2, ldc, lds, rows, cols, fmt)
         self._codes, self._scales, self._memory = codes, scales, None
         self.rows, self.cols, self.format = rows, cols, format
 
@@ -244,22 +254,6 @@ class Q8:
 
     def __repr__(self):
         return f"Q8({self.rows} x {self.cols}, {self.format})"
-
-
-def _bytes_ld(torch, t, rows, width) -> int:
-    """The row stride of one of a checkpoint's byte tensors, which must hold rows x width."""
-    if t.dtype is not torch.uint8 or not t.is_cuda or t.dim() != 2:
-        raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
-    r, w = t.shape
-    if r != rows or w < width:
-        raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
-    s0, s1 = t.stride()
-    if rows and width and (s1 != 1 or t.data_ptr() & 15):
-        raise ValueError("codes and scales must have contiguous rows and 16-byte aligned bases")
-    ld = s0 if rows > 1 else (w + 15) & ~15
-    if ld & 15 or ld < width:
-        raise ValueError("row strides of codes and scales must be multiples of 16")
-    return ld
 
 
 def _place(memory, at, device, rows, cols, format, fmt) -> Q8:

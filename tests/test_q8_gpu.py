@@ -601,6 +601,32 @@ def test_many_elements():
     assert bool((back[:-2] == 0).all()) and bool((back[-2:] == want).all())
 
 
+def test_wgrad_with_more_than_2_31_outputs():
+    torch = t()
+    T, D, N = 8, 66000, 33000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-100, 101, (T, D), generator=gen, device="cuda").float()
+    dy = torch.randint(-50, 51, (T, N), generator=gen, device="cuda").float()
+    q = g.q8_store(x)
+    xv = g.q8_restore(q).double()
+    dw = g.q8_wgrad(q, dy)
+    for rows in (slice(0, 300), slice(32700, 32900), slice(65000, 66000)):  # 2^31 / N = 65075
+        assert torch.equal(dw[rows].double(), xv[:, rows].t() @ dy.double())
+
+
+def test_wgrad_with_more_than_2_31_codes():
+    torch = t()
+    T, D, N = 140000, 16416, 24
+    q = g.q8_store(torch.zeros(T, D, device="cuda"))
+    x = torch.arange(D, device="cuda") % 255 - 127.0
+    tail = g.q8_store(x.expand(3, D).contiguous())
+    q.codes[-3:] = tail.codes
+    q.scales[-3:] = tail.scales
+    dy = torch.ones(T, N, device="cuda")
+    want = 3 * g.q8_restore(tail)[0]
+    assert torch.equal(g.q8_wgrad(q, dy), want[:, None].expand(D, N))
+
+
 def test_binding_refuses():
     torch = t()
     x = torch.zeros(8, 64, device="cuda")
