@@ -137,8 +137,9 @@ constexpr double kWgradLeastGain = 0.05;
 // Stages per tensor-core sum, 256 tokens: relative error 7e-7 (2-norm; an fp32
 // product in one running sum has 1.6e-6 at 8192 tokens).  Each sum costs the
 // MMAs a wait of ~0.23 us: 128 tokens, 4e-7, were 2.2 % slower at 8192 x 8192
-// x 8192, 512 tokens, 1.4e-6, 0.8 % faster.
-constexpr int kWgradChunk = 8;
+// x 8192, 512 tokens, 1.4e-6, 0.8 % faster.  Units of up to 512 tokens, where
+// an fp32 product has no more than 4e-7 either, pay for 128 with two waits.
+constexpr int kWgradChunk = 8, kWgradShortChunk = 4, kWgradShortStages = 16;
 
 // The CUDA-core kernel, which has no pipeline to fill and no descriptors, for
 // a few tokens and small outputs (measured, against the tensor-core kernel's
@@ -389,7 +390,10 @@ int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int
     k.cols = x->cols;
     k.N = N;
     k.format = x->format;
-    k.chunk = kWgradChunk;
+    const int longest = k.share.shared && !k.share.whole
+                            ? (k.share.group_stages - 1) / k.share.group_runs + 1
+                            : k.share.stages;
+    k.chunk = longest <= kWgradShortStages ? kWgradShortChunk : kWgradChunk;
     k.fault = c.fault;
     k.timeout_ns = kDefaultTimeoutNs;
     k.alpha = alpha;
