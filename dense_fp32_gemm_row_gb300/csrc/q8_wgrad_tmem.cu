@@ -740,6 +740,8 @@ q8_wgrad_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
         bool ok = true;
         Unit w;
         for (Pieces<C> todo; ok && todo.next(share, w);) {
+#pragma unroll
+            for (int i = 0; i < EPI_COLS; ++i) acc[i] = 0.0f;
             for (int c0 = 0; c0 < w.nkb; c0 += chunk, ++g) {
                 const bool got = role_wait(accf, g & 1, timeout_ns, fault, kFaultAccumBarrier,
                                            abort_flag);
@@ -759,13 +761,8 @@ q8_wgrad_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
 #pragma unroll
                     for (int b = 0; b < C::DRAIN_BATCH; ++b) {
                         const int j = j0 + b;
-                        if (c0 == 0) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[16 * j + i] = __uint_as_float(r[b][i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[16 * j + i] += __uint_as_float(r[b][i]);
-                        }
+                        for (int i = 0; i < 16; ++i) acc[16 * j + i] += __uint_as_float(r[b][i]);
                     }
                 }
                 // the loads have completed: the arrival orders no writes
