@@ -7,7 +7,7 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel into
 ``_build/<name>.o`` (ptxas register/spill report in ``_build/<name>.ptxas.txt``)
 and the objects are linked, with the static CUDA runtime, into
 ``dense_fp32_gemm_row_gb300/libgemmf32.so``.  ``csrc/binding/tensors.cpp``, the
-Python binding's fast path for output tensors, is built with g++ against the
+Python binding's fast path for the 8-bit operators, is built with g++ against the
 installed torch into ``dense_fp32_gemm_row_gb300/_tensors.so``; the binding works
 without it, so a torch it cannot be built for is only reported.
 """
@@ -83,13 +83,13 @@ def _build_tensors(force: bool) -> None:
     torch_dir = os.path.dirname(spec.origin)
     # the build this module belongs to: another torch's headers are another module
     version_file = os.path.join(torch_dir, "version.py")
-    if not force and not _stale(TENSORS, [TENSORS_SRC, version_file, __file__]):
+    if not force and not _stale(TENSORS, [TENSORS_SRC, version_file, *_headers(), __file__]):
         return
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
     tmp = TENSORS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=1",
-           "-I", sysconfig.get_paths()["include"], "-isystem", include,
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", include,
            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
            TENSORS_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
@@ -98,7 +98,7 @@ def _build_tensors(force: bool) -> None:
     if res.returncode == 0:
         os.replace(tmp, TENSORS)
     else:
-        print(f"{TENSORS} not built, torch.empty is used instead:\n{res.stderr[-2000:]}",
+        print(f"{TENSORS} not built, every call of an 8-bit operator goes step by step in Python:\n{res.stderr[-2000:]}",
               file=sys.stderr)
 
 

@@ -100,80 +100,68 @@ def _declare(lib) -> None:
 # ---- tensors ---------------------------------------------------------------------------------
 #
 # A small call takes the GPU a few microseconds, so what the binding spends on the host is most
-# of it: a call looks at each tensor once and takes the slower ways (another stream, another
-# device) only where they are needed.  Making a tensor by torch.empty costs more than the launch
-# (see csrc/binding/tensors.cpp, which makes the outputs where it is built); memory alone from the
-# same allocator takes 0.6 us, so a checkpoint holds that and makes its two tensors when they are
-# asked for.
+# of it.  The ordinary call -- plain tensors on the current device, nothing given for its results --
+# is one call of the module built from csrc/binding/tensors.cpp, which answers None to anything
+# else; what follows here then looks at the operands one by one, and finds the error if there is one.
 
 _torch = None  # set on first use: importing the package does not import torch
-_stream_of = _alloc = _free = _empty = _lib = None
+_stream_of = _lib = None
+_native = None  # the module, where it is built for the installed torch
 _one_device = True
 
 
 def _load_torch():
-    global _torch, _stream_of, _alloc, _free, _empty, _lib, _one_device
+    global _torch, _stream_of, _lib, _native, _one_device
     import torch
 
-    # the functions behind torch.cuda's current_stream, caching_allocator_alloc and _delete
+    # the function behind torch.cuda.current_stream
     _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream",
                          lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc",
-                     lambda size, stream: torch.cuda.caching_allocator_alloc(size, None, stream))
-    _free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete",
-                    torch.cuda.caching_allocator_delete)
-    try:
-        from dense_fp32_gemm_row_gb300._tensors import empty as _empty
-    except ImportError:  # not built, or for another torch
-        def _empty(rows, cols, bf16, device):
-            return torch.empty((rows, cols), dtype=torch.bfloat16 if bf16 else torch.float32,
-                               device=device)
     _lib = _g.load()
+    try:
+        from dense_fp32_gemm_row_gb300 import _tensors
+    except ImportError:  # not built, or for another torch
+        pass
+    else:
+        _tensors.bind(*(ctypes.cast(getattr(_lib, "gemm_f32_q8_" + name), ctypes.c_void_p).value
+                        for name in ("store", "restore", "wgrad", "gated", "gated_backward")),
+                      _g.check)
+        _native = _tensors
     _one_device = torch.cuda.device_count() <= 1
     _torch = torch
     return torch
 
 
-class _Memory:
-    """Bytes of torch's caching allocator for the current stream, freed with this object."""
+class _Held:
+    """Two tensors and their layout, as the module's objects of this name hold them."""
 
-    __slots__ = ("address", "size", "device", "stream", "others", "__weakref__")
+    __slots__ = ("_tensors", "device", "rows", "cols", "codes", "scales", "ldcodes", "ldscales")
 
-    def __init__(self, size, device):
-        self.address, self.size, self.device, self.others = 0, size, device, None
-        self.stream = _stream_of(device)
-        if size:
-            self.address = _alloc(size, self.stream)
+    def __init__(self, codes, scales, ldcodes, ldscales, cols):
+        self._tensors = codes, scales
+        self.device, self.rows, self.cols = codes.get_device(), codes.shape[0], cols
+        self.codes, self.scales = codes.data_ptr(), scales.data_ptr()
+        self.ldcodes, self.ldscales = ldcodes, ldscales
 
-    def __del__(self):
-        if self.address and _free is not None:
-            if self.others:
-                self._order()
-            _free(self.address)
+    def tensors(self):
+        return self._tensors
 
-    def record_stream(self, stream):
-        """The memory is used on ``stream``: what that holds now comes before its reuse."""
-        self.others = (self.others or []) + [stream]
 
-    def _order(self):
-        # the allocator hands the memory to later work of the stream it was allocated for
-        cuda = _torch.cuda
-        mine = (cuda.ExternalStream(self.stream, device=self.device) if self.stream
-                else cuda.default_stream(self.device))
-        for other in self.others:
-            mine.wait_stream(other)
+def _empty(rows, cols, bf16, device):
+    if _native is not None:
+        return _native.empty(rows, cols, bf16, device)
+    return _torch.empty((rows, cols), dtype=_torch.bfloat16 if bf16 else _torch.float32,
+                        device=f"cuda:{device}")
 
-    @property
-    def __cuda_array_interface__(self):
-        return {"shape": (self.size,), "typestr": "|u1", "data": (self.address, False),
-                "version": 2}
 
-    def tensor(self):
-        """A uint8 tensor of these bytes, which keeps them."""
-        device = f"cuda:{self.device}"
-        if not self.size:
-            return _torch.empty(0, dtype=_torch.uint8, device=device)
-        return _torch.as_tensor(self, device=device)
+def _make(device, rows, cols, format) -> Q8:
+    """An uninitialised checkpoint: rows of codes and of exponents, each padded to 16 bytes."""
+    if _native is not None:
+        return _of(_native.make(rows, cols, Q8_FORMATS[format], device), format)
+    ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
+    codes, scales = (_torch.empty((rows, ld), dtype=_torch.uint8, device=f"cuda:{device}")
+                     for ld in (ldc, lds))
+    return _of(_Held(codes, scales, ldc, lds, cols), format)
 
 
 def _name(table, value, what):
@@ -191,53 +179,56 @@ class Q8:
     that are multiples of 16.  ``format`` is "int8" or "e4m3".
     """
 
-    __slots__ = ("_codes", "_scales", "_memory", "device", "rows", "cols", "format", "struct")
+    __slots__ = ("_held", "_struct", "format")
 
     def __init__(self, codes, scales, cols, format="int8"):
         u8 = (_torch or _load_torch()).uint8
         fmt = _name(Q8_FORMATS, format, "format")
+        self.format, self._struct = format, None
+        if _native is not None:
+            self._held = _native.wrap(codes, scales, cols, fmt)
+            if self._held is not None:
+                return
         if (codes.dtype is not u8 or scales.dtype is not u8 or codes.dim() != 2
                 or scales.dim() != 2 or not codes.is_cuda):
             raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
-        self.device = device = codes.get_device()
-        if scales.get_device() != device:
+        if scales.get_device() != codes.get_device():
             raise ValueError("codes and scales must be on one device")
         (rows, width), (rows2, width2) = codes.shape, scales.shape
         blocks = (cols + 31) >> 5
         if cols < 0 or rows2 != rows or width < cols or width2 < blocks:
             raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
         (ldc, one), (lds, one2) = codes.stride(), scales.stride()
-        at, at2 = codes.data_ptr(), scales.data_ptr()
         if rows <= 1:
             ldc, lds = (width + 15) & ~15, (width2 + 15) & ~15
-        if rows and cols and (one != 1 or one2 != 1 or (at | at2 | ldc | lds) & 15
-                              or ldc < cols or lds < blocks):
+        if rows and cols and (one != 1 or one2 != 1 or ldc < cols or lds < blocks
+                              or (codes.data_ptr() | scales.data_ptr() | ldc | lds) & 15):
             raise ValueError("codes and scales must have contiguous rows, 16-byte aligned bases "
                              "and row strides that are multiples of 16")
-        self.struct = Q8Struct(at, at2, ldc, lds, rows, cols, fmt)
-        self._codes, self._scales, self._memory = codes, scales, None
-        self.rows, self.cols, self.format = rows, cols, format
+        self._held = _Held(codes, scales, ldc, lds, cols)
+
+    rows = property(lambda self: self._held.rows)
+    cols = property(lambda self: self._held.cols)
+    device = property(lambda self: self._held.device, doc="The index of the CUDA device.")
 
     @property
     def codes(self):
         """The code bytes, (rows, cols rounded up to 16) for a checkpoint made here."""
-        if self._codes is None:
-            self._views()
-        return self._codes
+        return self._held.tensors()[0]
 
     @property
     def scales(self):
         """The exponent bytes, one for each block of 32 columns."""
-        if self._scales is None:
-            self._views()
-        return self._scales
+        return self._held.tensors()[1]
 
-    def _views(self):
-        s, all_bytes = self.struct, self._memory.tensor()
-        at = s.codes - self._memory.address if s.codes else 0
-        between, end = at + self.rows * s.ldcodes, at + self.rows * (s.ldcodes + s.ldscales)
-        self._codes = all_bytes[at:between].view(self.rows, s.ldcodes)
-        self._scales = all_bytes[between:end].view(self.rows, s.ldscales)
+    @property
+    def struct(self) -> Q8Struct:
+        """The checkpoint for the raw entry points; valid as long as this object."""
+        if self._struct is None:
+            h = self._held
+            self._struct = Q8Struct(h.codes, h.scales, h.ldcodes, h.ldscales, h.rows, h.cols,
+                                    Q8_FORMATS[self.format])
+        return self._struct
 
     @property
     def nbytes(self) -> int:
@@ -246,45 +237,17 @@ class Q8:
 
     def record_stream(self, stream) -> None:
         """As ``torch.Tensor.record_stream``, for a checkpoint used on another stream."""
-        if self._memory is not None:
-            self._memory.record_stream(stream)
-        else:
-            self._codes.record_stream(stream)
-            self._scales.record_stream(stream)
+        for t in self._held.tensors():
+            t.record_stream(stream)
 
     def __repr__(self):
         return f"Q8({self.rows} x {self.cols}, {self.format})"
 
 
-def _place(memory, at, device, rows, cols, format, fmt) -> Q8:
-    """An uninitialised checkpoint in a piece of memory: codes, then exponents."""
+def _of(held, format) -> Q8:
     q = Q8.__new__(Q8)
-    ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
-    base = memory.address + at
-    q.struct = Q8Struct(base, base + rows * ldc, ldc, lds, rows, cols, fmt)
-    q._codes = q._scales = None
-    q._memory = memory
-    q.device = device
-    q.rows = rows
-    q.cols = cols
-    q.format = format
+    q._held, q._struct, q.format = held, None, format
     return q
-
-
-def _bytes(rows, cols) -> int:
-    return rows * (((cols + 15) & ~15) + ((((cols + 31) >> 5) + 15) & ~15))
-
-
-def _make(device, rows, cols, format, fmt) -> Q8:
-    return _place(_Memory(_bytes(rows, cols), device), 0, device, rows, cols, format, fmt)
-
-
-def _make_two(device, rows, cols, format, fmt):
-    """Two checkpoints of one shape, kept for one backward pass, in one allocation."""
-    one = _bytes(rows, cols)
-    memory = _Memory(2 * one, device)
-    return (_place(memory, 0, device, rows, cols, format, fmt),
-            _place(memory, one, device, rows, cols, format, fmt))
 
 
 def _matrix(t, what):
@@ -349,25 +312,29 @@ def _away(device) -> bool:
 def q8_empty(rows, cols, format="int8", device="cuda") -> Q8:
     """An uninitialised checkpoint of a rows x cols matrix."""
     torch = _torch or _load_torch()
-    fmt = _name(Q8_FORMATS, format, "format")
+    _name(Q8_FORMATS, format, "format")
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError("a checkpoint is made on a CUDA device")
     with torch.cuda.device(device):
-        return _make(torch.cuda.current_device(), rows, cols, format, fmt)
+        return _make(torch.cuda.current_device(), rows, cols, format)
 
 
 def q8_store(x, format="int8", out=None, stream=None) -> Q8:
     """The 8-bit checkpoint of ``x`` (rows, cols), in ``out`` if given."""
     if _torch is None:
         _load_torch()
-    rows, cols, ld = _matrix(x, "x")
     fmt = _name(Q8_FORMATS, format, "format")
+    if out is None and stream is None and _native is not None:
+        held = _native.store(x, fmt)
+        if held is not None:
+            return _of(held, format)
+    rows, cols, ld = _matrix(x, "x")
     device = x.get_device()
     if stream is not None or _away(device):
         return _elsewhere(lambda: q8_store(x, format, out), device, stream, (x, out))
-    q = _make(device, rows, cols, format, fmt) if out is None else _given(out, rows, cols, format,
-                                                                     device, "out")
+    q = _make(device, rows, cols, format) if out is None else _given(out, rows, cols, format, device,
+                                                                     "out")
     st = _lib.gemm_f32_q8_store(x.data_ptr(), ld, q.struct, _stream_of(device))
     if st:
         _g.check(st, "q8_store")
@@ -381,6 +348,10 @@ def q8_restore(q, out=None, dtype=None, stream=None):
         dtype = torch.float32 if out is None else out.dtype
     if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError("dtype is torch.float32 or torch.bfloat16")
+    if out is None and stream is None and _native is not None:
+        x = _native.restore(q._held, dtype is torch.bfloat16)
+        if x is not None:
+            return x
     device = q.device
     if stream is not None or _away(device):
         return _elsewhere(lambda: q8_restore(q, out, dtype), device, stream, (q, out))
@@ -414,6 +385,11 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     """
     if _torch is None:
         _load_torch()
+    if (out is None and stream is None and _native is not None and algo == "auto" and splits == 0
+            and alpha == 1.0 and beta == 0.0):
+        dw = _native.wgrad(q._held, dy)
+        if dw is not None:
+            return dw
     rows, N, ldy = _matrix(dy, "dy")
     if rows != q.rows:
         raise ValueError(f"dy must have {q.rows} rows, not {rows}")
@@ -441,9 +417,13 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
     """``h = act(gate) * up`` and the checkpoints of gate and up: ``(h, gate_q, up_q)``."""
     if _torch is None:
         _load_torch()
-    rows, cols, ldg = _matrix(gate, "gate")
     code = _name(ACTS, act, "act")
     fmt = _name(Q8_FORMATS, format, "format")
+    if out is None and gate_q is None and up_q is None and stream is None and _native is not None:
+        made = _native.gated(gate, up, code, fmt)
+        if made is not None:
+            return made[0], _of(made[1], format), _of(made[2], format)
+    rows, cols, ldg = _matrix(gate, "gate")
     device = gate.get_device()
     ldu = _like(up, rows, cols, device, "up")
     if stream is not None or _away(device):
@@ -453,13 +433,9 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
         h, ldh = _empty(rows, cols, 0, device), cols or 1
     else:
         h, ldh = out, _like(out, rows, cols, device, "out")
-    if gate_q is None and up_q is None:
-        gq, uq = _make_two(device, rows, cols, format, fmt)
-    else:
-        gq = _make(device, rows, cols, format, fmt) if gate_q is None else _given(
-            gate_q, rows, cols, format, device, "gate_q")
-        uq = _make(device, rows, cols, format, fmt) if up_q is None else _given(
-            up_q, rows, cols, format, device, "up_q")
+    gq, uq = (_make(device, rows, cols, format) if q is None else
+              _given(q, rows, cols, format, device, what)
+              for q, what in ((gate_q, "gate_q"), (up_q, "up_q")))
     st = _lib.gemm_f32_q8_gated(code, gate.data_ptr(), ldg, up.data_ptr(), ldu, h.data_ptr(), ldh,
                                 gq.struct, uq.struct, _stream_of(device))
     if st:
@@ -478,8 +454,13 @@ def q8_gated_backward(gate_q, up_q, dh, act="silu", dgate=None, dup=None, h_q=No
     """
     if _torch is None:
         _load_torch()
-    rows, cols, format, device = gate_q.rows, gate_q.cols, gate_q.format, gate_q.device
     code = _name(ACTS, act, "act")
+    if dgate is None and dup is None and h_q is None and stream is None and _native is not None:
+        made = _native.gated_backward(gate_q._held, up_q._held, dh, code, bool(want_h))
+        if made is not None:
+            dg, du, held = made
+            return dg, du, None if held is None else _of(held, gate_q.format)
+    rows, cols, format, device = gate_q.rows, gate_q.cols, gate_q.format, gate_q.device
     _given(up_q, rows, cols, format, device, "up_q")
     ldh = _like(dh, rows, cols, device, "dh")
     if h_q is not None and not want_h:
@@ -498,7 +479,7 @@ def q8_gated_backward(gate_q, up_q, dh, act="silu", dgate=None, dup=None, h_q=No
     if h_q is not None:
         _given(h_q, rows, cols, format, device, "h_q")
     elif want_h:
-        h_q = _make(device, rows, cols, format, gate_q.struct.format)
+        h_q = _make(device, rows, cols, format)
     st = _lib.gemm_f32_q8_gated_backward(code, gate_q.struct, up_q.struct, dh.data_ptr(), ldh,
                                          dg.data_ptr(), ldg, du.data_ptr(), ldu,
                                          None if h_q is None else h_q.struct,

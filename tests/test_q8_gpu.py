@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import dense_fp32_gemm_row_gb300 as g
+from dense_fp32_gemm_row_gb300 import q8 as _binding
 from tests import _q8
 
 pytestmark = pytest.mark.gpu
@@ -745,3 +746,65 @@ def test_checkpoint_dropped_while_another_stream_reads_it():
         side.synchronize()
         assert torch.equal(back, want)
         del others
+
+
+def step(torch, x, gate, up, dh, dy):
+    """Every operator once as a user calls it, and what each gives."""
+    q = g.q8_store(x, format="e4m3")
+    h, gq, uq = g.q8_gated(gate, up, act="gelu")
+    dgate, dup, hq = g.q8_gated_backward(gq, uq, dh, act="gelu")
+    nothing = g.q8_gated_backward(gq, uq, dh, act="gelu", want_h=False)[2]
+    assert nothing is None and q.format == "e4m3" and hq.format == gq.format == "int8"
+    assert (q.rows, q.cols, q.device) == (x.shape[0], x.shape[1], x.get_device())
+    assert repr(q) == f"Q8({x.shape[0]} x {x.shape[1]}, e4m3)"
+    again = g.Q8(q.codes, q.scales, q.cols, format="e4m3")
+    return [h, dgate, dup, g.q8_restore(again), g.q8_restore(hq, dtype=torch.bfloat16),
+            g.q8_wgrad(again, dy), g.q8_restore(gq), g.q8_restore(uq)]
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 33), (1, 33), (5, 0), (1, 1), (64, 512), (37, 1001)])
+def test_calls_with_and_without_the_native_module(monkeypatch, rows, cols):
+    """The binding's two ways through a call give the same bits."""
+    torch = t()
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols)
+    wide = torch.randn(rows, 2 * cols + 3, device="cuda", generator=gen)
+    x, gate, up = wide[:, :cols], wide[:, :cols], wide[:, cols:2 * cols]
+    dh = torch.randn(rows, cols, device="cuda", generator=gen)
+    dy = torch.randn(rows, 40, device="cuda", generator=gen)
+    want = step(torch, x, gate, up, dh, dy)
+    assert _binding._native is not None
+    monkeypatch.setattr(_binding, "_native", None)
+    got = step(torch, x, gate, up, dh, dy)
+    for a, b in zip(want, got):
+        assert a.shape == b.shape and a.dtype == b.dtype and a.stride() == b.stride()
+        assert torch.equal(a, b)
+
+
+def test_native_module_takes_only_plain_tensors():
+    """A parameter, a double, a transpose, host memory: each by the other way, with its answer."""
+    torch = t()
+    x = torch.randn(70, 70, device="cuda")
+    want = g.q8_restore(g.q8_store(x))
+    assert torch.equal(g.q8_restore(g.q8_store(torch.nn.Parameter(x))), want)
+    for bad in (x.double(), x.t(), x.cpu(), x[0], x[:1].expand(8, 70)):
+        for call in (lambda: g.q8_store(bad), lambda: g.q8_gated(bad, bad),
+                     lambda: g.q8_wgrad(g.q8_store(x), bad)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        g.q8_store(x, format="int4")
+    q = g.q8_store(x)
+    with pytest.raises(ValueError):
+        g.q8_gated_backward(q, q, x, act="relu")
+
+
+def test_native_module_reports_the_librarys_status():
+    torch = t()
+    q, x, dy = wgrad_case(np.random.default_rng(1), 4096, 300, 300, "int8")
+    dev, _ = matrix(dy)
+    g.check(g.gemm_f32_release())
+    g.gemm_f32_inject_host_fault(g.INJECT_WORKSPACE)
+    with pytest.raises(g.GemmError) as e:
+        g.q8_wgrad(q, dev)
+    assert e.value.status == g.ERR_WORKSPACE
+    assert_wgrad(g.q8_wgrad(q, dev), x, dy)
