@@ -62,7 +62,7 @@
 // back at the power limit).  With operands that are never rewritten the same
 // MMAs and copies take 1.70 ms; three bf16 products at the burst rate of the
 // library's product take 1.72, at its sustained rate 1.91.  4096 x 2048 x
-// 2048: 75.5 us, 64 tiles on 76 pairs, the tensor pipe busy 79 % of a CTA's
+// 2048: 74.2 us, 64 tiles on 76 pairs, the tensor pipe busy 79 % of a CTA's
 // life, a stage 0.53 us.
 //
 // Where the tiles do not fill the units evenly, the last of them are shared:
