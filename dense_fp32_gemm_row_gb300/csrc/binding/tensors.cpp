@@ -39,7 +39,9 @@ struct Library {
     decltype(&gemm_f32_q8_wgrad) wgrad;
     decltype(&gemm_f32_q8_gated) gated;
     decltype(&gemm_f32_q8_gated_backward) gated_backward;
-    PyObject* check;  // the binding's check(status, where), which raises
+    PyObject* check;     // the binding's check(status, where), which raises
+    PyTypeObject* type;  // its checkpoint class, which has one slot:
+    PyObject* slot;      // the name of the slot for a Held
 } lib = {};
 
 // ---- checkpoints ---------------------------------------------------------------
@@ -105,6 +107,13 @@ struct Ref {
     }
 };
 
+// The binding's object around a Held; its class has no other state to set up.
+PyObject* checkpoint(const Ref& h) {
+    PyObject* q = lib.type->tp_alloc(lib.type, 0);
+    if (q && PyObject_SetAttr(q, lib.slot, h.p) < 0) Py_CLEAR(q);
+    return q;
+}
+
 // `n` uninitialised checkpoints of one layout in one allocation.
 void make(const gemm_f32_q8& shape, int device, int n, Ref* out) {
     const long long codes = shape.rows * shape.ldcodes, each = codes + shape.rows * shape.ldscales;
@@ -153,6 +162,7 @@ PyMethodDef held_methods[] = {{"tensors", held_tensors, METH_NOARGS, nullptr},
 PyGetSetDef held_fields[] = {
     {"rows", held_number<int, &gemm_f32_q8::rows>, nullptr, nullptr, nullptr},
     {"cols", held_number<int, &gemm_f32_q8::cols>, nullptr, nullptr, nullptr},
+    {"format", held_number<int, &gemm_f32_q8::format>, nullptr, nullptr, nullptr},
     {"ldcodes", held_number<long long, &gemm_f32_q8::ldcodes>, nullptr, nullptr, nullptr},
     {"ldscales", held_number<long long, &gemm_f32_q8::ldscales>, nullptr, nullptr, nullptr},
     {"codes", held_address<&gemm_f32_q8::codes>, nullptr, nullptr, nullptr},
@@ -215,9 +225,10 @@ bool call(const char* where, F f) {
 
 // ---- the functions -------------------------------------------------------------
 
-// bind(store, restore, wgrad, gated, gated_backward, check): the library's addresses
+// bind(store, restore, wgrad, gated, gated_backward, check, type): the library's
+// addresses, and what the binding gives
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (!count(n, 6)) return nullptr;
+    if (!count(n, 7)) return nullptr;
     void* p[5];
     for (int i = 0; i < 5; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;
@@ -226,9 +237,18 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
     lib.wgrad = reinterpret_cast<decltype(lib.wgrad)>(p[2]);
     lib.gated = reinterpret_cast<decltype(lib.gated)>(p[3]);
     lib.gated_backward = reinterpret_cast<decltype(lib.gated_backward)>(p[4]);
+    if (!PyType_Check(args[6])) {
+        PyErr_SetString(PyExc_TypeError, "the checkpoint class is a type");
+        return nullptr;
+    }
+    if (!lib.slot) lib.slot = PyUnicode_InternFromString("_held");
+    if (!lib.slot) return nullptr;
     Py_INCREF(args[5]);
+    Py_INCREF(args[6]);
     Py_XDECREF(lib.check);
+    Py_XDECREF(lib.type);
     lib.check = args[5];
+    lib.type = reinterpret_cast<PyTypeObject*>(args[6]);
     Py_RETURN_NONE;
 }
 
@@ -258,11 +278,11 @@ PyObject* py_make(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     Ref out;
     make(layout(v[0], v[1], static_cast<int>(v[2])), static_cast<int>(v[3]), 1, &out);
-    return out.take();
+    return checkpoint(out);
     END_HANDLE_TH_ERRORS
 }
 
-// wrap(codes, scales, cols, format): a checkpoint of two byte tensors, or None
+// wrap(codes, scales, cols, format): the Held of two byte tensors, or None
 PyObject* wrap(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     long v[2];
@@ -310,7 +330,7 @@ PyObject* store(PyObject*, PyObject* const* args, Py_ssize_t n) {
     make(layout(x.rows, x.cols, static_cast<int>(format)), x.device, 1, &out);
     const cudaStream_t s = stream_of(x.device);
     if (!call("q8_store", [&] { return lib.store(x.p, x.ld, &out->q, s); })) return nullptr;
-    return out.take();
+    return checkpoint(out);
     END_HANDLE_TH_ERRORS
 }
 
@@ -353,6 +373,15 @@ PyObject* wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+PyObject* three(Ref& a, Ref& b, Ref& c) {
+    PyObject* out = a.p && b.p && c.p ? PyTuple_New(3) : nullptr;
+    if (!out) return nullptr;
+    PyTuple_SET_ITEM(out, 0, a.take());
+    PyTuple_SET_ITEM(out, 1, b.take());
+    PyTuple_SET_ITEM(out, 2, c.take());
+    return out;
+}
+
 // gated(gate, up, act, format) -> (h, checkpoint of gate, checkpoint of up)
 PyObject* gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -371,14 +400,8 @@ PyObject* gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
                              &q[1]->q, s);
         }))
         return nullptr;
-    Ref t{THPVariable_Wrap(y)};
-    if (!t.p) return nullptr;
-    PyObject* out = PyTuple_New(3);
-    if (!out) return nullptr;
-    PyTuple_SET_ITEM(out, 0, t.take());
-    PyTuple_SET_ITEM(out, 1, q[0].take());
-    PyTuple_SET_ITEM(out, 2, q[1].take());
-    return out;
+    Ref t{THPVariable_Wrap(y)}, gq{checkpoint(q[0])}, uq{checkpoint(q[1])};
+    return three(t, gq, uq);
     END_HANDLE_TH_ERRORS
 }
 
@@ -405,18 +428,14 @@ PyObject* gated_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                       row(d.cols), pu, row(d.cols), q.p ? &q->q : nullptr, s);
         }))
         return nullptr;
-    Ref tg{THPVariable_Wrap(dg)}, tu{THPVariable_Wrap(du)};
-    if (!tg.p || !tu.p) return nullptr;
-    PyObject* out = PyTuple_New(3);
-    if (!out) return nullptr;
-    PyTuple_SET_ITEM(out, 0, tg.take());
-    PyTuple_SET_ITEM(out, 1, tu.take());
-    if (!q.p) {
+    Ref tg{THPVariable_Wrap(dg)}, tu{THPVariable_Wrap(du)}, hq;
+    if (q.p) {
+        hq.p = checkpoint(q);
+    } else {
         Py_INCREF(Py_None);
-        q.p = Py_None;
+        hq.p = Py_None;
     }
-    PyTuple_SET_ITEM(out, 2, q.take());
-    return out;
+    return three(tg, tu, hq);
     END_HANDLE_TH_ERRORS
 }
 

@@ -37,6 +37,7 @@ __all__ = [
 Q8_INT8 = 0
 Q8_E4M3 = 1
 Q8_FORMATS = {"int8": Q8_INT8, "e4m3": Q8_E4M3}
+_FORMAT_NAMES = {value: name for name, value in Q8_FORMATS.items()}
 Q8_BLOCK = 32
 Q8_TO_F32 = 0
 Q8_TO_BF16 = 1
@@ -125,7 +126,7 @@ def _load_torch():
     else:
         _tensors.bind(*(ctypes.cast(getattr(_lib, "gemm_f32_q8_" + name), ctypes.c_void_p).value
                         for name in ("store", "restore", "wgrad", "gated", "gated_backward")),
-                      _g.check)
+                      _g.check, Q8)
         _native = _tensors
     _one_device = torch.cuda.device_count() <= 1
     _torch = torch
@@ -135,13 +136,14 @@ def _load_torch():
 class _Held:
     """Two tensors and their layout, as the module's objects of this name hold them."""
 
-    __slots__ = ("_tensors", "device", "rows", "cols", "codes", "scales", "ldcodes", "ldscales")
+    __slots__ = ("_tensors", "device", "rows", "cols", "format", "codes", "scales", "ldcodes",
+                 "ldscales")
 
-    def __init__(self, codes, scales, ldcodes, ldscales, cols):
+    def __init__(self, codes, scales, ldcodes, ldscales, cols, format):
         self._tensors = codes, scales
         self.device, self.rows, self.cols = codes.get_device(), codes.shape[0], cols
         self.codes, self.scales = codes.data_ptr(), scales.data_ptr()
-        self.ldcodes, self.ldscales = ldcodes, ldscales
+        self.ldcodes, self.ldscales, self.format = ldcodes, ldscales, format
 
     def tensors(self):
         return self._tensors
@@ -157,11 +159,13 @@ def _empty(rows, cols, bf16, device):
 def _make(device, rows, cols, format) -> Q8:
     """An uninitialised checkpoint: rows of codes and of exponents, each padded to 16 bytes."""
     if _native is not None:
-        return _of(_native.make(rows, cols, Q8_FORMATS[format], device), format)
+        return _native.make(rows, cols, Q8_FORMATS[format], device)
     ldc, lds = (cols + 15) & ~15, (((cols + 31) >> 5) + 15) & ~15
     codes, scales = (_torch.empty((rows, ld), dtype=_torch.uint8, device=f"cuda:{device}")
                      for ld in (ldc, lds))
-    return _of(_Held(codes, scales, ldc, lds, cols), format)
+    q = Q8.__new__(Q8)
+    q._held = _Held(codes, scales, ldc, lds, cols, Q8_FORMATS[format])
+    return q
 
 
 def _name(table, value, what):
@@ -179,12 +183,11 @@ class Q8:
     that are multiples of 16.  ``format`` is "int8" or "e4m3".
     """
 
-    __slots__ = ("_held", "_struct", "format")
+    __slots__ = ("_held",)
 
     def __init__(self, codes, scales, cols, format="int8"):
         u8 = (_torch or _load_torch()).uint8
         fmt = _name(Q8_FORMATS, format, "format")
-        self.format, self._struct = format, None
         if _native is not None:
             self._held = _native.wrap(codes, scales, cols, fmt)
             if self._held is not None:
@@ -205,10 +208,11 @@ class Q8:
                               or (codes.data_ptr() | scales.data_ptr() | ldc | lds) & 15):
             raise ValueError("codes and scales must have contiguous rows, 16-byte aligned bases "
                              "and row strides that are multiples of 16")
-        self._held = _Held(codes, scales, ldc, lds, cols)
+        self._held = _Held(codes, scales, ldc, lds, cols, fmt)
 
     rows = property(lambda self: self._held.rows)
     cols = property(lambda self: self._held.cols)
+    format = property(lambda self: _FORMAT_NAMES[self._held.format])
     device = property(lambda self: self._held.device, doc="The index of the CUDA device.")
 
     @property
@@ -224,11 +228,8 @@ class Q8:
     @property
     def struct(self) -> Q8Struct:
         """The checkpoint for the raw entry points; valid as long as this object."""
-        if self._struct is None:
-            h = self._held
-            self._struct = Q8Struct(h.codes, h.scales, h.ldcodes, h.ldscales, h.rows, h.cols,
-                                    Q8_FORMATS[self.format])
-        return self._struct
+        h = self._held
+        return Q8Struct(h.codes, h.scales, h.ldcodes, h.ldscales, h.rows, h.cols, h.format)
 
     @property
     def nbytes(self) -> int:
@@ -242,12 +243,6 @@ class Q8:
 
     def __repr__(self):
         return f"Q8({self.rows} x {self.cols}, {self.format})"
-
-
-def _of(held, format) -> Q8:
-    q = Q8.__new__(Q8)
-    q._held, q._struct, q.format = held, None, format
-    return q
 
 
 def _matrix(t, what):
@@ -326,9 +321,9 @@ def q8_store(x, format="int8", out=None, stream=None) -> Q8:
         _load_torch()
     fmt = _name(Q8_FORMATS, format, "format")
     if out is None and stream is None and _native is not None:
-        held = _native.store(x, fmt)
-        if held is not None:
-            return _of(held, format)
+        q = _native.store(x, fmt)
+        if q is not None:
+            return q
     rows, cols, ld = _matrix(x, "x")
     device = x.get_device()
     if stream is not None or _away(device):
@@ -422,7 +417,7 @@ def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=No
     if out is None and gate_q is None and up_q is None and stream is None and _native is not None:
         made = _native.gated(gate, up, code, fmt)
         if made is not None:
-            return made[0], _of(made[1], format), _of(made[2], format)
+            return made
     rows, cols, ldg = _matrix(gate, "gate")
     device = gate.get_device()
     ldu = _like(up, rows, cols, device, "up")
@@ -456,10 +451,9 @@ def q8_gated_backward(gate_q, up_q, dh, act="silu", dgate=None, dup=None, h_q=No
         _load_torch()
     code = _name(ACTS, act, "act")
     if dgate is None and dup is None and h_q is None and stream is None and _native is not None:
-        made = _native.gated_backward(gate_q._held, up_q._held, dh, code, bool(want_h))
+        made = _native.gated_backward(gate_q._held, up_q._held, dh, code, 1 if want_h else 0)
         if made is not None:
-            dg, du, held = made
-            return dg, du, None if held is None else _of(held, gate_q.format)
+            return made
     rows, cols, format, device = gate_q.rows, gate_q.cols, gate_q.format, gate_q.device
     _given(up_q, rows, cols, format, device, "up_q")
     ldh = _like(dh, rows, cols, device, "dh")
