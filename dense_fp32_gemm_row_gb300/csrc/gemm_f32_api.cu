@@ -14,7 +14,9 @@
 #include <cstdint>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -37,21 +39,37 @@ struct DeviceState {
     int sm_count = 0;
     int cc_major = 0, cc_minor = 0;
     unsigned* fault = nullptr;  // device fault word (256-byte allocation)
+    cudaStream_t zeroing = nullptr;  // clears graph buffers, never captured
 };
 
 struct Workspace {
     void* ptr = nullptr;
     size_t bytes = 0;
-    // a call captured into a CUDA graph used ptr: the graph keeps the
-    // pointer, so a grown workspace retires the old buffer (freed by
-    // gemm_f32_release) instead of freeing it
-    bool captured = false;
-    std::vector<void*> retired;
 };
+
+// Device memory of calls captured into CUDA graphs.  A graph keeps the
+// pointers of its capture and may be replayed on any stream, beside other
+// graphs and beside calls on the stream that it was captured from: nothing
+// orders those with one another, so a captured call gets none of the stream's
+// own buffers but one that its graph holds (as a user object, whose
+// destructor the runtime calls when the graph, what was instantiated from it
+// and their launches are done with it).  Calls that one capture takes from
+// one stream run in order and share it.
+struct GraphBuffer {
+    int dev;
+    void* ptr;
+    size_t bytes;
+    int use;  // GraphUse
+    unsigned long long capture;
+    cudaStream_t stream;
+    std::shared_ptr<std::atomic<bool>> over;  // set by the destructor: free for another capture
+};
+enum GraphUse { kGraphWorkspace, kGraphHostCopies };
 
 std::mutex g_mutex;
 DeviceState g_dev[kMaxDevices];
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+std::vector<GraphBuffer> g_graph_buffers;
 EncodeTiledFn g_encode = nullptr;
 
 // A host-side failure armed by gemm_f32_inject_host_fault (0: none), taken
@@ -155,24 +173,101 @@ int encode_2d(CUtensorMap* map, const float* base, long long dim0, long long dim
                       swizzle);
 }
 
+// While it lives, this thread may allocate although a stream is captured.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// A graph's last hold on a buffer is gone; the runtime allows no CUDA call here.
+void CUDART_CB graph_buffer_over(void* p) {
+    auto* over = static_cast<std::shared_ptr<std::atomic<bool>>*>(p);
+    (*over)->store(true);
+    delete over;
+}
+
+// A buffer of at least `bytes` for a call that is captured from `stream`;
+// g_mutex must be held.  A workspace starts with its counters at zero.
+int graph_buffer(int dev, cudaStream_t stream, GraphUse use, size_t bytes, void** out) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long capture = 0;
+    cudaGraph_t graph = nullptr;
+    cudaError_t e =
+        cudaStreamGetCaptureInfo(stream, &status, &capture, &graph, nullptr, nullptr, nullptr);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (status != cudaStreamCaptureStatusActive)
+        return static_cast<int>(cudaErrorStreamCaptureInvalidated);
+    GraphBuffer* b = nullptr;  // the smallest of those that no graph holds
+    for (GraphBuffer& x : g_graph_buffers) {
+        if (x.dev != dev || x.use != use || x.bytes < bytes) continue;
+        if (x.over->load()) {
+            if (!b || x.bytes < b->bytes) b = &x;
+        } else if (x.capture == capture && x.stream == stream) {
+            *out = x.ptr;
+            return GEMM_F32_SUCCESS;
+        }
+    }
+    RelaxedCapture relaxed;
+    if (!b) {
+        const size_t size = static_cast<size_t>(round_up(static_cast<long long>(bytes), 1 << 20));
+        GraphBuffer made = {dev, nullptr, size, use, 0, nullptr,
+                            std::make_shared<std::atomic<bool>>(true)};
+        g_graph_buffers.reserve(g_graph_buffers.size() + 1);
+        if (injected(GEMM_F32_INJECT_WORKSPACE) || cudaMalloc(&made.ptr, size) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_F32_ERR_WORKSPACE;
+        }
+        g_graph_buffers.push_back(made);
+        b = &g_graph_buffers.back();
+    }
+    if (use == kGraphWorkspace) {
+        cudaStream_t& s = g_dev[dev].zeroing;
+        if (!s && (e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking)) != cudaSuccess)
+            return static_cast<int>(e);
+        if ((e = cudaMemsetAsync(b->ptr, 0, kWorkspaceCounterBytes, s)) != cudaSuccess ||
+            (e = cudaStreamSynchronize(s)) != cudaSuccess)
+            return static_cast<int>(e);
+    }
+    // where the graph takes no user object the buffer stays its own until
+    // gemm_f32_release
+    b->over = std::make_shared<std::atomic<bool>>(false);
+    auto held = std::make_unique<std::shared_ptr<std::atomic<bool>>>(
+        std::make_shared<std::atomic<bool>>(false));
+    const std::shared_ptr<std::atomic<bool>> over = *held;
+    cudaUserObject_t object = nullptr;
+    if (cudaUserObjectCreate(&object, held.get(), graph_buffer_over, 1,
+                             cudaUserObjectNoDestructorSync) == cudaSuccess) {
+        held.release();  // the object's
+        if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) == cudaSuccess)
+            b->over = over;
+        else
+            cudaUserObjectRelease(object, 1);
+    }
+    cudaGetLastError();
+    b->capture = capture;
+    b->stream = stream;
+    *out = b->ptr;
+    return GEMM_F32_SUCCESS;
+}
+
 // Workspace of at least `bytes` for (dev, stream); g_mutex must be held.
-int workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
+int workspace(int dev, cudaStream_t stream, size_t bytes, void** out) try {
     Workspace& w = g_ws[std::make_pair(dev, stream)];
-    const bool capturing = stream_capturing(stream);
+    if (stream_capturing(stream)) {
+        // the call has been issued on the stream before: everything else that
+        // it sets up is there
+        if (w.bytes < bytes) return GEMM_F32_ERR_CAPTURE;
+        return graph_buffer(dev, stream, kGraphWorkspace, bytes, out);
+    }
     if (w.bytes < bytes) {
-        // growing synchronises the stream and allocates: not while capturing
-        if (capturing) return GEMM_F32_ERR_CAPTURE;
         if (w.ptr) {
             // earlier calls on this stream may still read the old buffer
             cudaError_t e = cudaStreamSynchronize(stream);
             if (e != cudaSuccess) return static_cast<int>(e);
-            if (w.captured)
-                w.retired.push_back(w.ptr);
-            else
-                cudaFree(w.ptr);
+            cudaFree(w.ptr);
             w.ptr = nullptr;
             w.bytes = 0;
-            w.captured = false;
         }
         const size_t grow = static_cast<size_t>(round_up(static_cast<long long>(bytes), 1 << 20));
         if (injected(GEMM_F32_INJECT_WORKSPACE) || cudaMalloc(&w.ptr, grow) != cudaSuccess) {
@@ -189,9 +284,10 @@ int workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
         }
         w.bytes = grow;
     }
-    if (capturing) w.captured = true;
     *out = w.ptr;
     return GEMM_F32_SUCCESS;
+} catch (const std::bad_alloc&) {
+    return GEMM_F32_ERR_WORKSPACE;
 }
 
 struct Plan {
@@ -1690,11 +1786,14 @@ int gemm_f32_release(void) {
         if (e != cudaSuccess && status == GEMM_F32_SUCCESS) status = static_cast<int>(e);
         cudaFree(kv.second.ptr);
     }
-    for (auto& kv : g_ws) {
-        cudaSetDevice(kv.first.first);
-        for (void* p : kv.second.retired) cudaFree(p);
-    }
     g_ws.clear();
+    for (GraphBuffer& b : g_graph_buffers) {
+        cudaSetDevice(b.dev);
+        cudaError_t e = cudaDeviceSynchronize();
+        if (e != cudaSuccess && status == GEMM_F32_SUCCESS) status = static_cast<int>(e);
+        cudaFree(b.ptr);
+    }
+    g_graph_buffers.clear();
     for (auto& kv : g_pipes) {
         HostPipe& hp = kv.second;
         cudaSetDevice(kv.first.first);
