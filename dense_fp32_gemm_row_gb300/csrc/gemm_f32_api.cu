@@ -1183,20 +1183,21 @@ struct HostPipe {
     cudaEvent_t ev_start = nullptr, ev_b = nullptr, ev_done = nullptr;
     cudaEvent_t ev_a[kMaxPanels] = {}, ev_c[kMaxPanels] = {};
     cudaEvent_t ev_bblk[kMaxColBlocks] = {}, ev_cblk[kMaxColBlocks] = {};
-    void* dev_buf = nullptr;  // device copies of A, B and C
+    void* dev_buf = nullptr;  // device copies of A, B and C, of calls not captured
     size_t dev_bytes = 0;
-    bool captured = false;          // as for Workspace
-    std::vector<void*> retired;
 };
 std::map<std::pair<int, cudaStream_t>, HostPipe> g_pipes;
 
-// Side streams, events and the device copies for (dev, stream); g_mutex held.
-int host_pipe(int dev, cudaStream_t stream, size_t bytes, HostPipe** out) {
+// Side streams and events for (dev, stream), and room for the device copies;
+// g_mutex held.
+int host_pipe(int dev, cudaStream_t stream, size_t bytes, HostPipe** out, void** copies) try {
     HostPipe& hp = g_pipes[std::make_pair(dev, stream)];
     cudaError_t e = cudaSuccess;
-    const bool capturing = stream_capturing(stream);
-    if ((!hp.ready || hp.dev_bytes < bytes) && capturing) return GEMM_F32_ERR_CAPTURE;
-    if (capturing) hp.captured = true;
+    if (stream_capturing(stream)) {
+        if (!hp.ready || hp.dev_bytes < bytes) return GEMM_F32_ERR_CAPTURE;
+        *out = &hp;
+        return graph_buffer(dev, stream, kGraphHostCopies, bytes, copies);
+    }
     if (!hp.ready) {
         const unsigned fl = cudaEventDisableTiming;
         if ((e = cudaStreamCreateWithFlags(&hp.s_in, cudaStreamNonBlocking)) != cudaSuccess ||
@@ -1218,13 +1219,9 @@ int host_pipe(int dev, cudaStream_t stream, size_t bytes, HostPipe** out) {
     if (hp.dev_bytes < bytes) {
         if (hp.dev_buf) {
             if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return static_cast<int>(e);
-            if (hp.captured)
-                hp.retired.push_back(hp.dev_buf);
-            else
-                cudaFree(hp.dev_buf);
+            cudaFree(hp.dev_buf);
             hp.dev_buf = nullptr;
             hp.dev_bytes = 0;
-            hp.captured = false;
         }
         if (injected(GEMM_F32_INJECT_WORKSPACE) || cudaMalloc(&hp.dev_buf, bytes) != cudaSuccess) {
             cudaGetLastError();
@@ -1234,7 +1231,10 @@ int host_pipe(int dev, cudaStream_t stream, size_t bytes, HostPipe** out) {
         hp.dev_bytes = bytes;
     }
     *out = &hp;
+    *copies = hp.dev_buf;
     return GEMM_F32_SUCCESS;
+} catch (const std::bad_alloc&) {
+    return GEMM_F32_ERR_WORKSPACE;
 }
 
 // Deep K: K panels.  Panel k of A (M x Kp, a strided 2-D copy from the host)
@@ -1329,12 +1329,13 @@ int run_host(const float* A, const float* B, float* C, int M, int N, int K, int 
     const size_t bytes_b = static_cast<size_t>(round_up(static_cast<long long>(K) * N * 4, 256));
     const size_t bytes_c = static_cast<size_t>(round_up(static_cast<long long>(M) * N * 4, 256));
     HostPipe* hp = nullptr;
-    if ((st = host_pipe(dev, stream, bytes_a + bytes_b + bytes_c, &hp)) != GEMM_F32_SUCCESS)
+    void* copies = nullptr;
+    if ((st = host_pipe(dev, stream, bytes_a + bytes_b + bytes_c, &hp, &copies)) !=
+        GEMM_F32_SUCCESS)
         return st;
-    float* dA = static_cast<float*>(hp->dev_buf);
-    float* dB = reinterpret_cast<float*>(static_cast<unsigned char*>(hp->dev_buf) + bytes_a);
-    float* dC = reinterpret_cast<float*>(static_cast<unsigned char*>(hp->dev_buf) + bytes_a +
-                                         bytes_b);
+    float* dA = static_cast<float*>(copies);
+    float* dB = reinterpret_cast<float*>(static_cast<unsigned char*>(copies) + bytes_a);
+    float* dC = reinterpret_cast<float*>(static_cast<unsigned char*>(copies) + bytes_a + bytes_b);
 
     if (kpanels) {
         cudaError_t e0 = cudaEventRecord(hp->ev_start, stream);
@@ -1800,7 +1801,6 @@ int gemm_f32_release(void) {
         cudaError_t e = cudaDeviceSynchronize();
         if (e != cudaSuccess && status == GEMM_F32_SUCCESS) status = static_cast<int>(e);
         if (hp.dev_buf) cudaFree(hp.dev_buf);
-        for (void* p : hp.retired) cudaFree(p);
         if (hp.ready) {
             cudaStreamDestroy(hp.s_in);
             cudaStreamDestroy(hp.s_out);

@@ -41,15 +41,13 @@
  * stream's workspace (or the host entry's device copies); neither is done
  * during a capture, so such a call returns GEMM_F32_ERR_CAPTURE without
  * enqueuing anything.  Issue each captured call once on the same stream
- * before capturing it.  A captured call does not use the stream's workspace:
- * it gets one that belongs to its graph, shared by the calls that the capture
- * takes from one stream, so graphs may be replayed on any streams, at the
- * same time as one another and as calls on the stream of the capture.  When
- * the graph and the executables made from it are destroyed, that memory
- * serves later captures; gemm_f32_release() frees it: do not release while a
- * graph that holds such a call may still be replayed.  (The host entry's
- * device copies are the stream's in a captured call too: replays of such
- * graphs have to be ordered with one another and with that stream's calls.)
+ * before capturing it.  A captured call does not use the stream's workspace
+ * and device copies: it gets some that belong to its graph, shared by the
+ * calls that the capture takes from one stream, so graphs may be replayed on
+ * any streams, at the same time as one another and as calls on the stream of
+ * the capture.  When the graph and the executables made from it are
+ * destroyed, that memory serves later captures; gemm_f32_release() frees it:
+ * do not release while a graph that holds such a call may still be replayed.
  *
  * Errors: 0 is success.  Negative values are library errors (GEMM_F32_ERR_*),
  * positive values are the cudaError_t of the failing CUDA runtime call.  No

@@ -69,6 +69,21 @@ class PaddedProduct(SplitProduct):
         self.a = t.cat([t.zeros(1, device="cuda"), self.a.flatten()])[1:].view(256, 32768)
 
 
+class HostProduct:
+    """C = A B from host buffers through copies on the device, by row panels or by panels of K."""
+
+    def __init__(self, seed, shape):
+        t = _gpu.torch()
+        gen = t.Generator().manual_seed(seed)
+        self.shape = M, N, K = shape
+        self.a, self.b = (t.randn(s, generator=gen).pin_memory() for s in ((M, K), (K, N)))
+        self.out = t.empty((M, N)).pin_memory()
+
+    def call(self, stream):
+        g.check(g.gemm_f32_host(self.a.data_ptr(), self.b.data_ptr(), self.out.data_ptr(), *self.shape,
+                                stream=stream.cuda_stream), "gemm_f32_host")
+
+
 def captured(case, stream):
     t = _gpu.torch()
     t.cuda.synchronize()
@@ -120,6 +135,24 @@ def test_a_graph_replayed_beside_calls_on_its_stream(kind):
             with t.cuda.stream(other):
                 graph.replay()
             cases[1].call(source)
+        t.cuda.synchronize()
+        for case, w in zip(cases, want):
+            assert t.equal(case.out, w)
+            case.out.fill_(float("nan"))
+
+
+@pytest.mark.parametrize("shape", [(2304, 1100, 1024), (2048, 2048, 2048)])
+def test_captured_host_calls_replayed_at_once(shape):
+    t = _gpu.torch()
+    source, left, right = t.cuda.Stream(), t.cuda.Stream(), t.cuda.Stream()
+    cases = [HostProduct(seed, shape) for seed in (1, 2, 3)]
+    want = answers(cases, source)
+    graphs = [captured(case, source) for case in cases[:2]]
+    for _ in range(10):
+        for graph, stream in zip(graphs, (left, right)):
+            with t.cuda.stream(stream):
+                graph.replay()
+        cases[2].call(source)
         t.cuda.synchronize()
         for case, w in zip(cases, want):
             assert t.equal(case.out, w)
