@@ -17,7 +17,7 @@
 #include <memory>
 #include <mutex>
 #include <new>
-#include <utility>
+#include <tuple>
 #include <vector>
 
 #include "gemm_f32.h"
@@ -42,6 +42,36 @@ struct DeviceState {
     cudaStream_t zeroing = nullptr;  // clears graph buffers, never captured
 };
 
+// A host thread, for as long as it runs.
+struct Thread {
+    unsigned long long number;  // never used again
+    std::shared_ptr<std::atomic<bool>> ended = std::make_shared<std::atomic<bool>>(false);
+    ~Thread() { ended->store(true); }
+};
+const Thread& this_thread() {
+    static std::atomic<unsigned long long> last{0};
+    thread_local Thread thread{++last};
+    return thread;
+}
+
+// Whose buffers a stream's are.  cudaStreamPerThread is one handle for a
+// stream of every host thread.
+struct StreamKey {
+    int dev;
+    cudaStream_t stream;
+    unsigned long long thread;  // 0: the handle alone names the stream
+    std::shared_ptr<std::atomic<bool>> ended;  // of that thread, whose stream went with it
+    bool operator<(const StreamKey& o) const {
+        return std::tie(dev, stream, thread) < std::tie(o.dev, o.stream, o.thread);
+    }
+    bool operator==(const StreamKey& o) const { return !(*this < o) && !(o < *this); }
+    bool gone() const { return ended && ended->load(); }
+};
+StreamKey key_of(int dev, cudaStream_t stream) {
+    if (stream != cudaStreamPerThread) return {dev, stream, 0, nullptr};
+    return {dev, stream, this_thread().number, this_thread().ended};
+}
+
 struct Workspace {
     void* ptr = nullptr;
     size_t bytes = 0;
@@ -61,14 +91,14 @@ struct GraphBuffer {
     size_t bytes;
     int use;  // GraphUse
     unsigned long long capture;
-    cudaStream_t stream;
+    StreamKey stream;
     std::shared_ptr<std::atomic<bool>> over;  // set by the destructor: free for another capture
 };
 enum GraphUse { kGraphWorkspace, kGraphHostCopies };
 
 std::mutex g_mutex;
 DeviceState g_dev[kMaxDevices];
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+std::map<StreamKey, Workspace> g_ws;
 std::vector<GraphBuffer> g_graph_buffers;
 EncodeTiledFn g_encode = nullptr;
 
@@ -198,12 +228,13 @@ int graph_buffer(int dev, cudaStream_t stream, GraphUse use, size_t bytes, void*
     if (e != cudaSuccess) return static_cast<int>(e);
     if (status != cudaStreamCaptureStatusActive)
         return static_cast<int>(cudaErrorStreamCaptureInvalidated);
+    const StreamKey key = key_of(dev, stream);
     GraphBuffer* b = nullptr;  // the smallest of those that no graph holds
     for (GraphBuffer& x : g_graph_buffers) {
         if (x.dev != dev || x.use != use || x.bytes < bytes) continue;
         if (x.over->load()) {
             if (!b || x.bytes < b->bytes) b = &x;
-        } else if (x.capture == capture && x.stream == stream) {
+        } else if (x.capture == capture && x.stream == key) {
             *out = x.ptr;
             return GEMM_F32_SUCCESS;
         }
@@ -211,7 +242,7 @@ int graph_buffer(int dev, cudaStream_t stream, GraphUse use, size_t bytes, void*
     RelaxedCapture relaxed;
     if (!b) {
         const size_t size = static_cast<size_t>(round_up(static_cast<long long>(bytes), 1 << 20));
-        GraphBuffer made = {dev, nullptr, size, use, 0, nullptr,
+        GraphBuffer made = {dev, nullptr, size, use, 0, key,
                             std::make_shared<std::atomic<bool>>(true)};
         g_graph_buffers.reserve(g_graph_buffers.size() + 1);
         if (injected(GEMM_F32_INJECT_WORKSPACE) || cudaMalloc(&made.ptr, size) != cudaSuccess) {
@@ -246,14 +277,34 @@ int graph_buffer(int dev, cudaStream_t stream, GraphUse use, size_t bytes, void*
     }
     cudaGetLastError();
     b->capture = capture;
-    b->stream = stream;
+    b->stream = key;
     *out = b->ptr;
     return GEMM_F32_SUCCESS;
 }
 
+// Frees the workspaces of per-thread streams whose thread has ended, before
+// another is made; g_mutex must be held.
+void free_ended(int dev) {
+    bool synchronised = false;
+    for (auto it = g_ws.begin(); it != g_ws.end();) {
+        if (it->first.dev != dev || !it->first.gone()) {
+            ++it;
+            continue;
+        }
+        // what the thread enqueued may still run
+        if (!synchronised && cudaDeviceSynchronize() != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        synchronised = true;
+        cudaFree(it->second.ptr);
+        it = g_ws.erase(it);
+    }
+}
+
 // Workspace of at least `bytes` for (dev, stream); g_mutex must be held.
 int workspace(int dev, cudaStream_t stream, size_t bytes, void** out) try {
-    Workspace& w = g_ws[std::make_pair(dev, stream)];
+    Workspace& w = g_ws[key_of(dev, stream)];
     if (stream_capturing(stream)) {
         // the call has been issued on the stream before: everything else that
         // it sets up is there
@@ -261,6 +312,7 @@ int workspace(int dev, cudaStream_t stream, size_t bytes, void** out) try {
         return graph_buffer(dev, stream, kGraphWorkspace, bytes, out);
     }
     if (w.bytes < bytes) {
+        if (!w.ptr) free_ended(dev);
         if (w.ptr) {
             // earlier calls on this stream may still read the old buffer
             cudaError_t e = cudaStreamSynchronize(stream);
@@ -1186,12 +1238,48 @@ struct HostPipe {
     void* dev_buf = nullptr;  // device copies of A, B and C, of calls not captured
     size_t dev_bytes = 0;
 };
-std::map<std::pair<int, cudaStream_t>, HostPipe> g_pipes;
+std::map<StreamKey, HostPipe> g_pipes;
+
+void destroy(HostPipe& hp) {
+    if (hp.dev_buf) cudaFree(hp.dev_buf);
+    if (!hp.ready) return;
+    cudaStreamDestroy(hp.s_in);
+    cudaStreamDestroy(hp.s_out);
+    cudaEventDestroy(hp.ev_start);
+    cudaEventDestroy(hp.ev_b);
+    cudaEventDestroy(hp.ev_done);
+    for (int i = 0; i < kMaxPanels; ++i) {
+        cudaEventDestroy(hp.ev_a[i]);
+        cudaEventDestroy(hp.ev_c[i]);
+    }
+    for (int i = 0; i < kMaxColBlocks; ++i) {
+        cudaEventDestroy(hp.ev_bblk[i]);
+        cudaEventDestroy(hp.ev_cblk[i]);
+    }
+}
+
+// As free_ended, for these.
+void destroy_ended(int dev) {
+    bool synchronised = false;
+    for (auto it = g_pipes.begin(); it != g_pipes.end();) {
+        if (it->first.dev != dev || !it->first.gone()) {
+            ++it;
+            continue;
+        }
+        if (!synchronised && cudaDeviceSynchronize() != cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        synchronised = true;
+        destroy(it->second);
+        it = g_pipes.erase(it);
+    }
+}
 
 // Side streams and events for (dev, stream), and room for the device copies;
 // g_mutex held.
 int host_pipe(int dev, cudaStream_t stream, size_t bytes, HostPipe** out, void** copies) try {
-    HostPipe& hp = g_pipes[std::make_pair(dev, stream)];
+    HostPipe& hp = g_pipes[key_of(dev, stream)];
     cudaError_t e = cudaSuccess;
     if (stream_capturing(stream)) {
         if (!hp.ready || hp.dev_bytes < bytes) return GEMM_F32_ERR_CAPTURE;
@@ -1199,6 +1287,7 @@ int host_pipe(int dev, cudaStream_t stream, size_t bytes, HostPipe** out, void**
         return graph_buffer(dev, stream, kGraphHostCopies, bytes, copies);
     }
     if (!hp.ready) {
+        destroy_ended(dev);
         const unsigned fl = cudaEventDisableTiming;
         if ((e = cudaStreamCreateWithFlags(&hp.s_in, cudaStreamNonBlocking)) != cudaSuccess ||
             (e = cudaStreamCreateWithFlags(&hp.s_out, cudaStreamNonBlocking)) != cudaSuccess ||
@@ -1782,7 +1871,7 @@ int gemm_f32_release(void) {
     int status = GEMM_F32_SUCCESS;
     for (auto& kv : g_ws) {
         if (!kv.second.ptr) continue;
-        cudaSetDevice(kv.first.first);
+        cudaSetDevice(kv.first.dev);
         cudaError_t e = cudaDeviceSynchronize();
         if (e != cudaSuccess && status == GEMM_F32_SUCCESS) status = static_cast<int>(e);
         cudaFree(kv.second.ptr);
@@ -1796,26 +1885,10 @@ int gemm_f32_release(void) {
     }
     g_graph_buffers.clear();
     for (auto& kv : g_pipes) {
-        HostPipe& hp = kv.second;
-        cudaSetDevice(kv.first.first);
+        cudaSetDevice(kv.first.dev);
         cudaError_t e = cudaDeviceSynchronize();
         if (e != cudaSuccess && status == GEMM_F32_SUCCESS) status = static_cast<int>(e);
-        if (hp.dev_buf) cudaFree(hp.dev_buf);
-        if (hp.ready) {
-            cudaStreamDestroy(hp.s_in);
-            cudaStreamDestroy(hp.s_out);
-            cudaEventDestroy(hp.ev_start);
-            cudaEventDestroy(hp.ev_b);
-            cudaEventDestroy(hp.ev_done);
-            for (int i = 0; i < kMaxPanels; ++i) {
-                cudaEventDestroy(hp.ev_a[i]);
-                cudaEventDestroy(hp.ev_c[i]);
-            }
-            for (int i = 0; i < kMaxColBlocks; ++i) {
-                cudaEventDestroy(hp.ev_bblk[i]);
-                cudaEventDestroy(hp.ev_cblk[i]);
-            }
-        }
+        destroy(kv.second);
     }
     g_pipes.clear();
     cudaSetDevice(prev);

@@ -31,8 +31,10 @@
  * them after the call returns.  Every call is asynchronous on `stream`
  * (enqueue and return; no implicit synchronisation).  The library owns a
  * workspace per (device, stream), grown on demand: a call that must grow it
- * synchronises that stream first.  gemm_f32_release() frees all of it.
- * The entry points are thread-safe.
+ * synchronises that stream first.  cudaStreamPerThread counts as a stream of
+ * each host thread (whose workspace goes once the thread has ended and another
+ * thread's is made).  gemm_f32_release() frees all of it.  The entry points
+ * are thread-safe.
  *
  * CUDA graphs: the calls that take a stream can be captured from it
  * (cudaStreamBeginCapture) and replayed; the graph keeps the pointers,
