@@ -51,12 +51,26 @@ Q8_ALGOS = {"auto": 0, "ffma": 1, "3xbf16": ALGO_3XBF16, "3xbf16_pair": ALGO_3XB
 ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
 
 
+_INT_MAX = 2 ** 31 - 1  # ctypes passes on the low 32 bits of an int that is larger
+
+
+def _int(value, what):
+    """``value``, which the library takes as an int of 32 bits."""
+    if not -_INT_MAX <= value <= _INT_MAX:
+        raise ValueError(f"{what} must be below 2^31, not {value}")
+    return value
+
+
 class Q8Struct(ctypes.Structure):
     """``gemm_f32_q8`` of the C header."""
 
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("ldcodes", ctypes.c_longlong), ("ldscales", ctypes.c_longlong),
                 ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("format", ctypes.c_int)]
+
+    def __init__(self, codes=None, scales=None, ldcodes=0, ldscales=0, rows=0, cols=0, format=0):
+        super().__init__(codes, scales, ldcodes, ldscales, _int(rows, "rows"), _int(cols, "cols"),
+                         format)
 
 
 # ---- raw entry points: addresses and the stream are plain integers --------------------------
@@ -71,6 +85,8 @@ def gemm_f32_q8_restore(q, X, ldx, type=Q8_TO_F32, stream=0) -> int:
 
 
 def gemm_f32_q8_wgrad(x, dY, lddy, N, alpha, beta, dW, lddw, algo=0, splits=0, stream=0) -> int:
+    if abs(N) > _INT_MAX or abs(splits) > _INT_MAX:
+        return _g.ERR_INVALID_VALUE
     return _g.load().gemm_f32_q8_wgrad(x, dY or None, lddy, N, alpha, beta, dW or None, lddw, algo,
                                        splits, stream or None)
 
@@ -199,6 +215,8 @@ class Q8:
             raise ValueError("codes and scales must be on one device")
         (rows, width), (rows2, width2) = codes.shape, scales.shape
         blocks = (cols + 31) >> 5
+        _int(rows, "the rows of codes")
+        _int(cols, "cols")
         if cols < 0 or rows2 != rows or width < cols or width2 < blocks:
             raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
         (ldc, one), (lds, one2) = codes.stride(), scales.stride()
@@ -254,6 +272,8 @@ def _matrix(t, what):
 
 def _strides(t, what):
     rows, cols = t.shape
+    if rows > _INT_MAX or cols > _INT_MAX:
+        raise ValueError(f"{what} must have fewer than 2^31 rows and columns, not {rows} x {cols}")
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1 and rows:
         raise ValueError(f"{what} must have contiguous rows")
@@ -311,6 +331,8 @@ def q8_empty(rows, cols, format="int8", device="cuda") -> Q8:
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError("a checkpoint is made on a CUDA device")
+    _int(rows, "rows")
+    _int(cols, "cols")
     with torch.cuda.device(device):
         return _make(torch.cuda.current_device(), rows, cols, format)
 
@@ -402,7 +424,7 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     else:
         dw, ldw = out, _like(out, q.cols, N, device, "out")
     st = _lib.gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(), ldw,
-                                code, splits, _stream_of(device))
+                                code, _int(splits, "splits"), _stream_of(device))
     if st:
         _g.check(st, "q8_wgrad")
     return dw
