@@ -411,6 +411,7 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     if rows != q.rows:
         raise ValueError(f"dy must have {q.rows} rows, not {rows}")
     code = _name(Q8_ALGOS, algo, "algo")
+    _int(splits, "splits")
     device = q.device
     if dy.get_device() != device:
         raise ValueError("all tensors must be on one device")
@@ -424,7 +425,7 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     else:
         dw, ldw = out, _like(out, q.cols, N, device, "out")
     st = _lib.gemm_f32_q8_wgrad(q.struct, dy.data_ptr(), ldy, N, alpha, beta, dw.data_ptr(), ldw,
-                                code, _int(splits, "splits"), _stream_of(device))
+                                code, splits, _stream_of(device))
     if st:
         _g.check(st, "q8_wgrad")
     return dw
