@@ -286,6 +286,9 @@ def matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None):
             raise ValueError("A and B must be contiguous float32 CUDA tensors")
     M, K = A.shape
     N = B.shape[1]
+    for value in (M, N, K, int(splits)):
+        if abs(value) >= 2 ** 31:  # ctypes would pass on its low 32 bits
+            raise ValueError(f"sizes and splits must be below 2^31, not {value}")
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
     elif out.shape != (M, N) or out.dtype != torch.float32 or not out.is_contiguous():

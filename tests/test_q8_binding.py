@@ -74,6 +74,21 @@ def test_checkpoints_beyond_32_bits(size):
     assert checkpoint(2 ** 31 - 1, 1).struct.rows == 2 ** 31 - 1
 
 
+def test_product_beyond_32_bits():
+    class Contiguous(Memory):
+        def is_contiguous(self):
+            return True
+
+    def f(rows, cols):
+        return Contiguous((rows, cols), torch.float32)
+
+    for a, b in ((f(WIDE, 1), f(1, 1)), (f(1, 1), f(1, WIDE)), (f(1, WIDE), f(WIDE, 1))):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            g.matmul(a, b)
+    with pytest.raises(ValueError, match=r"2\^31"):
+        g.matmul(f(1, 1), f(1, 1), splits=2 ** 32 + 1)
+
+
 def test_raw_arguments_beyond_32_bits():
     q = g.Q8Struct(0x7000_0000_0000, 0x7100_0000_0000, 16, 16, 1, 1, 0)
     for N, splits in ((WIDE, 0), (-WIDE, 0), (8, 2 ** 32 + 1)):
