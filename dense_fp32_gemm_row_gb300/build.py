@@ -8,14 +8,16 @@ Each ``csrc/*.cu`` translation unit is compiled in parallel into
 and the objects are linked, with the static CUDA runtime, into
 ``dense_fp32_gemm_row_gb300/libgemmf32.so``.  ``csrc/binding/tensors.cpp``, the
 Python binding's fast path for the 8-bit operators, is built with g++ against the
-installed torch into ``dense_fp32_gemm_row_gb300/_tensors.so``; the binding works
-without it, so a torch it cannot be built for is only reported.
+installed torch into ``dense_fp32_gemm_row_gb300/_tensors`` with this Python's suffix
+for extension modules, and names that torch's version; the binding works without it,
+so a torch it cannot be built for is only reported.
 """
 
 from __future__ import annotations
 
 import argparse
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -29,7 +31,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemmf32.so")
 TENSORS_SRC = os.path.join(CSRC, "binding", "tensors.cpp")
-TENSORS = os.path.join(PKG, "_tensors.so")
+TENSORS = os.path.join(PKG, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
+TENSORS_FOR = os.path.join(BUILD, "tensors.txt")  # the torch that TENSORS was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -73,32 +76,58 @@ def _compile(nvcc: str, src: str, force: bool) -> str:
     return obj
 
 
+def _torch_version(torch_dir: str) -> str:
+    """``torch.__version__`` of the torch in a folder, without importing it; "" if there is none."""
+    try:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            found = re.search(r"^__version__ = ['\"]([\w.+-]+)['\"]", f.read(), re.M)
+    except OSError:
+        return ""
+    return found.group(1) if found else ""
+
+
 def _build_tensors(force: bool) -> None:
-    """Build the binding's module for the installed torch, if there is one."""
+    """Build the binding's module for the installed torch, if there is one.
+
+    The module reads torch's objects by their layout in its headers, so one that was
+    built for another torch is removed, whether or not it can be replaced.
+    """
     import importlib.util
 
     spec = importlib.util.find_spec("torch")
-    if spec is None or spec.origin is None:
-        return
-    torch_dir = os.path.dirname(spec.origin)
-    # the build this module belongs to: another torch's headers are another module
-    version_file = os.path.join(torch_dir, "version.py")
-    if not force and not _stale(TENSORS, [TENSORS_SRC, version_file, *_headers(), __file__]):
+    torch_dir = os.path.dirname(spec.origin) if spec is not None and spec.origin else ""
+    version = _torch_version(torch_dir)
+    made_for = f"{version} {torch_dir}"
+    if not force and not _stale(TENSORS, [TENSORS_SRC, *_headers(), __file__]):
+        if os.path.exists(TENSORS_FOR):
+            with open(TENSORS_FOR) as f:
+                if f.read() == made_for:
+                    return
+    for old in (TENSORS, TENSORS_FOR, os.path.join(PKG, "_tensors.so")):
+        if os.path.exists(old):
+            os.remove(old)
+    if not version:
         return
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
     tmp = TENSORS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=1",
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", include,
+           f'-DTENSORS_TORCH="{version}"', "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", include,
            "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
            TENSORS_SRC, "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode == 0:
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        failed = res.stderr[-2000:] if res.returncode else ""
+    except OSError as e:  # no g++
+        failed = str(e)
+    if not failed:
         os.replace(tmp, TENSORS)
+        with open(TENSORS_FOR, "w") as f:
+            f.write(made_for)
     else:
-        print(f"{TENSORS} not built, every call of an 8-bit operator goes step by step in Python:\n{res.stderr[-2000:]}",
+        print(f"{TENSORS} not built, every call of an 8-bit operator goes step by step in Python:\n{failed}",
               file=sys.stderr)
 
 

@@ -25,6 +25,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <cstring>
 #include <new>
 #include <optional>
 
@@ -225,10 +226,17 @@ bool call(const char* where, F f) {
 
 // ---- the functions -------------------------------------------------------------
 
-// bind(store, restore, wgrad, gated, gated_backward, check, type): the library's
-// addresses, and what the binding gives
+// bind(store, restore, wgrad, gated, gated_backward, check, type, torch): the
+// library's addresses, what the binding gives, and the version of the torch
+// that is running, which has to be the one whose headers this was built with
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (!count(n, 7)) return nullptr;
+    if (!count(n, 8)) return nullptr;
+    const char* running = PyUnicode_AsUTF8(args[7]);
+    if (!running) return nullptr;
+    if (std::strcmp(running, TENSORS_TORCH) != 0) {
+        PyErr_Format(PyExc_ImportError, "built for torch %s, not %s", TENSORS_TORCH, running);
+        return nullptr;
+    }
     void* p[5];
     for (int i = 0; i < 5; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;

@@ -137,13 +137,13 @@ def _load_torch():
     _lib = _g.load()
     try:
         from dense_fp32_gemm_row_gb300 import _tensors
-    except ImportError:  # not built, or for another torch
-        pass
-    else:
+
         _tensors.bind(*(ctypes.cast(getattr(_lib, "gemm_f32_q8_" + name), ctypes.c_void_p).value
                         for name in ("store", "restore", "wgrad", "gated", "gated_backward")),
-                      _g.check, Q8)
+                      _g.check, Q8, str(torch.__version__))
         _native = _tensors
+    except ImportError:  # not built, or for another torch
+        _native = None
     _one_device = torch.cuda.device_count() <= 1
     _torch = torch
     return torch
