@@ -309,6 +309,8 @@ def _elsewhere(call, device, stream, tensors):
     """``call()`` on ``device`` and ``stream``, whose results then belong to that stream, with the
     tensors it reads or writes kept from reuse until it has run.  None: nothing to switch."""
     torch = _torch
+    if stream is not None and stream.device.index != device:
+        raise ValueError("the stream must be on the tensors' device")
     if stream is not None and stream != torch.cuda.current_stream(device):
         with torch.cuda.stream(stream):
             result = call()

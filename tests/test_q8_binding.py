@@ -50,6 +50,19 @@ def checkpoint(rows, cols):
                 Memory((rows, -(-cols // 512) * 16), torch.uint8), cols)
 
 
+def test_a_stream_of_another_device():
+    """Entering it would make its device the current one, and the call run on the other's stream."""
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    x, q = floats(8, 64), checkpoint(8, 64)
+    for call in (lambda: g.q8_store(x, stream=Stream), lambda: g.q8_restore(q, stream=Stream),
+                 lambda: g.q8_wgrad(q, x, stream=Stream), lambda: g.q8_gated(x, x, stream=Stream),
+                 lambda: g.q8_gated_backward(q, q, x, stream=Stream)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
 # ---- sizes that the library's 32-bit arguments cannot hold ----------------------------------------
 
 
