@@ -48,17 +48,18 @@ struct Library {
 // ---- checkpoints ---------------------------------------------------------------
 
 // A checkpoint's arrays and what keeps them: one tensor of bytes made here, or
-// the two tensors that the checkpoint was made of.
+// the two tensors that the checkpoint was made of.  Whoever has these tensors
+// can give them other memory, so q is only as good as the last live().
 struct Held {
     PyObject_HEAD
     gemm_f32_q8 q;
     int device;
-    at::Tensor bytes;          // the arrays lie in it, or
+    at::Tensor bytes;          // the arrays lie in it, from `at`, or
     at::Tensor codes, scales;  // are these
+    long long at;
 };
 PyTypeObject HeldType = {PyVarObject_HEAD_INIT(nullptr, 0)};
 
-bool is_held(PyObject* o) { return Py_TYPE(o) == &HeldType; }
 Held* held(PyObject* o) { return reinterpret_cast<Held*>(o); }
 
 Held* new_held(const gemm_f32_q8& q, int device) {
@@ -78,6 +79,55 @@ void held_dealloc(PyObject* self) {
     h->codes.~Tensor();
     h->scales.~Tensor();
     Py_TYPE(self)->tp_free(self);
+}
+
+// Whether a tensor's last row of `width` bytes lies in its memory.
+bool covers(const at::Tensor& t, long long width) {
+    const unsigned long long end = t.storage_offset() + (t.size(0) - 1) * t.stride(0) + width;
+    return t.storage().nbytes() >= end;
+}
+
+// The checkpoint of two byte tensors, if they are as one has to be.
+bool describe(const at::Tensor& c, const at::Tensor& s, long long cols, int format,
+              gemm_f32_q8* q) {
+    for (const at::Tensor* t : {&c, &s})
+        if (t->layout() != at::kStrided || !t->is_cuda() || t->scalar_type() != at::kByte ||
+            t->dim() != 2)
+            return false;
+    const long long rows = c.size(0), blocks = (cols + 31) >> 5;
+    if (rows < 2 || rows > INT_MAX || cols < 1 || cols > INT_MAX || s.size(0) != rows ||
+        c.size(1) < cols || s.size(1) < blocks || c.stride(1) != 1 || s.stride(1) != 1 ||
+        c.stride(0) < cols || s.stride(0) < blocks || c.device() != s.device() ||
+        !covers(c, cols) || !covers(s, blocks))
+        return false;
+    q->codes = static_cast<unsigned char*>(c.data_ptr());
+    q->scales = static_cast<unsigned char*>(s.data_ptr());
+    q->ldcodes = c.stride(0);
+    q->ldscales = s.stride(0);
+    q->rows = static_cast<int>(rows);
+    q->cols = static_cast<int>(cols);
+    q->format = format;
+    return ((reinterpret_cast<uintptr_t>(q->codes) | reinterpret_cast<uintptr_t>(q->scales) |
+             static_cast<uintptr_t>(q->ldcodes | q->ldscales)) & 15) == 0;
+}
+
+// Brings h->q up to where its tensors' memory is now; false if that is no
+// longer the checkpoint's.
+bool live(Held* h) {
+    if (!h->bytes.defined()) {
+        gemm_f32_q8 now;
+        if (!describe(h->codes, h->scales, h->q.cols, h->q.format, &now) ||
+            now.rows != h->q.rows || h->codes.device().index() != h->device)
+            return false;
+        h->q = now;
+        return true;
+    }
+    if (h->bytes.storage().nbytes() < static_cast<size_t>(h->bytes.numel())) return false;
+    unsigned char* base = static_cast<unsigned char*>(h->bytes.data_ptr());
+    if (!base) return true;  // no elements
+    h->q.codes = base + h->at;
+    h->q.scales = h->q.codes + h->q.rows * h->q.ldcodes;
+    return true;
 }
 
 // A row of codes and one of exponents, each padded to 16 bytes.
@@ -117,18 +167,15 @@ PyObject* checkpoint(const Ref& h) {
 
 // `n` uninitialised checkpoints of one layout in one allocation.
 void make(const gemm_f32_q8& shape, int device, int n, Ref* out) {
-    const long long codes = shape.rows * shape.ldcodes, each = codes + shape.rows * shape.ldscales;
+    const long long each = shape.rows * (shape.ldcodes + shape.ldscales);
     const int64_t size = n * each;
     const at::Tensor bytes = new_tensor(at::IntArrayRef(&size, 1), at::kByte, device);
-    unsigned char* at = static_cast<unsigned char*>(bytes.data_ptr());
     for (int i = 0; i < n; ++i) {
         Held* h = new_held(shape, device);
         out[i].p = reinterpret_cast<PyObject*>(h);
         h->bytes = bytes;
-        if (at) {
-            h->q.codes = at + i * each;
-            h->q.scales = h->q.codes + codes;
-        }
+        h->at = i * each;
+        live(h);
     }
 }
 
@@ -137,11 +184,10 @@ PyObject* held_tensors(PyObject* self, PyObject*) {
     HANDLE_TH_ERRORS
     Held* h = held(self);
     if (h->bytes.defined() && !h->codes.defined()) {
-        unsigned char* base = static_cast<unsigned char*>(h->bytes.data_ptr());
-        const long long at = base ? h->q.codes - base : 0, rows = h->q.rows;
-        h->codes = h->bytes.as_strided({rows, h->q.ldcodes}, {h->q.ldcodes, 1}, at);
+        const long long rows = h->q.rows;
+        h->codes = h->bytes.as_strided({rows, h->q.ldcodes}, {h->q.ldcodes, 1}, h->at);
         h->scales = h->bytes.as_strided({rows, h->q.ldscales}, {h->q.ldscales, 1},
-                                        at + rows * h->q.ldcodes);
+                                        h->at + rows * h->q.ldcodes);
     }
     Ref c{THPVariable_Wrap(h->codes)}, s{THPVariable_Wrap(h->scales)};
     return c.p && s.p ? PyTuple_Pack(2, c.p, s.p) : nullptr;
@@ -154,6 +200,10 @@ PyObject* held_number(PyObject* self, void*) {
 }
 template <unsigned char* gemm_f32_q8::* field>
 PyObject* held_address(PyObject* self, void*) {
+    if (!live(held(self))) {
+        PyErr_SetString(PyExc_ValueError, "the checkpoint's tensors no longer hold it");
+        return nullptr;
+    }
     return PyLong_FromVoidPtr(held(self)->q.*field);
 }
 PyObject* held_device(PyObject* self, void*) { return PyLong_FromLong(held(self)->device); }
@@ -172,6 +222,8 @@ PyGetSetDef held_fields[] = {
     {nullptr, nullptr, nullptr, nullptr, nullptr}};
 
 // ---- operands ------------------------------------------------------------------
+
+bool is_held(PyObject* o) { return Py_TYPE(o) == &HeldType && live(held(o)); }
 
 // A float32 CUDA matrix with contiguous rows on the current device.
 struct Matrix {
@@ -300,26 +352,8 @@ PyObject* wrap(PyObject*, PyObject* const* args, Py_ssize_t n) {
         Py_RETURN_NONE;
     if (!ints(args + 2, 2, v)) return nullptr;
     const at::Tensor &c = THPVariable_Unpack(args[0]), &s = THPVariable_Unpack(args[1]);
-    for (const at::Tensor* t : {&c, &s})
-        if (t->layout() != at::kStrided || !t->is_cuda() || t->scalar_type() != at::kByte ||
-            t->dim() != 2)
-            Py_RETURN_NONE;
-    const long long rows = c.size(0), cols = v[0], blocks = (cols + 31) >> 5;
-    if (rows < 2 || rows > INT_MAX || cols < 1 || cols > INT_MAX || s.size(0) != rows ||
-        c.size(1) < cols || s.size(1) < blocks || c.stride(1) != 1 || s.stride(1) != 1 ||
-        c.stride(0) < cols || s.stride(0) < blocks || c.device() != s.device())
-        Py_RETURN_NONE;
     gemm_f32_q8 q = {};
-    q.codes = static_cast<unsigned char*>(c.data_ptr());
-    q.scales = static_cast<unsigned char*>(s.data_ptr());
-    q.ldcodes = c.stride(0);
-    q.ldscales = s.stride(0);
-    if ((reinterpret_cast<uintptr_t>(q.codes) | reinterpret_cast<uintptr_t>(q.scales) |
-         static_cast<uintptr_t>(q.ldcodes | q.ldscales)) & 15)
-        Py_RETURN_NONE;
-    q.rows = static_cast<int>(rows);
-    q.cols = static_cast<int>(cols);
-    q.format = static_cast<int>(v[1]);
+    if (!describe(c, s, v[0], static_cast<int>(v[1]), &q)) Py_RETURN_NONE;
     Held* h = new_held(q, c.device().index());
     h->codes = c;
     h->scales = s;

@@ -149,20 +149,57 @@ def _load_torch():
     return torch
 
 
+def _layout(codes, scales, cols):
+    """(device, rows, row strides) of a checkpoint's two tensors, which are checked."""
+    if (codes.dtype is not _torch.uint8 or scales.dtype is not _torch.uint8 or codes.dim() != 2
+            or scales.dim() != 2 or not codes.is_cuda):
+        raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
+    if scales.get_device() != codes.get_device():
+        raise ValueError("codes and scales must be on one device")
+    (rows, width), (rows2, width2) = codes.shape, scales.shape
+    blocks = (cols + 31) >> 5
+    _int(rows, "the rows of codes")
+    _int(cols, "cols")
+    if cols < 0 or rows2 != rows or width < cols or width2 < blocks:
+        raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
+    (ldc, one), (lds, one2) = codes.stride(), scales.stride()
+    if rows <= 1:
+        ldc, lds = (width + 15) & ~15, (width2 + 15) & ~15
+    if rows and cols:
+        if (one != 1 or one2 != 1 or ldc < cols or lds < blocks
+                or (codes.data_ptr() | scales.data_ptr() | ldc | lds) & 15):
+            raise ValueError("codes and scales must have contiguous rows, 16-byte aligned bases "
+                             "and row strides that are multiples of 16")
+        for t, ld, n in ((codes, ldc, cols), (scales, lds, blocks)):
+            if t.storage_offset() + (rows - 1) * ld + n > t.untyped_storage().nbytes():
+                raise ValueError("codes and scales must have their memory")
+    return codes.get_device(), rows, ldc, lds
+
+
 class _Held:
     """Two tensors and their layout, as the module's objects of this name hold them."""
 
-    __slots__ = ("_tensors", "device", "rows", "cols", "format", "codes", "scales", "ldcodes",
-                 "ldscales")
+    __slots__ = ("_tensors", "device", "rows", "cols", "format", "ldcodes", "ldscales")
 
-    def __init__(self, codes, scales, ldcodes, ldscales, cols, format):
+    def __init__(self, codes, scales, cols, format):
         self._tensors = codes, scales
-        self.device, self.rows, self.cols = codes.get_device(), codes.shape[0], cols
-        self.codes, self.scales = codes.data_ptr(), scales.data_ptr()
-        self.ldcodes, self.ldscales, self.format = ldcodes, ldscales, format
+        self.cols, self.format = cols, format
+        self.device, self.rows, self.ldcodes, self.ldscales = _layout(codes, scales, cols)
 
     def tensors(self):
         return self._tensors
+
+    # whoever has the tensors can give them other memory: looked at again for every call
+    @property
+    def codes(self):
+        layout = self.device, self.rows, self.ldcodes, self.ldscales
+        if _layout(*self._tensors, self.cols) != layout:
+            raise ValueError("the checkpoint's tensors no longer hold it")
+        return self._tensors[0].data_ptr()
+
+    @property
+    def scales(self):
+        return self._tensors[1].data_ptr()
 
 
 def _empty(rows, cols, bf16, device):
@@ -180,7 +217,7 @@ def _make(device, rows, cols, format) -> Q8:
     codes, scales = (_torch.empty((rows, ld), dtype=_torch.uint8, device=f"cuda:{device}")
                      for ld in (ldc, lds))
     q = Q8.__new__(Q8)
-    q._held = _Held(codes, scales, ldc, lds, cols, Q8_FORMATS[format])
+    q._held = _Held(codes, scales, cols, Q8_FORMATS[format])
     return q
 
 
@@ -196,37 +233,22 @@ class Q8:
 
     ``codes`` is a (rows, >= cols) and ``scales`` a (rows, >= ceil(cols / 32))
     uint8 CUDA tensor; both start on 16-byte boundaries and have row strides
-    that are multiples of 16.  ``format`` is "int8" or "e4m3".
+    that are multiples of 16.  ``format`` is "int8" or "e4m3".  A call reads or
+    writes the memory that these tensors have at that time, and is refused when
+    it has become too small.
     """
 
     __slots__ = ("_held",)
 
     def __init__(self, codes, scales, cols, format="int8"):
-        u8 = (_torch or _load_torch()).uint8
+        if _torch is None:
+            _load_torch()
         fmt = _name(Q8_FORMATS, format, "format")
         if _native is not None:
             self._held = _native.wrap(codes, scales, cols, fmt)
             if self._held is not None:
                 return
-        if (codes.dtype is not u8 or scales.dtype is not u8 or codes.dim() != 2
-                or scales.dim() != 2 or not codes.is_cuda):
-            raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
-        if scales.get_device() != codes.get_device():
-            raise ValueError("codes and scales must be on one device")
-        (rows, width), (rows2, width2) = codes.shape, scales.shape
-        blocks = (cols + 31) >> 5
-        _int(rows, "the rows of codes")
-        _int(cols, "cols")
-        if cols < 0 or rows2 != rows or width < cols or width2 < blocks:
-            raise ValueError("codes must be (rows, >= cols), scales (rows, >= ceil(cols / 32))")
-        (ldc, one), (lds, one2) = codes.stride(), scales.stride()
-        if rows <= 1:
-            ldc, lds = (width + 15) & ~15, (width2 + 15) & ~15
-        if rows and cols and (one != 1 or one2 != 1 or ldc < cols or lds < blocks
-                              or (codes.data_ptr() | scales.data_ptr() | ldc | lds) & 15):
-            raise ValueError("codes and scales must have contiguous rows, 16-byte aligned bases "
-                             "and row strides that are multiples of 16")
-        self._held = _Held(codes, scales, ldc, lds, cols, fmt)
+        self._held = _Held(codes, scales, cols, fmt)
 
     rows = property(lambda self: self._held.rows)
     cols = property(lambda self: self._held.cols)
@@ -245,7 +267,8 @@ class Q8:
 
     @property
     def struct(self) -> Q8Struct:
-        """The checkpoint for the raw entry points; valid as long as this object."""
+        """The checkpoint for the raw entry points; valid as long as this object and the memory its
+        tensors have now."""
         h = self._held
         return Q8Struct(h.codes, h.scales, h.ldcodes, h.ldscales, h.rows, h.cols, h.format)
 

@@ -40,6 +40,15 @@ class Memory:
     def numel(self):
         return self.shape[0] * self.shape[1]
 
+    def storage_offset(self):
+        return 0
+
+    def untyped_storage(self):
+        return self
+
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
+
 
 def floats(rows, cols):
     return Memory((rows, cols), torch.float32)
