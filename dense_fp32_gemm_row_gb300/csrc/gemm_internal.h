@@ -198,10 +198,15 @@ struct Q8Out {
     unsigned char* scales;
     long long ldcodes, ldscales;
 };
+// where the elementwise kernels run
+struct Q8Launch {
+    cudaStream_t stream;
+    int sm_count;
+};
 cudaError_t launch_q8_store(const float* x, long long ldx, int rows, int cols, int format,
-                            const Q8Out& q, cudaStream_t s);
+                            const Q8Out& q, const Q8Launch& on);
 cudaError_t launch_q8_restore(const Q8In& q, int rows, int cols, int format, void* x,
-                              long long ldx, int bf16, cudaStream_t s);
+                              long long ldx, int bf16, const Q8Launch& on);
 struct GatedArgs {
     const float *g, *u;
     float* h;
@@ -209,7 +214,7 @@ struct GatedArgs {
     Q8Out gq, uq;
     int rows, cols, format, act;
 };
-cudaError_t launch_q8_gated(const GatedArgs& a, cudaStream_t s);
+cudaError_t launch_q8_gated(const GatedArgs& a, const Q8Launch& on);
 struct GatedBackwardArgs {
     Q8In gq, uq;
     const float* dh;
@@ -218,7 +223,7 @@ struct GatedBackwardArgs {
     Q8Out hq;  // codes null: not wanted
     int rows, cols, format, act;
 };
-cudaError_t launch_q8_gated_backward(const GatedBackwardArgs& a, cudaStream_t s);
+cudaError_t launch_q8_gated_backward(const GatedBackwardArgs& a, const Q8Launch& on);
 struct Q8WgradArgs {
     Q8In x;
     const float* dy;

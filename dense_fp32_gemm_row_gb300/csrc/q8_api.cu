@@ -248,7 +248,8 @@ int gemm_f32_q8_store(const float* X, long long ldx, const gemm_f32_q8* q, cudaS
     std::lock_guard<std::mutex> lock(api_mutex());
     CallState c;
     Q8_TRY(call_state(stream, &c));
-    return status(launch_q8_store(X, ldx, q->rows, q->cols, q->format, out_of(q), stream));
+    return status(launch_q8_store(X, ldx, q->rows, q->cols, q->format, out_of(q),
+                                  {stream, c.sm_count}));
 }
 
 int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
@@ -267,7 +268,7 @@ int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
     CallState c;
     Q8_TRY(call_state(stream, &c));
     return status(launch_q8_restore(in_of(q), q->rows, q->cols, q->format, X, ldx, elem == 2,
-                                    stream));
+                                    {stream, c.sm_count}));
 }
 
 int gemm_f32_q8_gated(int act, const float* G, long long ldg, const float* U, long long ldu,
@@ -292,7 +293,7 @@ int gemm_f32_q8_gated(int act, const float* G, long long ldg, const float* U, lo
     CallState c;
     Q8_TRY(call_state(stream, &c));
     GatedArgs a = {G, U, H, ldg, ldu, ldh, out_of(gq), out_of(uq), rows, cols, gq->format, act};
-    return status(launch_q8_gated(a, stream));
+    return status(launch_q8_gated(a, {stream, c.sm_count}));
 }
 
 int gemm_f32_q8_gated_backward(int act, const gemm_f32_q8* gq, const gemm_f32_q8* uq,
@@ -330,7 +331,7 @@ int gemm_f32_q8_gated_backward(int act, const gemm_f32_q8* gq, const gemm_f32_q8
     GatedBackwardArgs a = {in_of(gq), in_of(uq), dH, dG, dU, lddh, lddg, lddu,
                            hq ? out_of(hq) : Q8Out{nullptr, nullptr, 0, 0},
                            rows, cols, gq->format, act};
-    return status(launch_q8_gated_backward(a, stream));
+    return status(launch_q8_gated_backward(a, {stream, c.sm_count}));
 }
 
 int gemm_f32_q8_wgrad(const gemm_f32_q8* x, const float* dY, long long lddy, int N, float alpha,

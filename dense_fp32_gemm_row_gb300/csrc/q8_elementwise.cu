@@ -390,10 +390,11 @@ q8_gated_backward_kernel(Q8In gq, Q8In uq, const float* dh, long long lddh, unsi
 // many rounds as it takes (8192 x 8192: 64 an SM 51.5, 54.0, 137.6 and 162.3
 // us for store, restore, gated forward and backward; 8 an SM 53.2, 61.7, 155.1
 // and 161.5; 256 an SM 53.7, 73.9, 143.5 and 172.0).
-unsigned grid_for(int rows, int cols) {
+unsigned grid_for(int rows, int cols, int sm_count) {
     const long long items = static_cast<long long>(rows) * ((cols - 1) / kSegment + 1);
     const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-    return static_cast<unsigned>(blocks < 152 * kBlocksPerSm ? blocks : 152 * kBlocksPerSm);
+    const long long most = static_cast<long long>(sm_count) * kBlocksPerSm;
+    return static_cast<unsigned>(blocks < most ? blocks : most);
 }
 
 unsigned vectors(const void* p, long long ld, int rows) {
@@ -408,12 +409,12 @@ unsigned vectors_bf16(const void* p, long long ld, int rows) {
 // Launched as programmatic dependents: a kernel's launch overlaps the end of
 // the one before it, whose outputs it waits for.
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int rows, int cols, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kernel)(P...), int rows, int cols, const Q8Launch& on, A... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
-    cfg.gridDim = dim3(grid_for(rows, cols));
+    cfg.gridDim = dim3(grid_for(rows, cols, on.sm_count));
     cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
+    cfg.stream = on.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
@@ -422,65 +423,65 @@ cudaError_t launch(void (*kernel)(P...), int rows, int cols, cudaStream_t s, A..
 
 template <int FMT, typename T>
 cudaError_t restore(const Q8In& q, int rows, int cols, void* x, long long ldx, unsigned vec,
-                    cudaStream_t s) {
+                    const Q8Launch& on) {
     return launch(vec ? q8_restore_kernel<FMT, T, true> : q8_restore_kernel<FMT, T, false>, rows,
-                  cols, s, q, rows, cols, static_cast<T*>(x), ldx, vec);
+                  cols, on, q, rows, cols, static_cast<T*>(x), ldx, vec);
 }
 template <int FMT>
 cudaError_t store(const float* x, long long ldx, int rows, int cols, const Q8Out& q,
-                  cudaStream_t s) {
+                  const Q8Launch& on) {
     const unsigned vec = vectors(x, ldx, rows);
-    return launch(vec ? q8_store_kernel<FMT, true> : q8_store_kernel<FMT, false>, rows, cols, s, x,
+    return launch(vec ? q8_store_kernel<FMT, true> : q8_store_kernel<FMT, false>, rows, cols, on, x,
                   ldx, vec, rows, cols, q);
 }
 template <int FMT, int ACT>
-cudaError_t gated(const GatedArgs& a, cudaStream_t s) {
+cudaError_t gated(const GatedArgs& a, const Q8Launch& on) {
     const unsigned vg = vectors(a.g, a.ldg, a.rows), vu = vectors(a.u, a.ldu, a.rows),
                    vh = vectors(a.h, a.ldh, a.rows);
     return launch(
         vg && vu && vh ? q8_gated_kernel<FMT, ACT, true> : q8_gated_kernel<FMT, ACT, false>, a.rows,
-        a.cols, s, a.g, a.ldg, vg, a.u, a.ldu, vu, a.rows, a.cols, a.h, a.ldh, vh, a.gq, a.uq);
+        a.cols, on, a.g, a.ldg, vg, a.u, a.ldu, vu, a.rows, a.cols, a.h, a.ldh, vh, a.gq, a.uq);
 }
 template <int FMT, int ACT>
-cudaError_t gated_backward(const GatedBackwardArgs& a, cudaStream_t s) {
+cudaError_t gated_backward(const GatedBackwardArgs& a, const Q8Launch& on) {
     const unsigned vd = vectors(a.dh, a.lddh, a.rows), vg = vectors(a.dg, a.lddg, a.rows),
                    vu = vectors(a.du, a.lddu, a.rows);
     return launch(vd && vg && vu ? q8_gated_backward_kernel<FMT, ACT, true>
                                  : q8_gated_backward_kernel<FMT, ACT, false>,
-                  a.rows, a.cols, s, a.gq, a.uq, a.dh, a.lddh, vd, a.rows, a.cols, a.dg, a.lddg,
+                  a.rows, a.cols, on, a.gq, a.uq, a.dh, a.lddh, vd, a.rows, a.cols, a.dg, a.lddg,
                   vg, a.du, a.lddu, vu, a.hq);
 }
 
 }  // namespace
 
 cudaError_t launch_q8_store(const float* x, long long ldx, int rows, int cols, int format,
-                            const Q8Out& q, cudaStream_t s) {
-    return format == kQ8Int8 ? store<kQ8Int8>(x, ldx, rows, cols, q, s)
-                             : store<kQ8E4m3>(x, ldx, rows, cols, q, s);
+                            const Q8Out& q, const Q8Launch& on) {
+    return format == kQ8Int8 ? store<kQ8Int8>(x, ldx, rows, cols, q, on)
+                             : store<kQ8E4m3>(x, ldx, rows, cols, q, on);
 }
 
 cudaError_t launch_q8_restore(const Q8In& q, int rows, int cols, int format, void* x,
-                              long long ldx, int bf16, cudaStream_t s) {
+                              long long ldx, int bf16, const Q8Launch& on) {
     const unsigned vec = bf16 ? vectors_bf16(x, ldx, rows) : vectors(x, ldx, rows);
     if (format == kQ8Int8)
-        return bf16 ? restore<kQ8Int8, __nv_bfloat16>(q, rows, cols, x, ldx, vec, s)
-                    : restore<kQ8Int8, float>(q, rows, cols, x, ldx, vec, s);
-    return bf16 ? restore<kQ8E4m3, __nv_bfloat16>(q, rows, cols, x, ldx, vec, s)
-                : restore<kQ8E4m3, float>(q, rows, cols, x, ldx, vec, s);
+        return bf16 ? restore<kQ8Int8, __nv_bfloat16>(q, rows, cols, x, ldx, vec, on)
+                    : restore<kQ8Int8, float>(q, rows, cols, x, ldx, vec, on);
+    return bf16 ? restore<kQ8E4m3, __nv_bfloat16>(q, rows, cols, x, ldx, vec, on)
+                : restore<kQ8E4m3, float>(q, rows, cols, x, ldx, vec, on);
 }
 
-cudaError_t launch_q8_gated(const GatedArgs& a, cudaStream_t s) {
+cudaError_t launch_q8_gated(const GatedArgs& a, const Q8Launch& on) {
     if (a.format == kQ8Int8)
-        return a.act == kActSilu ? gated<kQ8Int8, kActSilu>(a, s) : gated<kQ8Int8, kActGelu>(a, s);
-    return a.act == kActSilu ? gated<kQ8E4m3, kActSilu>(a, s) : gated<kQ8E4m3, kActGelu>(a, s);
+        return a.act == kActSilu ? gated<kQ8Int8, kActSilu>(a, on) : gated<kQ8Int8, kActGelu>(a, on);
+    return a.act == kActSilu ? gated<kQ8E4m3, kActSilu>(a, on) : gated<kQ8E4m3, kActGelu>(a, on);
 }
 
-cudaError_t launch_q8_gated_backward(const GatedBackwardArgs& a, cudaStream_t s) {
+cudaError_t launch_q8_gated_backward(const GatedBackwardArgs& a, const Q8Launch& on) {
     if (a.format == kQ8Int8)
-        return a.act == kActSilu ? gated_backward<kQ8Int8, kActSilu>(a, s)
-                                 : gated_backward<kQ8Int8, kActGelu>(a, s);
-    return a.act == kActSilu ? gated_backward<kQ8E4m3, kActSilu>(a, s)
-                             : gated_backward<kQ8E4m3, kActGelu>(a, s);
+        return a.act == kActSilu ? gated_backward<kQ8Int8, kActSilu>(a, on)
+                                 : gated_backward<kQ8Int8, kActGelu>(a, on);
+    return a.act == kActSilu ? gated_backward<kQ8E4m3, kActSilu>(a, on)
+                             : gated_backward<kQ8E4m3, kActGelu>(a, on);
 }
 
 }  // namespace gemm_f32_impl
