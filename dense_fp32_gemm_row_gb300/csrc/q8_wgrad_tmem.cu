@@ -2,7 +2,7 @@
 // tensor core:  dW[d][n] = sum_t x^[t][d] dY[t][n].
 //
 // Arithmetic.  Every value of the checkpoint is exactly a bf16 number.  A
-// float of dY is exactly the sum of three: b0 its upper 16 bits, b1 the upper
+// float of dY (from 2^-110 up) is exactly the sum of three: b0 its upper 16 bits, b1 the upper
 // 16 bits of y - b0, b2 = y - b0 - b1 (8 significant bits each, truncated, so
 // the differences are exact).  Three bf16 MMAs a step, x^ b2 + x^ b1 + x^ b0,
 // thus form exact products of the fp32 values; what is rounded is the
@@ -10,9 +10,10 @@
 // addition (an error of about 2^-24 * 0.7 of the sum, always towards zero),
 // so a tensor-memory sum covers one chunk of tokens and is then added, with
 // rounding, into fp32 registers.  (Two bf16 parts would leave 2^-17 of each
-// product; TF32 parts need two MMAs at half the rate.)  Parts of dY below
-// 2^-126 are at the tensor core's mercy; an infinity in dY leaves a NaN part,
-// as in the 3xTF32 kernels, so it comes back as NaN.
+// product; TF32 parts need two MMAs at half the rate.)  The tensor core
+// takes denormal parts as they are, so what is lost of dY is what lies below
+// the least of them, 2^-133: nothing from 2^-110 up.  An infinity in dY leaves
+// a NaN part, as in the 3xTF32 kernels, so it comes back as NaN.
 //
 // Shape.  Both operands have the summed index, the token, as their slow
 // axis.  The MMA's A operand comes from tensor memory, one row per lane, and

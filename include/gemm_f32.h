@@ -423,7 +423,10 @@ int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
  * 256 x 128 by one CTA) chosen by size or, _PAIR and _SINGLE, forced;
  * GEMM_F32_ALGO_AUTO, all of this chosen by size.  splits:
  * for the tensor-core kernel, over how many ranges the tokens are split, as
- * for gemm_f32_algo_splitk (0: the library chooses).  With beta == 0 the old dW is not read; with alpha ==
+ * for gemm_f32_algo_splitk (0: the library chooses).
+ * The split of dY is exact down to 2^-110; what a smaller element has below
+ * 2^-133 is cut off (the CUDA-core kernel takes all of it).
+ * With beta == 0 the old dW is not read; with alpha ==
  * 0 or no rows, x and dY are not read and dW = beta * dW.  A NaN or infinity
  * in dY or a block of x that restores to NaN gives non-finite outputs in the
  * columns or rows of dW it enters.

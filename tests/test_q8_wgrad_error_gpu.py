@@ -114,3 +114,24 @@ def test_accumulation_over_micro_batches(form):
         dw = g.q8_wgrad(qi, device(dy[part]), out=dw, beta=0.0 if dw is None else 1.0, algo=form)
     # three sums of at most 256 fp32 additions or 24 truncations, and two additions of them
     check(dw, x, dy, (256 / 2, SHORT[1] + 2.0 ** -23))
+
+
+@pytest.mark.parametrize("form", FORMS + ("ffma",))
+@pytest.mark.parametrize("fmt", _q8.FORMATS)
+def test_gradients_near_the_least_floats(form, fmt):
+    """dY of 2^-110 and more enters exactly.  Below, its three parts hold it down to the least bf16
+    number, 2^-133: on the tensor core it is cut to a multiple of that; on the CUDA cores it is exact."""
+    T, D, N = 16, 32, 512
+    x = np.zeros((T, D), dtype=np.float32)
+    x[np.arange(T), np.arange(T)] = 2.0 ** 100  # so that what enters is seen in dW, which is normal
+    q = g.q8_store(device(x), format=fmt)
+    rng = np.random.default_rng(0)
+    for e in (-100, -109, -110, -111, -114, -118, -122, -126, -127, -131, -134, -149):
+        y = (rng.uniform(1, 2, (T, N)) * rng.choice([-1.0, 1.0], (T, N)) * 2.0 ** e).astype(np.float32)
+        enters = y.astype(np.float64)
+        if form != "ffma":
+            enters = np.trunc(enters * 2.0 ** 133) * 2.0 ** -133
+            assert e < -110 or np.array_equal(enters, y)
+        want = np.zeros((D, N))
+        want[:T] = enters * 2.0 ** 100
+        assert np.array_equal(g.q8_wgrad(q, device(y), algo=form).double().cpu().numpy(), want)
