@@ -19,7 +19,8 @@
 // what lies above it).  A power of two scales exactly, so the only rounding
 // is the one to the code (to nearest, ties to even), and every value has at
 // most 7 significant bits: it is exactly a bf16 number, which is how the
-// tensor-core product reads it.
+// tensor-core product reads it.  (E4M3 under E = 247 rounds to nearest beyond
+// the largest float: 248 * 2^120 and more, to 2^128, which reads as infinity.)
 //
 // E = 255 marks a block that holds a NaN or an infinity: its codes are 0 and
 // every element of it restores to NaN, so that an overflow in the forward

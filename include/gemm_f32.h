@@ -369,7 +369,9 @@ int gemm_f32_noalloc_selftest_watchdog(long long timeout_ns, cudaStream_t stream
  * for INT8 at most 254.  Codes are rounded to nearest, ties to even.  A block
  * that holds a NaN or an infinity gets E = 255 and codes 0, and all of it
  * restores to NaN.  An E below its least value reads as a scale of zero.
- * Every value is exactly representable in bf16.
+ * Every value is exactly representable in bf16.  (E4M3 rounds finite
+ * magnitudes of 248 * 2^120 = 3.296e38 and more to 2^128, which both types
+ * restore as an infinity.)
  *
  * Layout: row i's codes are at codes + i * ldcodes, its exponents at scales +
  * i * ldscales (bytes).  Both arrays are in device memory, 16-byte aligned,

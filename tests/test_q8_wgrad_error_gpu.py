@@ -135,3 +135,17 @@ def test_gradients_near_the_least_floats(form, fmt):
         want = np.zeros((D, N))
         want[:T] = enters * 2.0 ** 100
         assert np.array_equal(g.q8_wgrad(q, device(y), algo=form).double().cpu().numpy(), want)
+
+
+def test_e4m3_beyond_its_largest_float():
+    """248 * 2^120 and more rounds to 2^128: an infinity, which gradients do not hide."""
+    torch = t()
+    x = torch.ones(4, 64, device="cuda")
+    x[1, 3], x[2, 40] = 3.2e38, 3.4e38  # 248 * 2^120 is 3.2964e38
+    q = g.q8_store(x, format="e4m3")
+    for dtype in (torch.float32, torch.bfloat16):
+        back = g.q8_restore(q, dtype=dtype).float()
+        assert float(back[1, 3]) == 240 * 2.0 ** 120 and float(back[2, 40]) == float("inf")
+    dw = g.q8_wgrad(q, torch.ones(4, 8, device="cuda"))
+    assert not torch.isfinite(dw[40]).any() and torch.isfinite(dw[:3]).all()
+    assert torch.isfinite(g.q8_restore(g.q8_store(x))).all()  # int8 takes the nearest value it has
