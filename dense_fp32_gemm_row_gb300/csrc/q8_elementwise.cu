@@ -42,10 +42,13 @@ constexpr int kActGelu = 1;
 // F(a) = erfc(a / sqrt 2) e^(a^2/2) / 2 as a polynomial in t = 1 / (1 + 0.35 a)
 // without constant term (the form of Hastings, "Approximations for Digital
 // Computers", 1955).  The ten coefficients are a weighted least-squares fit
-// made for 0 <= a <= 14.5, refined towards equal relative errors: 2.2e-8
-// there, 2.5e-7 evaluated in fp32.  The derivative of gelu needs the same
-// exponential.  (erfcf and expf instead: 8192 x 8192 forward 164 us, backward
-// 193, bound by instructions.)
+// made for 0 <= a <= 14.5, refined towards equal relative errors: at most
+// 5.1e-8 with these coefficients, 3.3e-7 evaluated in fp32.  P(-a) itself has
+// that error and the one of the rounded a^2 / 2, which the exponential makes a
+// relative error of its own size: measured on gelu, at most 4.5e-7 for a < 2,
+// 5.6e-7 to 4, 1.3e-6 to 8, and 4.2e-6 to 13, where P is below 1e-15.  The
+// derivative of gelu needs the same exponential.  (erfcf and expf instead:
+// 8192 x 8192 forward 164 us, backward 193, bound by instructions.)
 __device__ __forceinline__ void normal(float z, float* p, float* bell) {
     const float a = fabsf(z);
     float t;

@@ -2,9 +2,9 @@
 // tensor core:  dW[d][n] = sum_t x^[t][d] dY[t][n].
 //
 // Arithmetic.  Every value of the checkpoint is exactly a bf16 number.  A
-// float of dY (from 2^-110 up) is exactly the sum of three: b0 its upper 16 bits, b1 the upper
-// 16 bits of y - b0, b2 = y - b0 - b1 (8 significant bits each, truncated, so
-// the differences are exact).  Three bf16 MMAs a step, x^ b2 + x^ b1 + x^ b0,
+// float of dY (from 2^-110 up) is exactly the sum of three: b0 its upper 16
+// bits, b1 the upper 16 bits of y - b0, b2 = y - b0 - b1 (8 significant bits
+// each, truncated, so the differences are exact).  Three bf16 MMAs a step, x^ b2 + x^ b1 + x^ b0,
 // thus form exact products of the fp32 values; what is rounded is the
 // accumulation.  The tensor core truncates its running fp32 sum at each
 // addition (an error of about 2^-24 * 0.7 of the sum, always towards zero),
