@@ -457,7 +457,12 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
 
 
 def q8_gated(gate, up, act="silu", format="int8", out=None, gate_q=None, up_q=None, stream=None):
-    """``h = act(gate) * up`` and the checkpoints of gate and up: ``(h, gate_q, up_q)``."""
+    """``h = act(gate) * up`` and the checkpoints of gate and up: ``(h, gate_q, up_q)``.
+
+    Two checkpoints made here may lie in one allocation, which is given back when both are gone
+    (and with it ``record_stream`` of one holds the other's memory too); made with
+    :func:`q8_empty` and given as ``gate_q`` and ``up_q`` they are apart.
+    """
     if _torch is None:
         _load_torch()
     code = _name(ACTS, act, "act")

@@ -383,7 +383,8 @@ int gemm_f32_noalloc_selftest_watchdog(long long timeout_ns, cudaStream_t stream
  * in elements, any 4-byte (bf16: 2-byte) alignment and any leading dimension
  * at least the row; an output may not share an element with an input or
  * another output (matrices side by side in one buffer, with equal leading
- * dimensions, are apart), else GEMM_F32_ERR_INVALID_VALUE; a matrix without
+ * dimensions, are apart; with different ones they count as sharing wherever
+ * their address ranges meet), else GEMM_F32_ERR_INVALID_VALUE; a matrix without
  * elements is a successful no-op; asynchronous on `stream`, with the status
  * codes, workspace and graph-capture rules above.  Results are deterministic.
  */
