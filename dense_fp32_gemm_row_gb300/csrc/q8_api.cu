@@ -113,16 +113,18 @@ long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
 
 // The tensor-core weight gradient's times in microseconds, fitted to calls
 // with each choice forced (a stage is 32 tokens of a tile): what a call takes
-// more than one of single CTAs; a stage of units that run through the tokens side by side and share operands in L2; of units
-// that are all at different tokens, with operands that fit L2 and beyond it;
-// the second kernel, and writing and adding one partial sum.
-// Measured, shared against whole: 4096 x 1280 x 2048 (40 tiles on 76 pairs)
-// 55.4 against 75.5 us, 4096 x 1536 x 2304 (54) 70.4 against 76.2, 4096 x 2048
-// x 2048 (64) 79.3 against 76.5, 16384 x 1280 x 2048 178 against 275, 16384 x
-// 2048 x 2048 287 against 277.  Single CTAs against pairs: 8192 x 8192 x 8192
-// 2.18 against 1.96 ms, 4096 x 2048 x 2048 83 against 76 us, 16384 x 8192 x 32
-// 82 against 149, 8192 x 4096 x 384 63 against 75, 64 x 512 x 512 7.0 against
-// 7.6.
+// more than one of single CTAs; a stage of units that run through the tokens
+// side by side and share operands in L2; of units that are all at different
+// tokens, with operands that fit L2 and beyond it; the second kernel, and
+// writing and adding one partial sum.
+// Measured in calls back to back, shared against whole: 4096 x 1280 x 2048 (40
+// tiles on 76 pairs) 52.8 against 72.2 us, 4096 x 1536 x 2304 (54) 66.9 against
+// 73.5, 16384 x 1280 x 2048 169 against 267; not taken, by the calls of the fit:
+// 4096 x 2048 x 2048 (64) 79.3 against 76.5, 16384 x 2048 x 2048 287 against
+// 277.  Single CTAs against pairs: 8192 x 8192 x 8192 2.20 against 2.00 ms, 4096
+// x 2048 x 2048 81 against 74 us, 16384 x 8192 x 32 81 against 139 to 150, 8192
+// x 4096 x 384 62 against 72, and replayed from a graph 64 x 512 x 512 6.3
+// against 6.8.  The old dW (beta) is not counted.
 struct WgradTimes {
     double more, stage, apart, far, sum, part;
 };
@@ -135,17 +137,21 @@ constexpr double kWgradL2Bytes = 64e6;
 constexpr double kWgradLeastGain = 0.05;
 
 // Stages per tensor-core sum, 256 tokens: relative error 7e-7 (2-norm; an fp32
-// product in one running sum has 1.6e-6 at 8192 tokens).  Each sum costs the
+// product in one running sum has 1.6e-6 at 8192 tokens, in sums over ranges
+// 5e-7 to 7e-7), most of it one way: 6e-7 towards zero.  Each sum costs the
 // MMAs a wait of ~0.23 us: 128 tokens, 4e-7, were 2.2 % slower at 8192 x 8192
 // x 8192, 512 tokens, 1.4e-6, 0.8 % faster.  Units of up to 512 tokens, where
-// an fp32 product has no more than 4e-7 either, pay for 128 with two waits.
+// an fp32 product has no more than 4e-7 either (2.1e-7 at 128 tokens, 2.9e-7 at
+// 256), pay for 128 with two waits.
 constexpr int kWgradChunk = 8, kWgradShortChunk = 4, kWgradShortStages = 16;
 
 // The CUDA-core kernel, which has no pipeline to fill and no descriptors, for
-// a few tokens and small outputs (measured, against the tensor-core kernel's
-// single CTAs, in microseconds: 16 x 512 x 512 5.6 and 6.3, 16 x 1024 x 1024
-// 5.7 and 6.6, 32 x 512 x 512 5.6 and 6.3, 24 x 300 x 300 6.1 and 6.8; but 4 x
-// 2048 x 2048 10.5 and 8.1, 64 x 512 x 512 8.3 and 7.0, 64 x 64 x 64 8.2 and 6).
+// a few tokens and small outputs (measured in calls back to back, against the
+// tensor-core kernel's single CTAs, in microseconds: 16 x 512 x 512 5.6 and 6.3,
+// 16 x 1024 x 1024 5.7 and 6.6, 32 x 512 x 512 5.6 and 6.3, 24 x 300 x 300 6.1
+// and 6.8; but 4 x 2048 x 2048 10.5 and 8.1, 64 x 512 x 512 8.3 and 7.0, 64 x 64
+// x 64 8.2 and 6; replayed from a graph, in the same order, 2.7 and 5.8, 3.9 and
+// 6.0, 3.7 and 5.8, 4.2 and 6.0, 9.0 and 7.3, 5.5 and 6.3, 5.4 and 5.3).
 constexpr int kFfmaTokens = 32;
 constexpr double kFfmaOutputs = 1 << 20, kFfmaProducts = 1.7e7;
 

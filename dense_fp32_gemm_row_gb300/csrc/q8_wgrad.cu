@@ -12,7 +12,8 @@
 // added into a second accumulator, so that the rounding error of a long sum
 // grows with the number of such chunks and not with the number of tokens.
 // It is for small calls (a few tokens, small outputs), which are bound by the
-// launch: 16 x 512 x 512 takes 5.6 us against 6.3 on the tensor core.
+// launch: 16 x 512 x 512 takes 5.6 us against 6.3 on the tensor core (replayed
+// from a graph 2.7 against 5.8).
 #include <cstdint>
 
 #include "device_sync.cuh"

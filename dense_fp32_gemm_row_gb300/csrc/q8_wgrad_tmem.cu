@@ -32,9 +32,9 @@
 // half its share; dY in shared memory as well (both operands, three parts)
 // would take more than the whole.  Or one CTA computes 256 x 128 (M = 128) and
 // holds all the features: it decodes and reads twice as much of x^ for the
-// same MMAs (8192 x 8192 x 8192 2.14 ms against 1.89), but wastes less of them
+// same MMAs (8192 x 8192 x 8192 2.12 ms against 1.89), but wastes less of them
 // on few or odd columns, is quicker to start, and has no partner to tell
-// (16384 x 8192 x 32 82 us against 149, 64 x 512 x 512 7.0 against 7.6).  In a
+// (16384 x 8192 x 32 81 us against 139, 64 x 512 x 512 6.3 against 6.8).  In a
 // tile with fewer features the MMAs are as much narrower.
 //
 // 640 threads per CTA, registers rebalanced at start (launched at 96 each):
@@ -59,8 +59,8 @@
 // What set the speed, 8192 x 8192 x 8192 (INT8), pairs: one relay lane for the
 // peer, whose release at cluster scope takes ~650 ns against 400 ns of MMAs a
 // stage, 2.69 ms; three relays and the separate rings 2.19; four decoder warps
-// instead of two, each of whose stores fills all banks, 1.89 (2.03 back to
-// back at the power limit).  With operands that are never rewritten the same
+// instead of two, each of whose stores fills all banks, 1.89 (2.00 to 2.04
+// back to back at the power limit).  With operands that are never rewritten the same
 // MMAs and copies take 1.70 ms; three bf16 products at the burst rate of the
 // library's product take 1.72, at its sustained rate 1.91.  4096 x 2048 x
 // 2048: 74.2 us, 64 tiles on 76 pairs, the tensor pipe busy 79 % of a CTA's

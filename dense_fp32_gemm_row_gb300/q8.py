@@ -423,7 +423,9 @@ def q8_wgrad(q, dy, out=None, alpha=1.0, beta=0.0, algo="auto", splits=0, stream
     must be given for ``beta`` other than 0 (gradient accumulation).  ``algo``
     is "auto", "ffma" or "3xbf16" (the tensor-core kernel; "3xbf16_pair" and
     "3xbf16_single" force its tiles), ``splits`` the number of ranges the
-    latter splits the tokens into (0: chosen by size).
+    latter splits the tokens into (0: chosen by size).  "ffma" sums with
+    rounding to nearest; the tensor core truncates (relative errors of 4e-7 up
+    to 512 tokens and 7e-7 beyond, nearly all towards zero).
     """
     if _torch is None:
         _load_torch()

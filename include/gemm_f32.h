@@ -79,8 +79,8 @@ extern "C" {
 /* the driver rejected a tensor-memory-access descriptor */
 #define GEMM_F32_ERR_DESCRIPTOR         (-5)
 /* the stream is being captured into a CUDA graph and the call would first
- * have to set up this device or allocate device memory (a larger workspace,
- * the host entry's device copies), which capture does not allow: issue the
+ * have to set up this device or the stream's buffers (a larger workspace, the
+ * host entry's device copies), which is not done during a capture: issue the
  * same call once on the stream before capturing it.  Nothing was enqueued. */
 #define GEMM_F32_ERR_CAPTURE            (-6)
 
@@ -429,6 +429,10 @@ int gemm_f32_q8_restore(const gemm_f32_q8* q, void* X, long long ldx, int type,
  * for gemm_f32_algo_splitk (0: the library chooses).
  * The split of dY is exact down to 2^-110; what a smaller element has below
  * 2^-133 is cut off (the CUDA-core kernel takes all of it).
+ * The tensor-core kernel's running sums are truncated, the CUDA-core kernel's
+ * rounded to nearest: measured 2-norm errors 2e-7 to 4e-7 (a unit of work of up
+ * to 512 tokens) or 7e-7 to 8e-7 (beyond), of which 1.5e-7 to 3e-7 or 6e-7
+ * towards zero, against 1e-7 to 4e-7 without a direction.
  * With beta == 0 the old dW is not read; with alpha ==
  * 0 or no rows, x and dY are not read and dW = beta * dW.  A NaN or infinity
  * in dY or a block of x that restores to NaN gives non-finite outputs in the
