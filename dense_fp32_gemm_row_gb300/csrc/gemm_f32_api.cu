@@ -270,12 +270,15 @@ int graph_buffer(int dev, cudaStream_t stream, GraphUse use, size_t bytes, void*
     if (cudaUserObjectCreate(&object, held.get(), graph_buffer_over, 1,
                              cudaUserObjectNoDestructorSync) == cudaSuccess) {
         held.release();  // the object's
-        if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) == cudaSuccess)
+        if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) == cudaSuccess) {
             b->over = over;
-        else
+        } else {
+            cudaGetLastError();
             cudaUserObjectRelease(object, 1);
+        }
+    } else {
+        cudaGetLastError();
     }
-    cudaGetLastError();
     b->capture = capture;
     b->stream = key;
     *out = b->ptr;

@@ -234,3 +234,40 @@ def test_a_capture_whose_workspace_cannot_be_had():
     again.replay()
     t.cuda.synchronize()
     assert t.equal(case.out, want)
+
+
+def test_a_graph_destroyed_while_it_runs():
+    """Its memory goes to no other graph before its last replay is done."""
+    t = _gpu.torch()
+    source, left = t.cuda.Stream(), t.cuda.Stream()
+    cases = [WeightGradient(10), WeightGradient(11)]
+    want = answers(cases, source)
+
+    def late(case, cycles):
+        # without the waits and the collection of torch.cuda.graph
+        graph = t.cuda.CUDAGraph()
+        with t.cuda.stream(source):
+            graph.capture_begin()
+            if cycles:
+                t.cuda._sleep(cycles)
+            case.call(source)
+            graph.capture_end()
+        return graph
+
+    t.cuda.synchronize()
+    t.cuda.empty_cache()
+    start = t.cuda.mem_get_info()[0]
+    first = late(cases[0], 400_000_000)
+    done = t.cuda.Event()
+    with t.cuda.stream(left):
+        first.replay()
+        done.record()
+    del first
+    second = late(cases[1], 0)
+    running = not done.query()
+    used = start - t.cuda.mem_get_info()[0]
+    assert not running or used >= 2 * WeightGradient.bytes
+    second.replay()
+    t.cuda.synchronize()
+    for case, w in zip(cases, want):
+        assert t.equal(case.out, w)
