@@ -200,11 +200,13 @@ PyObject* held_number(PyObject* self, void*) {
 }
 template <unsigned char* gemm_f32_q8::* field>
 PyObject* held_address(PyObject* self, void*) {
+    HANDLE_TH_ERRORS
     if (!live(held(self))) {
         PyErr_SetString(PyExc_ValueError, "the checkpoint's tensors no longer hold it");
         return nullptr;
     }
     return PyLong_FromVoidPtr(held(self)->q.*field);
+    END_HANDLE_TH_ERRORS
 }
 PyObject* held_device(PyObject* self, void*) { return PyLong_FromLong(held(self)->device); }
 

@@ -47,7 +47,8 @@
  * and device copies: it gets some that belong to its graph, shared by the
  * calls that the capture takes from one stream, so graphs may be replayed on
  * any streams, at the same time as one another and as calls on the stream of
- * the capture.  When the graph and the executables made from it are
+ * the capture (gemm_f32_noalloc's scratch is one for all calls: see there).
+ * When the graph and the executables made from it are
  * destroyed, that memory serves later captures; gemm_f32_release() frees it:
  * do not release while a graph that holds such a call may still be replayed.
  *

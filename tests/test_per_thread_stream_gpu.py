@@ -83,5 +83,5 @@ def test_what_ended_threads_held_is_given_back():
     start = t.cuda.mem_get_info()[0]
     for _ in range(12):
         in_threads(lambda case: case.call(PerThread), cases)
-    # the last thread's, and room for what the driver keeps of a thread
+    # the last thread's, and room for what CUDA keeps of a thread
     assert start - t.cuda.mem_get_info()[0] < 3 * WeightGradient.bytes
