@@ -17,7 +17,8 @@ Tensor convenience (torch CUDA tensors, float32, row-major contiguous)::
     matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None) -> C
 
 8-bit activation checkpoints and the operators that read them are in
-:mod:`dense_fp32_gemm_row_gb300.q8` and exported here.
+:mod:`dense_fp32_gemm_row_gb300.q8`, 8-bit integer linear layers in
+:mod:`dense_fp32_gemm_row_gb300.i8`; both are exported here.
 """
 
 from __future__ import annotations
@@ -149,6 +150,7 @@ def load():
                      "gemm_f32_version"):
             getattr(lib, name).restype = ctypes.c_int
         _q8._declare(lib)
+        _i8._declare(lib)
         _lib = lib
         return lib
 
@@ -304,4 +306,7 @@ def matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None):
 from dense_fp32_gemm_row_gb300 import q8 as _q8  # noqa: E402
 from dense_fp32_gemm_row_gb300.q8 import *  # noqa: E402,F401,F403
 
-__all__ += _q8.__all__
+from dense_fp32_gemm_row_gb300 import i8 as _i8  # noqa: E402
+from dense_fp32_gemm_row_gb300.i8 import *  # noqa: E402,F401,F403
+
+__all__ += _q8.__all__ + _i8.__all__

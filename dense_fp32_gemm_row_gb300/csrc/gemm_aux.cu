@@ -10,7 +10,8 @@
 //                    loads in flight), and few outputs with many partials
 //                    get one thread per output over a flat grid.
 //  * fill_zero:      C = 0 for K == 0 (the empty sum of the lecture-12
-//                    golden reference); scale_c: C = beta C for K == 0.
+//                    golden reference); scale_c: C = beta C for K == 0;
+//                    zero_rows: the same for outputs of any type.
 //  * transpose_pad:  a transposed copy, for operands stored the other way
 //                    round from what a kernel reads.
 //  * watchdog:       a self-test that waits on a barrier nothing completes.
@@ -200,6 +201,14 @@ __global__ void __launch_bounds__(kThreads) fill_zero_kernel(float* __restrict__
         C[i] = 0.0f;
 }
 
+__global__ void __launch_bounds__(kThreads)
+zero_rows_kernel(unsigned short* __restrict__ p, long long ld, long long rows, long long width) {
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y)
+        for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < width;
+             i += static_cast<long long>(gridDim.x) * kThreads)
+            p[r * ld + i] = 0;
+}
+
 __global__ void watchdog_selftest_kernel(unsigned* fault, long long timeout_ns) {
     __shared__ __align__(8) uint64_t bar;
     const uint32_t b = smem_addr(&bar);
@@ -294,6 +303,15 @@ cudaError_t launch_scale_c(float* C, long long ldc, int M, int N, float beta, cu
 cudaError_t launch_fill_zero(float* C, long long count, cudaStream_t s) {
     if (count <= 0) return cudaSuccess;
     fill_zero_kernel<<<grid_1d(count, kThreads, 4096), kThreads, 0, s>>>(C, count);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_zero_rows(void* p, long long ld, long long rows, long long width,
+                             cudaStream_t s) {
+    if (rows <= 0 || width <= 0) return cudaSuccess;
+    const dim3 grid(grid_1d(width / 2, kThreads, 64), grid_1d(rows, 1, 1024));
+    zero_rows_kernel<<<grid, kThreads, 0, s>>>(static_cast<unsigned short*>(p), ld / 2, rows,
+                                               width / 2);
     return cudaGetLastError();
 }
 

@@ -182,6 +182,9 @@ cudaError_t launch_transpose_pad(const float* src, long long lds, long long rows
 cudaError_t launch_scale_c(float* C, long long ldc, int M, int N, float beta, cudaStream_t s);
 // C[0 .. count) = 0
 cudaError_t launch_fill_zero(float* C, long long count, cudaStream_t s);
+// `rows` rows of `width` zero bytes, ld bytes apart, all three even
+cudaError_t launch_zero_rows(void* p, long long ld, long long rows, long long width,
+                             cudaStream_t s);
 // watchdog self-test: waits on a never-completed barrier for timeout_ns
 cudaError_t launch_watchdog_selftest(unsigned* fault, long long timeout_ns, cudaStream_t s);
 
@@ -297,6 +300,38 @@ struct Q8WgradTmemArgs {
     int mode;
 };
 cudaError_t launch_q8_wgrad_tmem(const Q8WgradTmemArgs& a, cudaStream_t s, int dev, int sm_count);
+
+// ---- 8-bit integer linear layers (i8_rows.cu, i8_dp4a.cu) ---------------------
+// Rows to codes (row stride ldq bytes) and scales: of x, or (w not null) of the
+// norm of s = x + r, which is written to s if that is not null.  All of one
+// type, r and s null or not as they are wanted.  No rows or columns: not called.
+struct I8RowsArgs {
+    const void *x, *r, *w;
+    void* s;
+    long long ldx, ldr, lds;
+    signed char* codes;
+    float* scales;
+    long long ldq;
+    int rows, cols, bf16;
+    float eps;
+};
+cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t s, int sm_count);
+// One operand's codes and scales, as the kernels take them.
+struct I8In {
+    const signed char* codes;
+    const float* scales;
+    long long ld;
+};
+// y = a b^T (T x N, row stride ldy elements), or, with c's codes not null, the
+// gated product act(a b^T) (a c^T).  type: kI8Float, kI8Bfloat16, kI8Int32 (not
+// gated).  T, N and K are not zero.
+struct I8ProductArgs {
+    I8In a, b, c;
+    void* y;
+    long long ldy;
+    int T, N, K, type, act;
+};
+cudaError_t launch_i8_dp4a(const I8ProductArgs& p, cudaStream_t s);
 
 // ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------
 // Device look-up and set-up, workspace and descriptors are one library-wide

@@ -1,0 +1,144 @@
+// i8_api.cu -- the C ABI of the 8-bit integer linear layers: argument checks,
+// the edge rules and kernel dispatch.  Empty matrices are a successful no-op,
+// as in the GEMM entry points; nothing here exits the process.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "arguments.h"
+#include "gemm_f32.h"
+#include "gemm_internal.h"
+
+using namespace gemm_f32_impl;
+
+#define I8_TRY(expr)                                  \
+    do {                                              \
+        const int st_ = (expr);                       \
+        if (st_ != GEMM_F32_SUCCESS) return st_;      \
+    } while (0)
+
+namespace {
+
+int check_shape(const gemm_f32_i8* q) {
+    return q && q->rows >= 0 && q->cols >= 0 ? GEMM_F32_SUCCESS : GEMM_F32_ERR_INVALID_VALUE;
+}
+
+// The arrays of a matrix with elements: codes 16-byte aligned with a row stride
+// that is a multiple of 16 bytes and holds a row.
+int check_arrays(const gemm_f32_i8* q) {
+    if (!q->codes || !q->scales) return GEMM_F32_ERR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(q->codes) & 15u) || (q->ld & 15) ||
+        (reinterpret_cast<uintptr_t>(q->scales) & 3u))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    return bad_dims(q->rows, q->cols, q->ld) ? GEMM_F32_ERR_INVALID_VALUE : GEMM_F32_SUCCESS;
+}
+
+Region codes_of(const gemm_f32_i8* q) { return region(q->codes, q->rows, q->cols, q->ld, 1); }
+Region scales_of(const gemm_f32_i8* q) { return region(q->scales, 1, q->rows, q->rows, 4); }
+I8In in_of(const gemm_f32_i8* q) { return {q->codes, q->scales, q->ld}; }
+
+int elem_of(int type) { return type == GEMM_F32_TYPE_BF16 ? 2 : 4; }
+bool is_float(int type) { return type == GEMM_F32_TYPE_F32 || type == GEMM_F32_TYPE_BF16; }
+
+// Both products: y = a b^T, or with c the gated product of b and c.
+int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, int act, void* Y,
+            int type, long long ldy, cudaStream_t stream) {
+    I8_TRY(check_shape(a));
+    I8_TRY(check_shape(b));
+    if (a->cols != b->cols || a->cols > GEMM_F32_I8_MAX_COLS) return GEMM_F32_ERR_INVALID_VALUE;
+    if (c) {
+        I8_TRY(check_shape(c));
+        if (c->rows != b->rows || c->cols != b->cols) return GEMM_F32_ERR_INVALID_VALUE;
+    }
+    const int T = a->rows, N = b->rows, K = a->cols;
+    if (T == 0 || N == 0) return GEMM_F32_SUCCESS;
+    I8_TRY(check_matrix(Y, T, N, ldy, elem_of(type)));
+    if (K > 0) {
+        I8_TRY(check_arrays(a));
+        I8_TRY(check_arrays(b));
+        if (c) I8_TRY(check_arrays(c));
+        const Region out[] = {region(Y, T, N, ldy, elem_of(type))};
+        const Region in[] = {codes_of(a), scales_of(a), codes_of(b), scales_of(b),
+                             c ? codes_of(c) : Region{}, c ? scales_of(c) : Region{}};
+        I8_TRY(check_apart(out, 1, in, 6));
+    }
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState s;
+    I8_TRY(call_state(stream, &s));
+    if (K == 0)
+        return status(launch_zero_rows(Y, ldy * elem_of(type), T,
+                                       static_cast<long long>(N) * elem_of(type), stream));
+    const I8ProductArgs p = {in_of(a), in_of(b), c ? in_of(c) : I8In{}, Y, ldy, T, N, K, type, act};
+    return status(launch_i8_dp4a(p, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_f32_i8_store(const void* X, int type, long long ldx, const gemm_f32_i8* q,
+                      cudaStream_t stream) {
+    if (!is_float(type)) return GEMM_F32_ERR_INVALID_VALUE;
+    I8_TRY(check_shape(q));
+    if (q->rows == 0 || q->cols == 0) return GEMM_F32_SUCCESS;
+    I8_TRY(check_arrays(q));
+    I8_TRY(check_matrix(X, q->rows, q->cols, ldx, elem_of(type)));
+    const Region out[] = {codes_of(q), scales_of(q)};
+    const Region in[] = {region(X, q->rows, q->cols, ldx, elem_of(type))};
+    I8_TRY(check_apart(out, 2, in, 1));
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState s;
+    I8_TRY(call_state(stream, &s));
+    I8RowsArgs a = {};
+    a.x = X;
+    a.ldx = ldx;
+    a.codes = q->codes;
+    a.scales = q->scales;
+    a.ldq = q->ld;
+    a.rows = q->rows;
+    a.cols = q->cols;
+    a.bf16 = type == GEMM_F32_TYPE_BF16;
+    return status(launch_i8_rows(a, stream, s.sm_count));
+}
+
+int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr, const void* W,
+                     float eps, int type, void* S, long long lds, const gemm_f32_i8* q,
+                     cudaStream_t stream) {
+    if (!is_float(type) || !(eps >= GEMM_F32_I8_LEAST_EPS) || !std::isfinite(eps) || (S && !R))
+        return GEMM_F32_ERR_INVALID_VALUE;
+    I8_TRY(check_shape(q));
+    const int rows = q->rows, cols = q->cols, elem = elem_of(type);
+    if (rows == 0 || cols == 0) return GEMM_F32_SUCCESS;
+    I8_TRY(check_arrays(q));
+    I8_TRY(check_matrix(X, rows, cols, ldx, elem));
+    I8_TRY(check_matrix(W, 1, cols, cols, elem));
+    if (R) I8_TRY(check_matrix(R, rows, cols, ldr, elem));
+    if (S) I8_TRY(check_matrix(S, rows, cols, lds, elem));
+    const Region out[] = {codes_of(q), scales_of(q), region(S, rows, cols, lds, elem)};
+    const Region in[] = {region(X, rows, cols, ldx, elem), region(R, rows, cols, ldr, elem),
+                         region(W, 1, cols, cols, elem)};
+    I8_TRY(check_apart(out, 3, in, 3));
+    std::lock_guard<std::mutex> lock(api_mutex());
+    CallState s;
+    I8_TRY(call_state(stream, &s));
+    const I8RowsArgs a = {X, R, W, S, ldx, ldr, lds, q->codes, q->scales, q->ld, rows, cols,
+                          type == GEMM_F32_TYPE_BF16, eps};
+    return status(launch_i8_rows(a, stream, s.sm_count));
+}
+
+int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int type,
+                       long long ldy, cudaStream_t stream) {
+    if (!is_float(type) && type != GEMM_F32_TYPE_I32) return GEMM_F32_ERR_INVALID_VALUE;
+    return product(a, b, nullptr, 0, Y, type, ldy, stream);
+}
+
+int gemm_f32_i8_gated(int act, const gemm_f32_i8* a, const gemm_f32_i8* gate,
+                      const gemm_f32_i8* up, void* H, int type, long long ldh,
+                      cudaStream_t stream) {
+    if ((act != GEMM_F32_ACT_SILU && act != GEMM_F32_ACT_GELU) || !is_float(type) || !up)
+        return GEMM_F32_ERR_INVALID_VALUE;
+    return product(a, gate, up, act, H, type, ldh, stream);
+}
+
+}  // extern "C"

@@ -468,6 +468,87 @@ int gemm_f32_q8_gated_backward(int act, const gemm_f32_q8* gq, const gemm_f32_q8
                                float* dU, long long lddu, const gemm_f32_q8* hq,
                                cudaStream_t stream);
 
+/* ---- 8-bit integer linear layers --------------------------------------- */
+/*
+ * The layers of a trained model as they are served: weights and activations in
+ * 8-bit integers with one fp32 scale a row, a row of activations being a token
+ * and a row of weights an output channel.  The pages have no counterpart: these
+ * serve the callers that use the product above to train such layers.  A gated
+ * block is norm, gated, store, matmul, in this order.
+ *
+ * The form: rows x cols codes -128 .. 127 and `rows` scales, value =
+ * code * scale[row].  Row i's codes are at codes + i * ld (bytes); codes are
+ * 16-byte aligned and ld is a multiple of 16, at least cols; bytes beyond a
+ * row's last column are neither read for their value nor written.  The scales
+ * are contiguous floats.  Both are in device memory and the caller's.
+ *
+ * What store and norm write for a row z: with a the larger of 2^-100 and z's
+ * largest magnitude, code = z * (127 / a) rounded to nearest, ties to even, and
+ * scale = a / 127, each operation rounded to fp32.  A row in which z is not
+ * finite gets codes 0 and scale NaN, so that its products are NaN.
+ *
+ * For all four entry points: float and bf16 matrices are row-major with leading
+ * dimensions in elements, aligned to their elements, with any leading dimension
+ * at least the row; outputs may not share an element with an input or another
+ * output, by the rules of the 8-bit checkpoints above; a matrix without rows or
+ * columns is a successful no-op; asynchronous on `stream`, with the status
+ * codes, workspace and graph-capture rules above.  Results are deterministic.
+ */
+#define GEMM_F32_TYPE_F32   0
+#define GEMM_F32_TYPE_BF16  1
+#define GEMM_F32_TYPE_I32   2
+typedef struct gemm_f32_i8 {
+    signed char* codes;
+    float* scales;
+    long long ld;
+    int rows;
+    int cols;
+} gemm_f32_i8;
+
+/* gemm_f32_i8_store -- write the rows of X (q->rows x q->cols, floats or bf16
+ * by type, row stride ldx) to q. */
+int gemm_f32_i8_store(const void* X, int type, long long ldx, const gemm_f32_i8* q,
+                      cudaStream_t stream);
+
+/*
+ * gemm_f32_i8_norm -- write to q the root-mean-square norm of S = X + R,
+ *
+ *     S / sqrt(mean(S^2) + eps) * W      (mean over a row, W one value a column)
+ *
+ * and S itself, the residual stream, to S unless that is NULL.  R NULL: the
+ * norm of X, and S must be NULL.  All are floats or all bf16 by type; sums are
+ * in fp32, and the norm is that of X + R before it is rounded to the type of S.
+ * z above is S * W: the norm's factor is the same for all columns and is
+ * multiplied into the scale alone (after a / 127).  eps is finite and at
+ * least 1e-30.
+ */
+#define GEMM_F32_I8_LEAST_EPS 1e-30f
+int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr, const void* W,
+                     float eps, int type, void* S, long long lds, const gemm_f32_i8* q,
+                     cudaStream_t stream);
+
+/*
+ * gemm_f32_i8_matmul -- Y = a b^T, T x N from T x K tokens a and N x K weights
+ * b: the integer sums of code products, exact whatever the sizes, times a's and
+ * then b's scale, each product rounded to fp32, as floats or bf16 by type; or
+ * with GEMM_F32_TYPE_I32 the sums themselves (the scales are then not read).
+ * K is at most GEMM_F32_I8_MAX_COLS, so that no sum overflows 32 bits; K = 0
+ * writes zeros.  A token's outputs do not depend on the other tokens of the
+ * call, bit for bit.
+ */
+#define GEMM_F32_I8_MAX_COLS 131071
+int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int type,
+                       long long ldy, cudaStream_t stream);
+
+/*
+ * gemm_f32_i8_gated -- both projections of a gated block and their product,
+ * H = act(a gate^T) * (a up^T), each as gemm_f32_i8_matmul gives it in fp32;
+ * act as for gemm_f32_q8_gated, type F32 or BF16.
+ */
+int gemm_f32_i8_gated(int act, const gemm_f32_i8* a, const gemm_f32_i8* gate,
+                      const gemm_f32_i8* up, void* H, int type, long long ldh,
+                      cudaStream_t stream);
+
 /* Release every workspace (synchronises each device that has one). */
 int gemm_f32_release(void);
 
