@@ -1217,11 +1217,11 @@ int call_workspace(const CallState& c, cudaStream_t stream, size_t bytes, unsign
 }
 
 int call_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long dim0,
-                    long long dim1, long long ld_bytes, int box0, int box1) {
+                    long long dim1, long long ld_bytes, int box0, int box1,
+                    CUtensorMapSwizzle swizzle) {
     const int st = get_encoder();
     if (st != GEMM_F32_SUCCESS) return st;
-    return encode_map(map, type, base, dim0, dim1, ld_bytes, box0, box1,
-                      CU_TENSOR_MAP_SWIZZLE_NONE);
+    return encode_map(map, type, base, dim0, dim1, ld_bytes, box0, box1, swizzle);
 }
 
 }  // namespace gemm_f32_impl

@@ -333,6 +333,42 @@ struct I8ProductArgs {
 };
 cudaError_t launch_i8_dp4a(const I8ProductArgs& p, cudaStream_t s);
 
+// The same on the tensor core (i8_tmem.cu): CTA pairs with tiles of 256 channels
+// x 2 `tokens`, or single CTAs with 128 x `tokens` (gated: half the channels),
+// `tokens` a multiple of 16, at most 128; single CTAs' tiles in `splits` ranges
+// of the stages of K.
+struct I8Share {
+    int tiles_c, tiles_t;  // tiles of channels and of tokens
+    int tokens;            // of a CTA
+    int stages;            // of one tile
+    int splits;            // not more than stages; 1 for pairs
+};
+struct I8Tile {
+    int channels, tokens, k;  // of a tile; of a CTA, at most; of a pipeline stage
+};
+I8Tile i8_tile(bool pair);
+// bytes of the splits' sums
+size_t i8_parts_bytes(const I8Share& s);
+// Codes as {K, rows} bytes with 64-byte swizzle: a's box 64 x tokens, b's (and
+// c's, gated) 64 x 128, or gated 64 x 64.
+struct I8TmemMaps {
+    CUtensorMap a, b, c;
+};
+struct I8TmemArgs {
+    const float *as, *bs, *cs;
+    void* y;
+    long long ldy;
+    int T, N, type;
+    I8Share share;
+    int* parts;     // the splits' sums
+    int* counters;  // one a tile, zero between calls
+    unsigned* fault;
+    long long timeout_ns;
+};
+// act: as for gated, or -1
+cudaError_t launch_i8_tmem(const I8TmemMaps& maps, const I8TmemArgs& a, bool pair, int act,
+                           cudaStream_t s, int dev, int sm_count);
+
 // ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------
 // Device look-up and set-up, workspace and descriptors are one library-wide
 // state; api_mutex() is held around them and the launches of a call.
@@ -347,7 +383,8 @@ int call_state(cudaStream_t stream, CallState* out);
 int call_workspace(const CallState& c, cudaStream_t stream, size_t bytes, unsigned char** out);
 // a 2-D tensor map: dim0 contiguous elements, dim1 rows ld_bytes apart
 int call_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long dim0,
-                    long long dim1, long long ld_bytes, int box0, int box1);
+                    long long dim1, long long ld_bytes, int box0, int box1,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 // gemm_f32_noalloc's fault word on device `dev` (0 if that entry point has
 // not set the device up); blocking read, zeroed afterwards when `clear`.

@@ -41,9 +41,50 @@ I8In in_of(const gemm_f32_i8* q) { return {q->codes, q->scales, q->ld}; }
 int elem_of(int type) { return type == GEMM_F32_TYPE_BF16 ? 2 : 4; }
 bool is_float(int type) { return type == GEMM_F32_TYPE_F32 || type == GEMM_F32_TYPE_BF16; }
 
+int map_codes(CUtensorMap* map, const gemm_f32_i8* q, int k, int rows) {
+    return call_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q->codes, q->cols, q->rows, q->ld, k,
+                           rows, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// How a product is shared out.
+I8Share share_out(int T, int N, int K, bool gated, int algo, int splits, int sm_count, bool* pair) {
+    I8Share s = {};
+    const auto tiles = [&](bool p, int tokens) {
+        const I8Tile t = i8_tile(p);
+        s.tokens = tokens;
+        s.tiles_c = (N - 1) / (gated ? t.channels / 2 : t.channels) + 1;
+        s.tiles_t = (T - 1) / (p ? 2 * tokens : tokens) + 1;
+        s.stages = (K - 1) / t.k + 1;
+        s.splits = 1;
+        return static_cast<long long>(s.tiles_c) * s.tiles_t;
+    };
+    *pair = algo == GEMM_F32_ALGO_I8_PAIR;
+    if (algo == GEMM_F32_ALGO_AUTO) *pair = tiles(true, 128) >= sm_count / 4;
+    if (*pair) {
+        int w = 128;
+        while (w > 16 && T <= w) w -= 16;
+        tiles(true, w);
+        return s;
+    }
+    int w = 128;
+    while (w > 16 && w - 16 >= T) w -= 16;
+    while (w > 32 && 2 * tiles(false, w) <= sm_count) w = (w / 2 + 15) / 16 * 16;
+    const long long n = tiles(false, w);
+    long long most = n * 8 <= kWorkspaceCounterBytes / 4 * 8 && n <= 1024 ? sm_count / n : 1;
+    if (splits > 0) most = n <= 1024 ? splits : 1;
+    else if (most > s.stages / 4) most = s.stages / 4;
+    if (most > s.stages) most = s.stages;
+    s.splits = most < 1 ? 1 : static_cast<int>(most);
+    return s;
+}
+
 // Both products: y = a b^T, or with c the gated product of b and c.
 int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, int act, void* Y,
-            int type, long long ldy, cudaStream_t stream) {
+            int type, long long ldy, int algo, int splits, cudaStream_t stream) {
+    if ((algo != GEMM_F32_ALGO_AUTO && algo != GEMM_F32_ALGO_I8_PAIR &&
+         algo != GEMM_F32_ALGO_I8_SINGLE) ||
+        splits < 0 || splits > GEMM_F32_MAX_SPLITS)
+        return GEMM_F32_ERR_INVALID_VALUE;
     I8_TRY(check_shape(a));
     I8_TRY(check_shape(b));
     if (a->cols != b->cols || a->cols > GEMM_F32_I8_MAX_COLS) return GEMM_F32_ERR_INVALID_VALUE;
@@ -69,8 +110,31 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     if (K == 0)
         return status(launch_zero_rows(Y, ldy * elem_of(type), T,
                                        static_cast<long long>(N) * elem_of(type), stream));
-    const I8ProductArgs p = {in_of(a), in_of(b), c ? in_of(c) : I8In{}, Y, ldy, T, N, K, type, act};
-    return status(launch_i8_dp4a(p, stream));
+    bool pair;
+    I8TmemArgs k = {};
+    k.share = share_out(T, N, K, c != nullptr, algo, splits, s.sm_count, &pair);
+    unsigned char* ws = nullptr;
+    if (k.share.splits > 1)
+        I8_TRY(call_workspace(s, stream, kWorkspaceCounterBytes + i8_parts_bytes(k.share), &ws));
+    const I8Tile tile = i8_tile(pair);
+    const int rows = c ? 64 : 128;
+    I8TmemMaps maps = {};
+    I8_TRY(map_codes(&maps.a, a, tile.k, k.share.tokens));
+    I8_TRY(map_codes(&maps.b, b, tile.k, rows));
+    if (c) I8_TRY(map_codes(&maps.c, c, tile.k, rows));
+    k.as = a->scales;
+    k.bs = b->scales;
+    k.cs = c ? c->scales : nullptr;
+    k.y = Y;
+    k.ldy = ldy;
+    k.T = T;
+    k.N = N;
+    k.type = type;
+    k.counters = reinterpret_cast<int*>(ws);
+    k.parts = reinterpret_cast<int*>(ws + kWorkspaceCounterBytes);
+    k.fault = s.fault;
+    k.timeout_ns = kDefaultTimeoutNs;
+    return status(launch_i8_tmem(maps, k, pair, c ? act : -1, stream, s.dev, s.sm_count));
 }
 
 }  // namespace
@@ -128,17 +192,17 @@ int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr,
 }
 
 int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int type,
-                       long long ldy, cudaStream_t stream) {
+                       long long ldy, int algo, int splits, cudaStream_t stream) {
     if (!is_float(type) && type != GEMM_F32_TYPE_I32) return GEMM_F32_ERR_INVALID_VALUE;
-    return product(a, b, nullptr, 0, Y, type, ldy, stream);
+    return product(a, b, nullptr, 0, Y, type, ldy, algo, splits, stream);
 }
 
 int gemm_f32_i8_gated(int act, const gemm_f32_i8* a, const gemm_f32_i8* gate,
-                      const gemm_f32_i8* up, void* H, int type, long long ldh,
-                      cudaStream_t stream) {
+                      const gemm_f32_i8* up, void* H, int type, long long ldh, int algo,
+                      int splits, cudaStream_t stream) {
     if ((act != GEMM_F32_ACT_SILU && act != GEMM_F32_ACT_GELU) || !is_float(type) || !up)
         return GEMM_F32_ERR_INVALID_VALUE;
-    return product(a, gate, up, act, H, type, ldh, stream);
+    return product(a, gate, up, act, H, type, ldh, algo, splits, stream);
 }
 
 }  // extern "C"

@@ -217,34 +217,6 @@ __device__ __forceinline__ void decode_bf16(uint32_t w, float scale, uint32_t& l
     hi = upper_halves(v.z * scale, v.w * scale);
 }
 
-// D += A B^T, A in tensor memory, for one CTA or (leader's thread) the pair.
-template <bool PAIR>
-__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate) {
-    if (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
-// Arrival on a barrier, in both CTAs of a pair, when the MMAs so far are done.
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar) {
-    if (PAIR)
-        mma_commit_pair_multicast(bar, 0x3);
-    else
-        mma_commit(bar);
-}
-
 // First feature and column of a tile: neighbouring tiles run down groups of 8
 // rows of tiles, so that the clusters at work share operands in L2.
 template <class C>
@@ -587,14 +559,14 @@ q8_wgrad_kernel(const __grid_constant__ Q8WgradMaps tmY, unsigned shifts,
                                 const uint64_t xk = x + static_cast<uint64_t>((k * C::UK * 128) >> 4);
                                 const uint32_t kc = static_cast<uint32_t>(k * C::UK / 2);
                                 const uint32_t acc = (kb > c0 || k > 0) ? 1u : 0u;
-                                mma_bf16_tmem_a<PAIR>(tmem_base, b2 + kc, xk, idesc, acc);
-                                mma_bf16_tmem_a<PAIR>(tmem_base, b1 + kc, xk, idesc, 1u);
-                                mma_bf16_tmem_a<PAIR>(tmem_base, b0 + kc, xk, idesc, 1u);
+                                mma_f16_tmem_a<PAIR>(tmem_base, b2 + kc, xk, idesc, acc);
+                                mma_f16_tmem_a<PAIR>(tmem_base, b1 + kc, xk, idesc, 1u);
+                                mma_f16_tmem_a<PAIR>(tmem_base, b0 + kc, xk, idesc, 1u);
                             }
-                            commit<PAIR>(empty0 + 8 * s);
+                            mma_commit_form<PAIR>(empty0 + 8 * s);
                         }
                         if (!ok) break;
-                        commit<PAIR>(accf);
+                        mma_commit_form<PAIR>(accf);
                     }
                 }
                 if (PAIR)

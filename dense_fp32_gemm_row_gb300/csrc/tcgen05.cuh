@@ -189,6 +189,35 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
         : "memory");
 }
 
+// D (+)= A B^T of 16-bit floats with A in tensor memory (one row a lane, two K
+// elements a column), for one CTA or (leader's thread) the pair.
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// Arrival on a barrier, in both CTAs of a pair, when the MMAs so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit_form(uint32_t bar) {
+    if (PAIR)
+        mma_commit_pair_multicast(bar, 0x3);
+    else
+        mma_commit(bar);
+}
+
 // ---- descriptors ---------------------------------------------------------
 // Shared-memory matrix descriptor of a K-major operand tile written by a
 // TMA load with 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes

@@ -25,6 +25,7 @@ from dense_fp32_gemm_row_gb300 import q8 as _q8
 
 __all__ = [
     "I8", "I8Struct", "TYPE_F32", "TYPE_BF16", "TYPE_I32", "I8_MAX_COLS", "I8_LEAST_EPS",
+    "ALGO_I8_PAIR", "ALGO_I8_SINGLE", "I8_ALGOS",
     "gemm_f32_i8_store", "gemm_f32_i8_norm", "gemm_f32_i8_matmul", "gemm_f32_i8_gated",
     "i8_empty", "i8_store", "i8_norm", "i8_matmul", "i8_gated",
 ]
@@ -34,6 +35,9 @@ TYPE_BF16 = 1
 TYPE_I32 = 2
 I8_MAX_COLS = 131071
 I8_LEAST_EPS = 1e-30
+ALGO_I8_PAIR = 6
+ALGO_I8_SINGLE = 7
+I8_ALGOS = {"auto": 0, "pair": ALGO_I8_PAIR, "single": ALGO_I8_SINGLE}
 
 
 class I8Struct(ctypes.Structure):
@@ -58,12 +62,13 @@ def gemm_f32_i8_norm(X, ldx, R, ldr, W, eps, type, S, lds, q, stream=0) -> int:
                                       lds, q, stream or None)
 
 
-def gemm_f32_i8_matmul(a, b, Y, type, ldy, stream=0) -> int:
-    return _g.load().gemm_f32_i8_matmul(a, b, Y or None, type, ldy, stream or None)
+def gemm_f32_i8_matmul(a, b, Y, type, ldy, algo=0, splits=0, stream=0) -> int:
+    return _g.load().gemm_f32_i8_matmul(a, b, Y or None, type, ldy, algo, splits, stream or None)
 
 
-def gemm_f32_i8_gated(act, a, gate, up, H, type, ldh, stream=0) -> int:
-    return _g.load().gemm_f32_i8_gated(act, a, gate, up, H or None, type, ldh, stream or None)
+def gemm_f32_i8_gated(act, a, gate, up, H, type, ldh, algo=0, splits=0, stream=0) -> int:
+    return _g.load().gemm_f32_i8_gated(act, a, gate, up, H or None, type, ldh, algo, splits,
+                                       stream or None)
 
 
 def _declare(lib) -> None:
@@ -71,8 +76,8 @@ def _declare(lib) -> None:
     q = ctypes.POINTER(I8Struct)
     lib.gemm_f32_i8_store.argtypes = [vp, i, ll, q, vp]
     lib.gemm_f32_i8_norm.argtypes = [vp, ll, vp, ll, vp, f, i, vp, ll, q, vp]
-    lib.gemm_f32_i8_matmul.argtypes = [q, q, vp, i, ll, vp]
-    lib.gemm_f32_i8_gated.argtypes = [i, q, q, q, vp, i, ll, vp]
+    lib.gemm_f32_i8_matmul.argtypes = [q, q, vp, i, ll, i, i, vp]
+    lib.gemm_f32_i8_gated.argtypes = [i, q, q, q, vp, i, ll, i, i, vp]
     for name in ("store", "norm", "matmul", "gated"):
         getattr(lib, "gemm_f32_i8_" + name).restype = ctypes.c_int
 
@@ -298,46 +303,54 @@ def _inputs(a, w):
     _on(w.device, a.device)
 
 
-def i8_matmul(a, w, dtype=None, out=None, stream=None):
+def i8_matmul(a, w, dtype=None, out=None, algo="auto", splits=0, stream=None):
     """``a @ w.T`` of tokens ``a`` and weights ``w`` (channels, inputs), both :class:`I8`.
 
     The sums over codes are exact; ``dtype`` is float32 (the default) or
-    bfloat16 for their values, or int32 for the sums themselves.
+    bfloat16 for their values, or int32 for the sums themselves.  ``algo``
+    ("pair" or "single" CTAs a tile) and ``splits`` (of single CTAs' tiles, over
+    K) are chosen by size; results do not depend on them.
     """
     torch = _torch or _load_torch()
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
     code = _type(dtype, "dtype", whole=True)
+    which = _q8._name(I8_ALGOS, algo, "algo")
+    _q8._int(splits, "splits")
     _inputs(a, w)
     device = a.device
     if stream is not None or _q8._away(device):
-        return _q8._elsewhere(lambda: i8_matmul(a, w, dtype, out), device, stream, (a, w, out))
+        return _q8._elsewhere(lambda: i8_matmul(a, w, dtype, out, algo, splits), device, stream, (a, w, out))
     qa, qw = a.struct, w.struct
     y, ldy = _output(a, w, dtype, out)
-    st = _q8._lib.gemm_f32_i8_matmul(qa, qw, y.data_ptr(), code, ldy, _q8._stream_of(device))
+    st = _q8._lib.gemm_f32_i8_matmul(qa, qw, y.data_ptr(), code, ldy, which, splits,
+                                     _q8._stream_of(device))
     if st:
         _g.check(st, "i8_matmul")
     return y
 
 
-def i8_gated(a, gate, up, act="silu", dtype=None, out=None, stream=None):
+def i8_gated(a, gate, up, act="silu", dtype=None, out=None, algo="auto", splits=0, stream=None):
     """``act(a @ gate.T) * (a @ up.T)`` of tokens ``a`` and two weights, all :class:`I8`, as
-    float32 (the default) or bfloat16; ``act`` is "silu" or "gelu"."""
+    float32 (the default) or bfloat16; ``act`` is "silu" or "gelu", ``algo`` and ``splits`` are as
+    for :func:`i8_matmul`."""
     torch = _torch or _load_torch()
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
     code = _type(dtype, "dtype")
     which = _q8._name(_q8.ACTS, act, "act")
+    how = _q8._name(I8_ALGOS, algo, "algo")
+    _q8._int(splits, "splits")
     _inputs(a, gate)
     _given(up, gate.rows, gate.cols, a.device, "up")
     device = a.device
     if stream is not None or _q8._away(device):
-        return _q8._elsewhere(lambda: i8_gated(a, gate, up, act, dtype, out), device, stream,
-                              (a, gate, up, out))
+        return _q8._elsewhere(lambda: i8_gated(a, gate, up, act, dtype, out, algo, splits), device,
+                              stream, (a, gate, up, out))
     qa, qg, qu = a.struct, gate.struct, up.struct
     h, ldh = _output(a, gate, dtype, out)
-    st = _q8._lib.gemm_f32_i8_gated(which, qa, qg, qu, h.data_ptr(), code, ldh,
-                                    _q8._stream_of(device))
+    st = _q8._lib.gemm_f32_i8_gated(which, qa, qg, qu, h.data_ptr(), code, ldh, how,
+                                    splits, _q8._stream_of(device))
     if st:
         _g.check(st, "i8_gated")
     return h

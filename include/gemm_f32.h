@@ -534,11 +534,17 @@ int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr,
  * with GEMM_F32_TYPE_I32 the sums themselves (the scales are then not read).
  * K is at most GEMM_F32_I8_MAX_COLS, so that no sum overflows 32 bits; K = 0
  * writes zeros.  A token's outputs do not depend on the other tokens of the
- * call, bit for bit.
+ * call, bit for bit.  algo: GEMM_F32_ALGO_AUTO, or this entry point's and
+ * gated's own: the tensor-core kernel with tiles of CTA pairs (I8_PAIR) or of
+ * single CTAs (I8_SINGLE), over how many ranges of K `splits` (at most
+ * GEMM_F32_MAX_SPLITS; 0: the library chooses) splits the latter.  Results do
+ * not depend on either.
  */
+#define GEMM_F32_ALGO_I8_PAIR    6
+#define GEMM_F32_ALGO_I8_SINGLE  7
 #define GEMM_F32_I8_MAX_COLS 131071
 int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int type,
-                       long long ldy, cudaStream_t stream);
+                       long long ldy, int algo, int splits, cudaStream_t stream);
 
 /*
  * gemm_f32_i8_gated -- both projections of a gated block and their product,
@@ -546,8 +552,8 @@ int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int 
  * act as for gemm_f32_q8_gated, type F32 or BF16.
  */
 int gemm_f32_i8_gated(int act, const gemm_f32_i8* a, const gemm_f32_i8* gate,
-                      const gemm_f32_i8* up, void* H, int type, long long ldh,
-                      cudaStream_t stream);
+                      const gemm_f32_i8* up, void* H, int type, long long ldh, int algo,
+                      int splits, cudaStream_t stream);
 
 /* Release every workspace (synchronises each device that has one). */
 int gemm_f32_release(void);

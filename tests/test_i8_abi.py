@@ -86,6 +86,9 @@ def test_bad_arguments_are_invalid():
         assert g.gemm_f32_i8_gated(0, q, w, w, y, 0, ld) == BAD
     for act in (-1, 2):
         assert g.gemm_f32_i8_gated(act, q, w, w, Z, 0, 7) == BAD
+    for algo, splits in ((-1, 0), (1, 0), (5, 0), (8, 0), (0, -1), (7, 257)):
+        assert g.gemm_f32_i8_matmul(q, w, Z, 0, 7, algo, splits) == BAD
+        assert g.gemm_f32_i8_gated(0, q, w, w, Z, 0, 7, algo, splits) == BAD
     # operands of one product have as many columns, those of a gated block one shape
     assert g.gemm_f32_i8_matmul(q, i8(cols=39, codes=W, scales=W + 0x10000), Z, 0, 4) == BAD
     assert g.gemm_f32_i8_gated(0, q, w, i8(rows=8, codes=W, scales=W + 0x10000), Z, 0, 7) == BAD
@@ -231,6 +234,8 @@ def test_types_and_shapes():
                  lambda: g.i8_store(x, out=matrix(8, 63)), lambda: g.i8_matmul(q, matrix(8, 63)),
                  lambda: g.i8_gated(q, q, matrix(9, 64)), lambda: g.i8_matmul(q, q, out=floats(8, 9)),
                  lambda: g.i8_matmul(q, q, dtype=torch.bfloat16, out=floats(8, 8)),
+                 lambda: g.i8_matmul(q, q, algo="ffma"), lambda: g.i8_gated(q, q, q, algo="ffma"),
+                 lambda: g.i8_matmul(q, q, algo="single", splits=2 ** 32 + 1),
                  lambda: g.i8_matmul(matrix(1, 131072), matrix(1, 131072)),
                  lambda: g.I8(q.codes, q.scales, 65), lambda: g.I8(q.codes, weight(9), 64),
                  lambda: g.I8(q.codes, weight(8, torch.float64), 64), lambda: g.I8(x, q.scales, 64),

@@ -254,6 +254,26 @@ def test_gated(T, N, K, act, name):
     assert np.all(np.abs(down(y) - want) <= bound)
 
 
+@pytest.mark.parametrize("algo,splits", [("pair", 0), ("single", 1), ("single", 2), ("single", 5), ("single", 256)])
+@pytest.mark.parametrize("T,N,K", PRODUCTS[::3] + [(257, 129, 1024), (513, 1023, 1088), (129, 513, 8200)])
+def test_forced_forms(T, N, K, algo, splits):
+    torch = t()
+    rng = np.random.default_rng(T + N + K)
+    qa, a, _ = operand(rng, T, K)
+    (qb, b, sb), (qc, _, sc) = operand(rng, N, K), operand(rng, N, K)
+    for q, s in ((qb, sb), (qc, sc)):
+        q.scales.copy_(torch.from_numpy(s / 60 / np.sqrt(K).astype(np.float32)))
+    y, untouched = output(T, N, "int32", pad=1)
+    g.i8_matmul(qa, qb, out=y, algo=algo, splits=splits)
+    quiet()
+    assert np.array_equal(down(y), sums_of(a, b).astype(np.int64)) and untouched()
+    for act in ("silu", "gelu"):
+        y, untouched = output(T, N, "float32", pad=1)
+        g.i8_gated(qa, qb, qc, act=act, out=y, algo=algo, splits=splits)
+        assert torch.equal(y, g.i8_gated(qa, qb, qc, act=act)) and untouched()
+    quiet()
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 40, 131071), (6, 33, 131071), (20, 300, 33000), (300, 300, 5000),
                                    (257, 130, 131071), (70, 4, 20000)])
 @pytest.mark.parametrize("a,b", [(-128, -128), (127, -128), (-128, 127)])
