@@ -301,7 +301,7 @@ struct Q8WgradTmemArgs {
 };
 cudaError_t launch_q8_wgrad_tmem(const Q8WgradTmemArgs& a, cudaStream_t s, int dev, int sm_count);
 
-// ---- 8-bit integer linear layers (i8_rows.cu, i8_dp4a.cu) ---------------------
+// ---- 8-bit integer linear layers (i8_rows.cu, i8_tmem.cu) ---------------------
 // Rows to codes (row stride ldq bytes) and scales: of x, or (w not null) of the
 // norm of s = x + r, which is written to s if that is not null.  All of one
 // type, r and s null or not as they are wanted.  No rows or columns: not called.
@@ -316,24 +316,8 @@ struct I8RowsArgs {
     float eps;
 };
 cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t s, int sm_count);
-// One operand's codes and scales, as the kernels take them.
-struct I8In {
-    const signed char* codes;
-    const float* scales;
-    long long ld;
-};
-// y = a b^T (T x N, row stride ldy elements), or, with c's codes not null, the
-// gated product act(a b^T) (a c^T).  type: kI8Float, kI8Bfloat16, kI8Int32 (not
-// gated).  T, N and K are not zero.
-struct I8ProductArgs {
-    I8In a, b, c;
-    void* y;
-    long long ldy;
-    int T, N, K, type, act;
-};
-cudaError_t launch_i8_dp4a(const I8ProductArgs& p, cudaStream_t s);
-
-// The same on the tensor core (i8_tmem.cu): CTA pairs with tiles of 256 channels
+// y = a b^T, or the gated product act(a b^T) (a c^T), on the tensor core
+// (i8_tmem.cu): CTA pairs with tiles of 256 channels
 // x 2 `tokens`, or single CTAs with 128 x `tokens` (gated: half the channels),
 // `tokens` a multiple of 16, at most 128; single CTAs' tiles in `splits` ranges
 // of the stages of K.
@@ -349,8 +333,8 @@ struct I8Tile {
 I8Tile i8_tile(bool pair);
 // bytes of the splits' sums
 size_t i8_parts_bytes(const I8Share& s);
-// Codes as {K, rows} bytes with 64-byte swizzle: a's box 64 x tokens, b's (and
-// c's, gated) 64 x 128, or gated 64 x 64.
+// Codes as {K, rows} bytes with 128-byte swizzle: a's box 128 x tokens, b's (and
+// c's, gated) 128 x 128, or gated 128 x 64.
 struct I8TmemMaps {
     CUtensorMap a, b, c;
 };

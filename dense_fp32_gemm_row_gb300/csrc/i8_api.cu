@@ -36,14 +36,13 @@ int check_arrays(const gemm_f32_i8* q) {
 
 Region codes_of(const gemm_f32_i8* q) { return region(q->codes, q->rows, q->cols, q->ld, 1); }
 Region scales_of(const gemm_f32_i8* q) { return region(q->scales, 1, q->rows, q->rows, 4); }
-I8In in_of(const gemm_f32_i8* q) { return {q->codes, q->scales, q->ld}; }
 
 int elem_of(int type) { return type == GEMM_F32_TYPE_BF16 ? 2 : 4; }
 bool is_float(int type) { return type == GEMM_F32_TYPE_F32 || type == GEMM_F32_TYPE_BF16; }
 
 int map_codes(CUtensorMap* map, const gemm_f32_i8* q, int k, int rows) {
     return call_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, q->codes, q->cols, q->rows, q->ld, k,
-                           rows, CU_TENSOR_MAP_SWIZZLE_64B);
+                           rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // How a product is shared out.

@@ -12,14 +12,17 @@ constexpr int kI8Float = 0;
 constexpr int kI8Bfloat16 = 1;
 constexpr int kI8Int32 = 2;
 
-// The value of a sum, the token's scale first: three roundings to fp32 (the
-// sum's own where it is beyond 2^24).
-__device__ __forceinline__ float i8_value(int sum, float token, float channel) {
-    return __fmul_rn(__fmul_rn(__int2float_rn(sum), token), channel);
+// The value of a sum, as a float (rounded where it is beyond 2^24), the token's
+// scale first.
+__device__ __forceinline__ float i8_value(float sum, float token, float channel) {
+    return __fmul_rn(__fmul_rn(sum, token), channel);
 }
 
-__device__ __forceinline__ float i8_gate(int act, float g, float u) {
-    return (act == kActSilu ? act_value<kActSilu>(g) : act_value<kActGelu>(g)) * u;
+// act(z) with the quotient of silu to 2 ulp (act_value rounds it correctly):
+// the sums' own roundings are as large.
+template <int ACT>
+__device__ __forceinline__ float i8_act(float z) {
+    return ACT == kActSilu ? __fdividef(z, 1.0f + expf(-z)) : act_value<kActGelu>(z);
 }
 
 __device__ __forceinline__ void put_output(void* y, long long at, int type, float v) {

@@ -4,9 +4,10 @@
 //
 // Arithmetic.  8-bit integers are exactly fp16 numbers, their products are at
 // most 2^14, and sums of up to 1024 of them at most 2^24, so an fp32
-// accumulator holds every partial sum of a 1024-deep chunk exactly, in
-// whatever order the tensor core adds.  Chunks are added up in 32-bit integer
-// registers: the sums are exact, and the same for any tile, split or kernel.
+// accumulator holds every partial sum of an 896-deep chunk exactly, in whatever
+// order the tensor core adds.  Chunks are added up in registers, as floats
+// while that is exact and as 32-bit integers beyond it: the sums are exact, and
+// the same for any tile, split or kernel.
 // (This part's integer MMAs run far below its 16-bit ones, and 8-bit floats
 // hold 4 significant bits: an 8-bit integer takes two of them, a product four
 // MMAs at twice the rate.)
@@ -24,19 +25,19 @@
 // tensor core works 128 cycles, and its shared memory moves 4 KB for the
 // weights (copy in, read out) and 12 KB for the tokens (copy in, read out, fp16
 // in, MMA).  Or one CTA computes 128 x up to 128, with two accumulators in
-// turn, its tiles split over K for few tokens.  The gated form has gate and up
-// channels in the two halves of a CTA's lanes, 64 each, and the warps of one
-// half exchange values with those of the other through shared memory.
+// turn, its tiles split over K for few tokens.  The gated form has 16 channels of
+// the gate and the same of up in the lanes of a warp, which exchange sums.
 //
 // 640 threads per CTA, registers rebalanced at start (launched at 96 each):
-//   warp 0       one lane: TMA loads of a 64-column stage of raw codes;
+//   warp 0       one lane: TMA loads of a 128-column stage of raw codes;
 //   warp 1       tensor-memory allocation; one lane (of a pair: the leader's)
 //                issues the MMAs and commits;
-//   warps 1-3 of a pair's peer  relay: one lane each tells the leader, in turn,
+//   warps 1-2 of a pair's peer  relay: one lane each tells the leader, in turn,
 //                that the peer's operands of a stage are written;
-//   warps 4-7    weights to fp16 in tensor memory (warp 4 + q: lanes 32 q ..);
-//   warps 8-11   tokens to fp16 in shared memory;
-//   warps 12-19  per chunk add the accumulator to 32-bit integers in registers
+//   warps 4-7, 8-11  conversion of every other stage each: weights to fp16 in
+//                tensor memory (warp 4 + q: lanes 32 q ..), tokens to fp16 in
+//                shared memory;
+//   warps 12-19  per chunk add the accumulator to the sums in their registers
 //                (warp 12 + e: lanes 32 (e % 4) .., half e / 4 of the columns);
 //                at the end of a unit scale and store them.
 // Splits of a tile write their sums to the workspace, and the one that comes
@@ -57,6 +58,12 @@ namespace {
 using namespace gemm_f32_dev;
 
 constexpr int kNoAct = -1;
+// Stages of K, 128 each, that one accumulator adds up, and the largest sum to
+// which another such is added exactly in fp32: 896 products of up to 2^14 are
+// 2^24 - 2^21.
+constexpr int kStageK = 128;
+constexpr int kChunk = 7;
+constexpr float kMostBefore = 16777216.0f - kChunk * kStageK * 16384.0f;
 
 template <bool PAIR_>
 struct I8Cfg {
@@ -65,40 +72,45 @@ struct I8Cfg {
     static constexpr int LANES = 128;                // rows of weights of a CTA
     static constexpr int TOK = 128;                  // tokens of a CTA, at most
     static constexpr int COLS = TOK * CTAS;          // accumulator columns
-    static constexpr int KT = 64;                    // K a stage
+    static constexpr int KT = kStageK;               // K a stage
     static constexpr int UK = 16;                    // K an MMA
-    static constexpr int CHUNK = 1024 / KT;          // stages of an exact fp32 sum
-    static constexpr int RAW = 6;                    // stages of raw codes
-    static constexpr int STAGES = 7;                 // stages of MMA operands
+    static constexpr int RAW = 3;                    // stages of raw codes
+    static constexpr int STAGES = 4;                 // stages of MMA operands
     static constexpr int ACCS = PAIR ? 1 : 2;        // accumulators
-    static constexpr int B_BYTES = TOK * KT * 2;     // tokens in fp16, rows of 128 bytes
+    static constexpr int B_HALF = TOK * 128;         // tokens in fp16: rows of 64, K halves
+    static constexpr int B_BYTES = 2 * B_HALF;
     static constexpr int W_RAW = LANES * KT;
     static constexpr int T_RAW = TOK * KT;
     static constexpr int RAW_BYTES = W_RAW + T_RAW;
     static constexpr int RAW_OFF = STAGES * B_BYTES;
-    static constexpr int EXCH_OFF = RAW_OFF + RAW * RAW_BYTES;
-    static constexpr int EXCH_WARP = 16 * 32 * 4;    // a warp's 16 columns
     static constexpr int EPI_WARPS = 8;
-    static constexpr int BAR_OFF = EXCH_OFF + EPI_WARPS * EXCH_WARP;
-    static constexpr int CONV_WARPS = 4 + 4;
-    // full, free (per raw stage), empty, ready (per operand stage), acc_full and
+    static constexpr int BAR_OFF = RAW_OFF + RAW * RAW_BYTES;
+    static constexpr int CONV_WARPS = 4;             // of a stage
+    // full, free (raw stages), empty, ready (per operand stage), acc_full and
     // acc_empty (per accumulator), drain
-    static constexpr int NBARS = 2 * RAW + 2 * STAGES + 2 * ACCS + 1;
+    static constexpr int NBARS = 3 * RAW + 2 * STAGES + 2 * ACCS + 1;
     static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;
     static constexpr int THREADS = 640;
     static constexpr int TMEM_COLS = 512;
-    static constexpr int OP_COL0 = 256;              // operand stage s at OP_COL0 + 32 s
+    static constexpr int OP_COL0 = 256;              // operand stage s at OP_COL0 + 64 s
     static constexpr int OP_COLS = KT / 2;
-    static constexpr int RELAYS = 3;
+    static constexpr int RELAYS = 2;
+    // A wait by parity has to come after the end of the barrier's phase before.
+    // Each barrier's stages belong to one warpgroup of the conversion and to one
+    // relay, which take theirs in order; raw slots, an odd number of them, have
+    // two barriers each in turn.
+    static constexpr int FULLS = 2 * RAW;
     static constexpr int EPI_COLS = COLS / 2;        // of a warp, at most
     static constexpr int REGS_LAUNCH = 96;
-    static constexpr int REGS_CONTROL = 40, REGS_WEIGHTS = 56, REGS_TOKENS = 48, REGS_EPI = 168;
+    static constexpr int REGS_CONTROL = 32, REGS_CONV = 56, REGS_EPI = 168;
     // D fp32, A and B fp16, both K-major, M = 128 a CTA; N is added
     static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(LANES * CTAS >> 4) << 24);
-    static_assert(REGS_CONTROL + REGS_WEIGHTS + REGS_TOKENS + 2 * REGS_EPI <= 5 * REGS_LAUNCH,
+    static_assert(REGS_CONTROL + 2 * REGS_CONV + 2 * REGS_EPI <= 5 * REGS_LAUNCH,
                   "register shares");
     static_assert(OP_COL0 + STAGES * OP_COLS <= TMEM_COLS && ACCS * COLS <= OP_COL0,
                   "tensor-memory columns");
+    static_assert(KT == 128, "two swizzled halves of K");
+    static_assert(STAGES % 2 == 0 && RELAYS % 2 == 0 && RAW < STAGES, "phases of the barriers");
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -116,14 +128,6 @@ __device__ __forceinline__ void sts_u32x4(uint32_t addr, uint32_t a, uint32_t b,
                  "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 // Barrier `id` of the CTA's named ones, for `threads` of its threads.
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -137,9 +141,16 @@ __device__ __forceinline__ void decode_f16(uint32_t w, uint32_t& lo, uint32_t& h
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(bias));
 }
 
-// Offset of a 16-byte chunk in a raw stage: rows of 64 bytes, 64-byte swizzle.
-__device__ __forceinline__ uint32_t raw_at(uint32_t row, uint32_t chunk) {
-    return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+__device__ __forceinline__ void decode_f16(const uint4& w, uint32_t (&h)[8]) {
+    decode_f16(w.x, h[0], h[1]);
+    decode_f16(w.y, h[2], h[3]);
+    decode_f16(w.z, h[4], h[5]);
+    decode_f16(w.w, h[6], h[7]);
+}
+
+// Offset of a 16-byte chunk: rows of 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk) {
+    return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
 // One unit of work: a split of a tile.
@@ -174,9 +185,56 @@ __device__ __forceinline__ int cta_tokens(int tokens, int left) {
     return min(tokens, (each + 15) & ~15);
 }
 
+// Adds an accumulator's columns to acc, which holds floats or (`whole`) 32-bit
+// integers.
+template <int COLS>
+__device__ __forceinline__ void add_columns(float (&acc)[COLS], uint32_t tbase, int count,
+                                            bool whole) {
+    if (whole) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += 16) {
+            if (j >= count) break;
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tbase + j, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[j + i] = __int_as_float(__float_as_int(acc[j + i]) +
+                                            __float2int_rn(__uint_as_float(r[i])));
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < COLS; j += 32) {
+        if (j >= count) break;
+        uint32_t r[2][16];
+        tmem_ld_32x32b_x16(tbase + j, r[0]);
+        tmem_ld_32x32b_x16(tbase + j + 16, r[1]);
+        tmem_ld_wait(r[0]);
+        tmem_ld_wait(r[1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[j + i] += __uint_as_float(r[i / 16][i % 16]);
+    }
+}
+
+// To 32-bit integers, unless another accumulator can be added to each sum of
+// the warp exactly.  (Conversions run at an eighth of the rate of additions:
+// with every chunk converted 8192 x 8192 x 8192 took 928 us.)
+template <int COLS>
+__device__ __forceinline__ void keep_exact(float (&acc)[COLS], bool& whole) {
+    if (whole) return;
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) most = fmaxf(most, fabsf(acc[i]));
+    if (!__any_sync(0xffffffffu, most > kMostBefore)) return;
+    whole = true;
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) acc[i] = __int_as_float(__float2int_rn(acc[i]));
+}
+
 // f(j, acc[j]) for the first `left` columns, unrolled: acc stays in registers.
 template <int COLS, typename F>
-__device__ __forceinline__ void for_columns(const int (&acc)[COLS], int left, F f) {
+__device__ __forceinline__ void for_columns(const float (&acc)[COLS], int left, F f) {
 #pragma unroll
     for (int j = 0; j < COLS; j += 16) {
         if (j + 16 <= left) {
@@ -202,7 +260,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_addr(smem);
     const uint32_t full0 = sbase + C::BAR_OFF;      // own: a raw stage has landed
-    const uint32_t free0 = full0 + 8 * C::RAW;      // own: its readers are done
+    const uint32_t free0 = full0 + 8 * C::FULLS;    // own: its readers are done
     const uint32_t empty0 = free0 + 8 * C::RAW;     // own, multicast commit: operands read
     const uint32_t ready0 = empty0 + 8 * STAGES;    // operands written
     const uint32_t accf = ready0 + 8 * STAGES;      // own, multicast commit
@@ -224,10 +282,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmB);
         if (GATED) prefetch_tmap(&tmC);
-        for (int r = 0; r < C::RAW; ++r) {
-            mbar_init(full0 + 8 * r, 1);
-            mbar_init(free0 + 8 * r, C::CONV_WARPS);
-        }
+        for (int r = 0; r < C::FULLS; ++r) mbar_init(full0 + 8 * r, 1);
+        for (int r = 0; r < C::RAW; ++r) mbar_init(free0 + 8 * r, C::CONV_WARPS);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(empty0 + 8 * s, 1);
             // in the leader also the relay of the peer's
@@ -298,7 +354,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             break;
                         }
                         const int k0 = (w.kb_begin + kb) * C::KT;
-                        const uint32_t fb = full0 + 8 * r;
+                        const uint32_t fb = full0 + 8 * (it % C::FULLS);
                         const uint32_t wb = sbase + C::RAW_OFF + r * C::RAW_BYTES;
                         mbar_arrive_expect_tx(fb, bytes);
                         tma_load_2d(wb, &tmB, fb, k0, ch0);
@@ -310,7 +366,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 // have reached its operand stages
                 const long long tail = ok ? timeout_ns : timeout_ns / 8 + 1000;
                 for (int j = (it > C::RAW ? it - C::RAW : 0); j < it; ++j)
-                    mbar_wait(full0 + 8 * (j % C::RAW), (j / C::RAW) & 1, tail, fault, kFaultDrain);
+                    mbar_wait(full0 + 8 * (j % C::FULLS), (j / C::FULLS) & 1, tail, fault,
+                              kFaultDrain);
                 for (int j = (it > STAGES ? it - STAGES : 0); j < it; ++j)
                     mbar_wait(empty0 + 8 * (j % STAGES), (j / STAGES) & 1, tail, fault, kFaultDrain);
             }
@@ -327,7 +384,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         C::IDESC | static_cast<uint32_t>(
                                        C::CTAS * cta_tokens<PAIR>(share.tokens, p.T - w.t0) / 8)
                                        << 17;
-                    for (int c0 = 0; c0 < w.nkb && ok; c0 += C::CHUNK, ++g) {
+                    for (int c0 = 0; c0 < w.nkb && ok; c0 += kChunk, ++g) {
                         const int b = g % C::ACCS;
                         // the accumulator: its last chunk has been drained
                         if (g >= C::ACCS &&
@@ -338,7 +395,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         }
                         tc_fence_after();
                         const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::COLS);
-                        const int c1 = min(w.nkb, c0 + C::CHUNK);
+                        const int c1 = min(w.nkb, c0 + kChunk);
                         for (int kb = c0; kb < c1; ++kb, ++it) {
                             const int s = it % STAGES;
                             if (!role_wait<PAIR>(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns,
@@ -353,8 +410,9 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                             for (int k = 0; k < C::KT / C::UK; ++k)
                                 // 16 columns of K: 32 bytes of a row, 8 columns of tensor memory
-                                mma_f16_tmem_a<PAIR>(d, a + 8u * k, x + 2u * k, idesc,
-                                                     (kb > c0 || k > 0) ? 1u : 0u);
+                                mma_f16_tmem_a<PAIR>(d, a + 8u * k,
+                                                     x + (k / 4) * (C::B_HALF >> 4) + 2u * (k % 4),
+                                                     idesc, (kb > c0 || k > 0) ? 1u : 0u);
                             mma_commit_form<PAIR>(empty0 + 8 * s);
                         }
                         if (!ok) break;
@@ -370,118 +428,92 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 relay(0);
             }
             __syncwarp();
-        } else if (PAIR && rank == 1 && lane == 0) {
-            // ------------------------------ relays (warps 2-3 of the peer) ------------
-            relay(warp - 1);
+        } else if (PAIR && rank == 1 && warp == 2 && lane == 0) {
+            // ------------------------------ the other relay ---------------------------
+            relay(1);
         }
         __syncwarp();
-    } else if (warp < 8) {
-        // ------------------------------ weights (warps 4-7) ----------------------------
-        regs_dec<C::REGS_WEIGHTS>();
+    } else if (warp < 12) {
+        // ------------------------------ conversion (warps 4-11) ------------------------
+        // A warpgroup takes every other stage, a half of K at a time.  Weights: a
+        // thread has its lane's row (gated: 16 of a warp's lanes the gate's, 16
+        // up's).  Tokens: a lane takes 16 codes; each eight lanes load from two rows
+        // whose numbers differ in bits 0 and 2, so that both the codes and the two
+        // chunks that they store lie in all banks.
+        regs_dec<C::REGS_CONV>();
+        constexpr int kItems = C::TOK / 8 / 4;
         const int q = warp & 3;
-        const uint32_t row = static_cast<uint32_t>(32 * q + lane);
+        const uint32_t row = static_cast<uint32_t>(
+            !GATED ? 32 * q + lane : (lane < 16 ? 0 : C::LANES / 2) + 16 * q + (lane & 15));
         const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+        const uint32_t c = static_cast<uint32_t>(lane & 3);
+        const uint32_t row0 =
+            static_cast<uint32_t>(8 * q + ((lane >> 3) ^ ((lane & 4) ? 5 : 0)));
         int it = 0;
+        const int parity = (warp >> 2) - 1;
         bool ok = true;
         Work w;
         for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
+            const int rows = cta_tokens<PAIR>(share.tokens, p.T - w.t0);
+            const int items = (rows - 8 * q + 31) / 32;  // of this warp: 8 rows each
             for (int kb = 0; kb < w.nkb; ++kb, ++it) {
+                if ((it & 1) != parity) continue;
                 const int s = it % STAGES, raw = it % C::RAW;
-                const bool got = role_wait(full0 + 8 * raw, (it / C::RAW) & 1, timeout_ns, fault,
-                                           kFaultFullBarrier, abort_flag);
+                const bool got = role_wait(full0 + 8 * (it % C::FULLS), (it / C::FULLS) & 1,
+                                           timeout_ns, fault, kFaultFullBarrier, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 const uint32_t src = sbase + C::RAW_OFF + raw * C::RAW_BYTES;
-                uint4 v[C::KT / 16];
-#pragma unroll
-                for (int c = 0; c < C::KT / 16; ++c)
-                    v[c] = lds_u32x4(src + raw_at(row, static_cast<uint32_t>(c)));
-                if (it >= STAGES) {
-                    const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns,
-                                               fault, kFaultEmptyBarrier, abort_flag);
-                    if (!__all_sync(0xffffffffu, can)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                // the MMAs that read this stage before are done
-                tc_fence_after();
+                const uint32_t dst = sbase + s * C::B_BYTES;
                 const uint32_t col =
                     lane_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
 #pragma unroll
-                for (int c = 0; c < C::KT / 16; c += 2) {
-                    uint32_t h[16];
+                for (uint32_t half = 0; half < 2; ++half) {
+                    uint4 v[4], x[kItems];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        decode_f16(v[c + i].x, h[8 * i], h[8 * i + 1]);
-                        decode_f16(v[c + i].y, h[8 * i + 2], h[8 * i + 3]);
-                        decode_f16(v[c + i].z, h[8 * i + 4], h[8 * i + 5]);
-                        decode_f16(v[c + i].w, h[8 * i + 6], h[8 * i + 7]);
+                    for (uint32_t i = 0; i < 4; ++i)
+                        v[i] = lds_u32x4(src + swizzled(row, 4u * half + i));
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i)
+                        if (i < items)
+                            x[i] = lds_u32x4(src + C::W_RAW +
+                                             swizzled(row0 + 32u * i, 4u * half + c));
+                    if (half == 0) {
+                        if (it >= STAGES) {
+                            const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1,
+                                                       timeout_ns, fault, kFaultEmptyBarrier,
+                                                       abort_flag);
+                            if (!__all_sync(0xffffffffu, can)) {
+                                ok = false;
+                                break;
+                            }
+                        }
+                        // the MMAs that read this stage before are done
+                        tc_fence_after();
                     }
-                    tmem_st_32x32b_x16(col + static_cast<uint32_t>(8 * c), h);
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        uint32_t h[8];
+                        decode_f16(v[i], h);
+                        tmem_st_32x32b_x8(col + 32u * half + 8u * i, h);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        if (i >= items) break;
+                        uint32_t h[8];
+                        decode_f16(x[i], h);
+                        const uint32_t at = dst + half * C::B_HALF;
+                        sts_u32x4(at + swizzled(row0 + 32u * i, 2u * c), h[0], h[1], h[2], h[3]);
+                        sts_u32x4(at + swizzled(row0 + 32u * i, 2u * c + 1u), h[4], h[5], h[6],
+                                  h[7]);
+                    }
                 }
+                if (!ok) break;
+                fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(ready0 + 8 * s);
-                    mbar_arrive(free0 + 8 * raw);
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp < 12) {
-        // ------------------------------ tokens (warps 8-11) ----------------------------
-        // A lane takes 16 codes: four lanes load a row's 64 bytes, and eight lanes
-        // store two rows' chunks in all banks.
-        regs_dec<C::REGS_TOKENS>();
-        constexpr int kItems = C::TOK / 8 / 4;
-        const uint32_t c = static_cast<uint32_t>(lane & 3);
-        const uint32_t row0 = static_cast<uint32_t>(8 * (warp - 8) + (lane >> 2));
-        int it = 0;
-        bool ok = true;
-        Work w;
-        for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
-            const int rows = cta_tokens<PAIR>(share.tokens, p.T - w.t0);
-            const int items = (rows - 8 * (warp - 8) + 31) / 32;  // of this warp: 8 rows each
-            for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                const int s = it % STAGES, raw = it % C::RAW;
-                const bool got = role_wait(full0 + 8 * raw, (it / C::RAW) & 1, timeout_ns, fault,
-                                           kFaultFullBarrier, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t src = sbase + C::RAW_OFF + raw * C::RAW_BYTES + C::W_RAW;
-                const uint32_t dst = sbase + s * C::B_BYTES;
-                uint4 v[kItems];
-#pragma unroll
-                for (int i = 0; i < kItems; ++i)
-                    if (i < items) v[i] = lds_u32x4(src + raw_at(row0 + 32u * i, c));
-                if (it >= STAGES) {
-                    const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns,
-                                               fault, kFaultEmptyBarrier, abort_flag);
-                    if (!__all_sync(0xffffffffu, can)) {
-                        ok = false;
-                        break;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    if (i >= items) break;
-                    const uint32_t r = row0 + 32u * i;
-                    uint32_t h[8];
-                    decode_f16(v[i].x, h[0], h[1]);
-                    decode_f16(v[i].y, h[2], h[3]);
-                    decode_f16(v[i].z, h[4], h[5]);
-                    decode_f16(v[i].w, h[6], h[7]);
-                    const uint32_t at = dst + r * 128u;
-                    sts_u32x4(at + (((2u * c) ^ (r & 7u)) << 4), h[0], h[1], h[2], h[3]);
-                    sts_u32x4(at + (((2u * c + 1u) ^ (r & 7u)) << 4), h[4], h[5], h[6], h[7]);
-                }
-                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(ready0 + 8 * s);
@@ -498,12 +530,10 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int e = warp - 12;
         const int q = warp & 3;                  // lanes 32 q .. 32 q + 31
         const int half = e >> 2;
-        const int n_lane = GATED ? rank * (C::LANES / 2) + 32 * (q & 1) + lane
+        const int n_lane = GATED ? rank * (C::LANES / 2) + 16 * q + (lane & 15)
                                  : rank * C::LANES + 32 * q + lane;
-        const float* const scales = GATED && q >= 2 ? p.cs : p.bs;
         const uint32_t acce_leader = PAIR ? map_to_cta(acce, 0) : acce;
-        const uint32_t exchange = sbase + C::EXCH_OFF + 4u * lane;
-        int acc[C::EPI_COLS];
+        float acc[C::EPI_COLS];
         int g = 0;
         bool ok = true;
         Work w;
@@ -513,8 +543,9 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const int col0 = half * each;
             const int count = min(each, cols - col0);  // of this warp: groups of 16, or none
 #pragma unroll
-            for (int i = 0; i < C::EPI_COLS; ++i) acc[i] = 0;
-            for (int c0 = 0; ok && c0 < w.nkb; c0 += C::CHUNK, ++g) {
+            for (int i = 0; i < C::EPI_COLS; ++i) acc[i] = 0.0f;
+            bool whole = false;  // acc holds 32-bit integers
+            for (int c0 = 0; ok && c0 < w.nkb; c0 += kChunk, ++g) {
                 const int b = g % C::ACCS;
                 const bool got = role_wait(accf + 8 * b, (g / C::ACCS) & 1, timeout_ns, fault,
                                            kFaultAccumBarrier, abort_flag);
@@ -525,16 +556,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 tc_fence_after();
                 const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                                        static_cast<uint32_t>(b * C::COLS + col0);
-#pragma unroll
-                for (int j = 0; j < C::EPI_COLS / 16; ++j) {
-                    if (16 * j >= count) break;
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(tbase + 16u * j, r);
-                    tmem_ld_wait(r);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[16 * j + i] += __float2int_rn(__uint_as_float(r[i]));
-                }
+                add_columns<C::EPI_COLS>(acc, tbase, count, whole);
                 // the loads have completed: the arrival orders no writes
                 tc_fence_before();
                 __syncwarp();
@@ -544,13 +566,20 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     else
                         mbar_arrive(acce + 8 * b);
                 }
+                // off the MMAs' path
+                if (c0 + kChunk < w.nkb) keep_exact<C::EPI_COLS>(acc, whole);
             }
             if (!PAIR && share.splits > 1) {
+                if (!whole)
+#pragma unroll
+                    for (int j = 0; j < C::EPI_COLS; ++j)
+                        acc[j] = __int_as_float(__float2int_rn(acc[j]));
+                whole = true;
                 const long long slot = static_cast<long long>(share.tokens) * C::LANES;
                 int* const mine = p.parts + u * slot + col0 * C::LANES + 32 * q + lane;
 #pragma unroll
                 for (int j = 0; j < C::EPI_COLS; ++j)
-                    if (j < count) __stcg(mine + j * C::LANES, acc[j]);
+                    if (j < count) __stcg(mine + j * C::LANES, __float_as_int(acc[j]));
                 __threadfence();
                 named_sync(1, 32 * C::EPI_WARPS);
                 if (e == 0 && lane == 0) {
@@ -567,61 +596,66 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     if (w.tile * share.splits + s == u) continue;
 #pragma unroll
                     for (int j = 0; j < C::EPI_COLS; ++j)
-                        if (j < count) acc[j] += __ldcg(all + s * slot + j * C::LANES);
+                        if (j < count)
+                            acc[j] = __int_as_float(__float_as_int(acc[j]) +
+                                                    __ldcg(all + s * slot + j * C::LANES));
                 }
+            }
+            // from here the sums as floats, or as the integers they are
+            const bool integers = !GATED && p.type == kI8Int32;
+            if (whole && !integers) {
+#pragma unroll
+                for (int j = 0; j < C::EPI_COLS; ++j)
+                    acc[j] = __int2float_rn(__float_as_int(acc[j]));
+            } else if (!whole && integers) {
+#pragma unroll
+                for (int j = 0; j < C::EPI_COLS; ++j)
+                    acc[j] = __int_as_float(__float2int_rn(acc[j]));
             }
             const int n = w.c0 + n_lane;
             const bool mine = ok && n < p.N;
-            const float channel = n < p.N ? scales[n] : 0.0f;
+            const float channel = n < p.N ? p.bs[n] : 0.0f;
             const int t_first = w.t0 + col0;
             if (GATED) {
-                // Of each two groups of 16 columns the gate's warp finishes the first
-                // and up's the second: both give the other its values of the other.
-                const int own = q >> 1;
-                const uint32_t to = exchange + static_cast<uint32_t>(e * C::EXCH_WARP);
-                const uint32_t from = exchange + static_cast<uint32_t>((e ^ 2) * C::EXCH_WARP);
+                // Lanes 0 .. 15 hold the gate's sums of 16 channels, lanes 16 .. 31 up's.  Of
+                // each two tokens the lower lanes finish the first and the upper the second.
+                const bool upper = lane >= 16;
+                const float channel_up = n < p.N ? p.cs[n] : 0.0f;
+                const int left = min(count, p.T - t_first) - (upper ? 1 : 0);
+                long long at = static_cast<long long>(t_first + (upper ? 1 : 0)) * p.ldy + n;
+                float token = 0.0f;  // of 32 of them, lane by lane
 #pragma unroll
-                for (int j = 0; j < C::EPI_COLS; j += 32) {
+                for (int j = 0; j < C::EPI_COLS; j += 2, at += 2 * p.ldy) {
                     if (j >= count) break;
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float first_t = p.as[min(t_first + j + i, p.T - 1)];
-                        const float second_t = p.as[min(t_first + j + 16 + i, p.T - 1)];
-                        const float a0 = i8_value(acc[j + i], first_t, channel);
-                        const float a1 = i8_value(acc[j + 16 + i], second_t, channel);
-                        v[i] = own ? a1 : a0;
-                        sts_f32(to + 128u * i, own ? a0 : a1);
+                    if (j % 32 == 0) {
+                        const int t = t_first + j + lane;
+                        token = t < p.T ? p.as[t] : 0.0f;
                     }
-                    named_sync(2 + half * 2 + (q & 1), 64);
-                    const int t = t_first + j + 16 * own;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float other = lds_f32(from + 128u * i);
-                        if (mine && j + 16 * own + i < count && t + i < p.T) {
-                            const float gate = own ? other : v[i], up = own ? v[i] : other;
-                            put_output(p.y, static_cast<long long>(t + i) * p.ldy + n, p.type,
-                                       act_value<ACT>(gate) * up);
-                        }
-                    }
-                    named_sync(2 + half * 2 + (q & 1), 64);
+                    const float st = __shfl_sync(0xffffffffu, token, j % 32 + (upper ? 1 : 0));
+                    const float other =
+                        __shfl_xor_sync(0xffffffffu, upper ? acc[j] : acc[j + 1], 16);
+                    const float own = upper ? acc[j + 1] : acc[j];
+                    const float gate = i8_value(upper ? other : own, st, channel);
+                    const float up = i8_value(upper ? own : other, st, channel_up);
+                    const float h = i8_act<ACT>(gate) * up;
+                    if (mine && j < left) put_output(p.y, at, p.type, h);
                 }
             } else if (mine) {
                 const long long at = static_cast<long long>(t_first) * p.ldy + n;
                 const float* const token = p.as + t_first;
                 const int left = min(count, p.T - t_first);
                 if (p.type == kI8Int32)
-                    for_columns<C::EPI_COLS>(acc, left, [&](int j, int v) {
-                        static_cast<int*>(p.y)[at + j * p.ldy] = v;
+                    for_columns<C::EPI_COLS>(acc, left, [&](int j, float v) {
+                        static_cast<int*>(p.y)[at + j * p.ldy] = __float_as_int(v);
                     });
                 else if (p.type == kI8Bfloat16)
-                    for_columns<C::EPI_COLS>(acc, left, [&](int j, int v) {
+                    for_columns<C::EPI_COLS>(acc, left, [&](int j, float v) {
                         put_output(p.y, at + j * p.ldy, kI8Bfloat16,
-                                   i8_value(v, token[j], channel));
+                                   i8_value(v, __ldg(token + j), channel));
                     });
                 else
-                    for_columns<C::EPI_COLS>(acc, left, [&](int j, int v) {
-                        put_output(p.y, at + j * p.ldy, kI8Float, i8_value(v, token[j], channel));
+                    for_columns<C::EPI_COLS>(acc, left, [&](int j, float v) {
+                        put_output(p.y, at + j * p.ldy, kI8Float, i8_value(v, __ldg(token + j), channel));
                     });
             }
         }
