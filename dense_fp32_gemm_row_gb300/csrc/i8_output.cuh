@@ -25,11 +25,4 @@ __device__ __forceinline__ float i8_act(float z) {
     return ACT == kActSilu ? __fdividef(z, 1.0f + expf(-z)) : act_value<kActGelu>(z);
 }
 
-__device__ __forceinline__ void put_output(void* y, long long at, int type, float v) {
-    if (type == kI8Bfloat16)
-        static_cast<__nv_bfloat16*>(y)[at] = __float2bfloat16_rn(v);
-    else
-        static_cast<float*>(y)[at] = v;
-}
-
 }  // namespace gemm_f32_dev

@@ -128,6 +128,11 @@ __device__ __forceinline__ void sts_u32x4(uint32_t addr, uint32_t a, uint32_t b,
                  "r"(d)
                  : "memory");
 }
+// Eight words to two neighbouring 16-byte chunks of a swizzled row, the first even.
+__device__ __forceinline__ void sts_u32x8(uint32_t addr, const uint32_t (&h)[8]) {
+    sts_u32x4(addr, h[0], h[1], h[2], h[3]);
+    sts_u32x4(addr ^ 16u, h[4], h[5], h[6], h[7]);
+}
 // Barrier `id` of the CTA's named ones, for `threads` of its threads.
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -232,19 +237,60 @@ __device__ __forceinline__ void keep_exact(float (&acc)[COLS], bool& whole) {
     for (int i = 0; i < COLS; ++i) acc[i] = __int_as_float(__float2int_rn(acc[i]));
 }
 
-// f(j, acc[j]) for the first `left` columns, unrolled: acc stays in registers.
-template <int COLS, typename F>
-__device__ __forceinline__ void for_columns(const float (&acc)[COLS], int left, F f) {
+// The scale of column j from registers that hold 32 a time, lane by lane.
+template <int N>
+__device__ __forceinline__ float scale_of(const float (&token)[N], int j) {
+    return __shfl_sync(0xffffffffu, token[j / 32], j % 32);
+}
+
+// value(j) to p + j ld for the first `left` columns of `count`, in groups of 16
+// without a branch among them: acc stays in registers, and the columns' loads,
+// shuffles and stores overlap.
+template <int COLS, typename T, typename F>
+__device__ __forceinline__ void put_columns(const float (&acc)[COLS], int count, int left, T* p,
+                                            long long ld, F value) {
 #pragma unroll
     for (int j = 0; j < COLS; j += 16) {
-        if (j + 16 <= left) {
+        if (j >= count) break;
+        T v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f(j + i, acc[j + i]);
-        } else {
+        for (int i = 0; i < 16; ++i) v[i] = value(j + i);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (j + i < left) f(j + i, acc[j + i]);
+        for (int i = 0; i < 16; ++i, p += ld)
+            if (j + i < left) *p = v[i];
+    }
+}
+
+__device__ __forceinline__ void put_float(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_float(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// The gated product of a warp whose lanes 0 .. 15 hold the gate's sums of 16
+// channels and lanes 16 .. 31 up's: of each two tokens the lower lanes finish the
+// first and the upper the second.
+template <int COLS, int ACT, typename T>
+__device__ __forceinline__ void put_gated(const float (&acc)[COLS], const float (&token)[COLS / 32],
+                                          float channel, float channel_up, int count, int left,
+                                          T* p, long long ld) {
+    const int upper = (threadIdx.x >> 4) & 1;
+    p += upper * ld;
+    left -= upper;
+#pragma unroll
+    for (int j = 0; j < COLS; j += 16) {
+        if (j >= count) break;
+        float h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = j + 2 * i;
+            const float st = __shfl_sync(0xffffffffu, token[k / 32], k % 32 + upper);
+            const float own = upper ? acc[k + 1] : acc[k];
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? acc[k] : acc[k + 1], 16);
+            const float gate = i8_value(upper ? other : own, st, channel);
+            const float up = i8_value(upper ? own : other, st, channel_up);
+            h[i] = i8_act<ACT>(gate) * up;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i, p += 2 * ld)
+            if (j + 2 * i < left) put_float(p, h[i]);
     }
 }
 
@@ -442,6 +488,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // chunks that they store lie in all banks.
         regs_dec<C::REGS_CONV>();
         constexpr int kItems = C::TOK / 8 / 4;
+        constexpr uint32_t kItemBytes = 32 * 128;
         const int q = warp & 3;
         const uint32_t row = static_cast<uint32_t>(
             !GATED ? 32 * q + lane : (lane < 16 ? 0 : C::LANES / 2) + 16 * q + (lane & 15));
@@ -449,6 +496,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t c = static_cast<uint32_t>(lane & 3);
         const uint32_t row0 =
             static_cast<uint32_t>(8 * q + ((lane >> 3) ^ ((lane & 4) ? 5 : 0)));
+        const uint32_t weights_at = swizzled(row, 0);  // of the first chunk
+        const uint32_t tokens_at = swizzled(row0, c), fp16_at = swizzled(row0, 2u * c);
         int it = 0;
         const int parity = (warp >> 2) - 1;
         bool ok = true;
@@ -465,52 +514,67 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     ok = false;
                     break;
                 }
+                // chunk c of a row of 128 bytes lies at (c << 4) ^ (row % 8 << 4) in it
                 const uint32_t src = sbase + C::RAW_OFF + raw * C::RAW_BYTES;
-                const uint32_t dst = sbase + s * C::B_BYTES;
+                const uint32_t from_w = src + weights_at, from_x = src + C::W_RAW + tokens_at;
+                const uint32_t to_x = sbase + s * C::B_BYTES + fp16_at;
                 const uint32_t col =
                     lane_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
+                uint4 v[4], x[kItems];
 #pragma unroll
-                for (uint32_t half = 0; half < 2; ++half) {
-                    uint4 v[4], x[kItems];
+                for (uint32_t i = 0; i < 4; ++i) v[i] = lds_u32x4(from_w ^ (i << 4));
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i)
-                        v[i] = lds_u32x4(src + swizzled(row, 4u * half + i));
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i)
-                        if (i < items)
-                            x[i] = lds_u32x4(src + C::W_RAW +
-                                             swizzled(row0 + 32u * i, 4u * half + c));
-                    if (half == 0) {
-                        if (it >= STAGES) {
-                            const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1,
-                                                       timeout_ns, fault, kFaultEmptyBarrier,
-                                                       abort_flag);
-                            if (!__all_sync(0xffffffffu, can)) {
-                                ok = false;
-                                break;
-                            }
-                        }
-                        // the MMAs that read this stage before are done
-                        tc_fence_after();
-                    }
-#pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) {
-                        uint32_t h[8];
-                        decode_f16(v[i], h);
-                        tmem_st_32x32b_x8(col + 32u * half + 8u * i, h);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i) {
-                        if (i >= items) break;
-                        uint32_t h[8];
-                        decode_f16(x[i], h);
-                        const uint32_t at = dst + half * C::B_HALF;
-                        sts_u32x4(at + swizzled(row0 + 32u * i, 2u * c), h[0], h[1], h[2], h[3]);
-                        sts_u32x4(at + swizzled(row0 + 32u * i, 2u * c + 1u), h[4], h[5], h[6],
-                                  h[7]);
+                for (int i = 0; i < kItems; ++i)
+                    if (items == kItems) x[i] = lds_u32x4(from_x + kItemBytes * i);
+                if (it >= STAGES) {
+                    const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns,
+                                               fault, kFaultEmptyBarrier, abort_flag);
+                    if (!__all_sync(0xffffffffu, can)) {
+                        ok = false;
+                        break;
                     }
                 }
-                if (!ok) break;
+                // the MMAs that read this stage before are done
+                tc_fence_after();
+                // the second half's codes are loaded as the first's are converted
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    uint32_t h[8];
+                    decode_f16(v[i], h);
+                    v[i] = lds_u32x4(from_w ^ ((i + 4u) << 4));
+                    tmem_st_32x32b_x8(col + 8u * i, h);
+                }
+                if (items == kItems) {
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        uint32_t h[8];
+                        decode_f16(x[i], h);
+                        x[i] = lds_u32x4((from_x ^ 64u) + kItemBytes * i);
+                        sts_u32x8(to_x + kItemBytes * i, h);
+                    }
+                } else {
+                    for (int i = 0; i < items; ++i) {
+                        uint32_t h[8];
+                        decode_f16(lds_u32x4(from_x + kItemBytes * i), h);
+                        sts_u32x8(to_x + kItemBytes * i, h);
+                        decode_f16(lds_u32x4((from_x ^ 64u) + kItemBytes * i), h);
+                        sts_u32x8(to_x + C::B_HALF + kItemBytes * i, h);
+                    }
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) {
+                    uint32_t h[8];
+                    decode_f16(v[i], h);
+                    tmem_st_32x32b_x8(col + 32u + 8u * i, h);
+                }
+                if (items == kItems) {
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        uint32_t h[8];
+                        decode_f16(x[i], h);
+                        sts_u32x8(to_x + C::B_HALF + kItemBytes * i, h);
+                    }
+                }
                 fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
@@ -545,6 +609,13 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
             for (int i = 0; i < C::EPI_COLS; ++i) acc[i] = 0.0f;
             bool whole = false;  // acc holds 32-bit integers
+            // the tokens' scales, 32 of them lane by lane, long before their use
+            float token[C::EPI_COLS / 32];
+#pragma unroll
+            for (int i = 0; i < C::EPI_COLS / 32; ++i) {
+                const int t = w.t0 + col0 + 32 * i + lane;
+                token[i] = t < p.T ? __ldg(p.as + t) : 0.0f;
+            }
             for (int c0 = 0; ok && c0 < w.nkb; c0 += kChunk, ++g) {
                 const int b = g % C::ACCS;
                 const bool got = role_wait(accf + 8 * b, (g / C::ACCS) & 1, timeout_ns, fault,
@@ -614,49 +685,34 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             const int n = w.c0 + n_lane;
             const bool mine = ok && n < p.N;
-            const float channel = n < p.N ? p.bs[n] : 0.0f;
+            const float channel = n < p.N ? __ldg(p.bs + n) : 0.0f;
             const int t_first = w.t0 + col0;
             if (GATED) {
-                // Lanes 0 .. 15 hold the gate's sums of 16 channels, lanes 16 .. 31 up's.  Of
-                // each two tokens the lower lanes finish the first and the upper the second.
-                const bool upper = lane >= 16;
-                const float channel_up = n < p.N ? p.cs[n] : 0.0f;
-                const int left = min(count, p.T - t_first) - (upper ? 1 : 0);
-                long long at = static_cast<long long>(t_first + (upper ? 1 : 0)) * p.ldy + n;
-                float token = 0.0f;  // of 32 of them, lane by lane
-#pragma unroll
-                for (int j = 0; j < C::EPI_COLS; j += 2, at += 2 * p.ldy) {
-                    if (j >= count) break;
-                    if (j % 32 == 0) {
-                        const int t = t_first + j + lane;
-                        token = t < p.T ? p.as[t] : 0.0f;
-                    }
-                    const float st = __shfl_sync(0xffffffffu, token, j % 32 + (upper ? 1 : 0));
-                    const float other =
-                        __shfl_xor_sync(0xffffffffu, upper ? acc[j] : acc[j + 1], 16);
-                    const float own = upper ? acc[j + 1] : acc[j];
-                    const float gate = i8_value(upper ? other : own, st, channel);
-                    const float up = i8_value(upper ? own : other, st, channel_up);
-                    const float h = i8_act<ACT>(gate) * up;
-                    if (mine && j < left) put_output(p.y, at, p.type, h);
-                }
-            } else if (mine) {
+                const float channel_up = n < p.N ? __ldg(p.cs + n) : 0.0f;
+                const int left = mine ? min(count, p.T - t_first) : 0;
                 const long long at = static_cast<long long>(t_first) * p.ldy + n;
-                const float* const token = p.as + t_first;
-                const int left = min(count, p.T - t_first);
-                if (p.type == kI8Int32)
-                    for_columns<C::EPI_COLS>(acc, left, [&](int j, float v) {
-                        static_cast<int*>(p.y)[at + j * p.ldy] = __float_as_int(v);
-                    });
-                else if (p.type == kI8Bfloat16)
-                    for_columns<C::EPI_COLS>(acc, left, [&](int j, float v) {
-                        put_output(p.y, at + j * p.ldy, kI8Bfloat16,
-                                   i8_value(v, __ldg(token + j), channel));
-                    });
+                if (p.type == kI8Bfloat16)
+                    put_gated<C::EPI_COLS, ACT>(acc, token, channel, channel_up, count, left,
+                                                static_cast<__nv_bfloat16*>(p.y) + at, p.ldy);
                 else
-                    for_columns<C::EPI_COLS>(acc, left, [&](int j, float v) {
-                        put_output(p.y, at + j * p.ldy, kI8Float, i8_value(v, __ldg(token + j), channel));
-                    });
+                    put_gated<C::EPI_COLS, ACT>(acc, token, channel, channel_up, count, left,
+                                                static_cast<float*>(p.y) + at, p.ldy);
+            } else {
+                const int left = mine ? min(count, p.T - t_first) : 0;
+                const long long at = static_cast<long long>(t_first) * p.ldy + n;
+                if (p.type == kI8Int32)
+                    put_columns<C::EPI_COLS>(acc, count, left, static_cast<int*>(p.y) + at, p.ldy,
+                                             [&](int j) { return __float_as_int(acc[j]); });
+                else if (p.type == kI8Bfloat16)
+                    put_columns<C::EPI_COLS>(
+                        acc, count, left, static_cast<__nv_bfloat16*>(p.y) + at, p.ldy, [&](int j) {
+                            return __float2bfloat16_rn(
+                                i8_value(acc[j], scale_of(token, j), channel));
+                        });
+                else
+                    put_columns<C::EPI_COLS>(
+                        acc, count, left, static_cast<float*>(p.y) + at, p.ldy,
+                        [&](int j) { return i8_value(acc[j], scale_of(token, j), channel); });
             }
         }
         __syncwarp();
