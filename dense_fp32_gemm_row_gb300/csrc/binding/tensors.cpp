@@ -1,5 +1,6 @@
 // tensors.cpp -- the Python binding's fast path for the 8-bit checkpoint
-// operators: tensors in, tensors and checkpoints out, one call each.
+// operators and the 8-bit integer layers: tensors in, tensors, checkpoints and
+// 8-bit matrices out, one call each.
 //
 // A small call of these operators takes the GPU a few microseconds, and its
 // host side more than that.  On a Grace core, around a launch of 2.5 us, making
@@ -11,9 +12,9 @@
 //
 // Each function handles the ordinary call -- exact tensors of the right type,
 // shape and strides on the current device, outputs not given -- and returns
-// None for anything else: q8.py then goes through the call step by step, with
-// its checks and its errors.  Built beside the library for the torch that is
-// installed; without it q8.py does everything that way.
+// None for anything else: q8.py or i8.py then goes through the call step by
+// step, with its checks and its errors.  Built beside the library for the torch
+// that is installed; without it they do everything that way.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -483,6 +484,263 @@ PyObject* gated_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// ---- 8-bit integer layers ------------------------------------------------------
+
+struct I8Library {
+    decltype(&gemm_f32_i8_store) store;
+    decltype(&gemm_f32_i8_norm) norm;
+    decltype(&gemm_f32_i8_matmul) matmul;
+    decltype(&gemm_f32_i8_gated) gated;
+    PyTypeObject* type;                // the binding's class, with three slots:
+    PyObject *codes, *scales, *cols;   // their names
+} i8 = {};
+
+// An 8-bit matrix as its tensors have it now; the tensors are kept until the
+// call has been made.
+struct I8Operand {
+    gemm_f32_i8 q = {};
+    int device = -1;
+    Ref codes, scales;
+};
+bool i8_describe(const at::Tensor& c, const at::Tensor& s, long long cols, I8Operand* m) {
+    if (c.layout() != at::kStrided || !c.is_cuda() || c.scalar_type() != at::kChar || c.dim() != 2 ||
+        s.layout() != at::kStrided || !s.is_cuda() || s.scalar_type() != at::kFloat || s.dim() != 1)
+        return false;
+    const long long rows = c.size(0), width = c.size(1);
+    if (rows < 1 || rows > INT_MAX || cols < 1 || cols > INT_MAX || width < cols ||
+        s.size(0) != rows || (width > 1 && c.stride(1) != 1) || (rows > 1 && s.stride(0) != 1) ||
+        c.device() != s.device())
+        return false;
+    const long long ld = rows > 1 ? c.stride(0) : (width + 15) & ~15LL;
+    if (ld < cols || !covers(c, cols) ||
+        s.storage().nbytes() < 4 * static_cast<unsigned long long>(s.storage_offset() + rows))
+        return false;
+    m->q.codes = static_cast<signed char*>(c.data_ptr());
+    m->q.scales = static_cast<float*>(s.data_ptr());
+    m->q.ld = ld;
+    m->q.rows = static_cast<int>(rows);
+    m->q.cols = static_cast<int>(cols);
+    m->device = c.device().index();
+    return ((reinterpret_cast<uintptr_t>(m->q.codes) | static_cast<uintptr_t>(ld)) & 15) == 0;
+}
+// False without an error: not the ordinary case.
+bool i8_operand(PyObject* o, I8Operand* m) {
+    if (Py_TYPE(o) != i8.type) return false;
+    m->codes.p = PyObject_GetAttr(o, i8.codes);
+    m->scales.p = PyObject_GetAttr(o, i8.scales);
+    const Ref cols{PyObject_GetAttr(o, i8.cols)};
+    if (!m->codes.p || !m->scales.p || !cols.p) {
+        PyErr_Clear();
+        return false;
+    }
+    if (!THPVariable_CheckExact(m->codes.p) || !THPVariable_CheckExact(m->scales.p) ||
+        !PyLong_CheckExact(cols.p))
+        return false;
+    const long long n = PyLong_AsLongLong(cols.p);
+    if (n == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    return i8_describe(THPVariable_Unpack(m->codes.p), THPVariable_Unpack(m->scales.p), n, m) &&
+           m->device == c10::cuda::current_device();
+}
+
+// A new matrix of rows padded to 16 bytes.
+struct I8New {
+    at::Tensor codes, scales;
+    gemm_f32_i8 q;
+    I8New(long long rows, long long cols, int device) {
+        const long long ld = (cols + 15) & ~15LL;
+        const int64_t size[2] = {rows, ld};
+        codes = new_tensor(at::IntArrayRef(size, 2), at::kChar, device);
+        scales = new_tensor(at::IntArrayRef(size, 1), at::kFloat, device);
+        q = {static_cast<signed char*>(codes.data_ptr()), floats(scales), ld,
+             static_cast<int>(rows), static_cast<int>(cols)};
+    }
+    // The binding's object.
+    PyObject* object() const {
+        Ref o{i8.type->tp_alloc(i8.type, 0)};
+        const Ref c{THPVariable_Wrap(codes)}, s{THPVariable_Wrap(scales)},
+            n{PyLong_FromLong(q.cols)};
+        if (!o.p || !c.p || !s.p || !n.p || PyObject_SetAttr(o.p, i8.codes, c.p) < 0 ||
+            PyObject_SetAttr(o.p, i8.scales, s.p) < 0 || PyObject_SetAttr(o.p, i8.cols, n.p) < 0)
+            return nullptr;
+        return o.take();
+    }
+};
+
+// A float32 or bfloat16 CUDA matrix with contiguous rows and elements, on the
+// current device.
+struct AnyMatrix {
+    void* p;
+    long long rows, cols, ld;
+    int device, type;
+};
+bool any_matrix(PyObject* o, AnyMatrix* m) {
+    if (!THPVariable_CheckExact(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.layout() != at::kStrided || !t.is_cuda() || t.dim() != 2) return false;
+    const at::ScalarType type = t.scalar_type();
+    if (type != at::kFloat && type != at::kBFloat16) return false;
+    m->type = type == at::kFloat ? GEMM_F32_TYPE_F32 : GEMM_F32_TYPE_BF16;
+    m->rows = t.size(0);
+    m->cols = t.size(1);
+    m->device = t.device().index();
+    if (m->rows < 1 || m->cols < 1 || m->rows > INT_MAX || m->cols > INT_MAX) return false;
+    if (m->device != c10::cuda::current_device()) return false;
+    if (m->cols > 1 && t.stride(1) != 1) return false;
+    m->ld = m->rows > 1 ? t.stride(0) : m->cols;
+    if (m->ld < m->cols) return false;
+    m->p = t.data_ptr();
+    return true;
+}
+
+at::Tensor i8_output(long long rows, long long cols, int type, int device) {
+    const int64_t size[2] = {rows, cols};
+    return new_tensor(at::IntArrayRef(size, 2),
+                      type == GEMM_F32_TYPE_BF16  ? at::kBFloat16
+                      : type == GEMM_F32_TYPE_I32 ? at::kInt
+                                                  : at::kFloat,
+                      device);
+}
+
+// bind_i8(store, norm, matmul, gated, type): after bind()
+PyObject* bind_i8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (!count(n, 5)) return nullptr;
+    void* p[4];
+    for (int i = 0; i < 4; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!PyType_Check(args[4])) {
+        PyErr_SetString(PyExc_TypeError, "the class of 8-bit matrices is a type");
+        return nullptr;
+    }
+    if (!i8.codes) i8.codes = PyUnicode_InternFromString("codes");
+    if (!i8.scales) i8.scales = PyUnicode_InternFromString("scales");
+    if (!i8.cols) i8.cols = PyUnicode_InternFromString("cols");
+    if (!i8.codes || !i8.scales || !i8.cols) return nullptr;
+    i8.store = reinterpret_cast<decltype(i8.store)>(p[0]);
+    i8.norm = reinterpret_cast<decltype(i8.norm)>(p[1]);
+    i8.matmul = reinterpret_cast<decltype(i8.matmul)>(p[2]);
+    i8.gated = reinterpret_cast<decltype(i8.gated)>(p[3]);
+    Py_INCREF(args[4]);
+    Py_XDECREF(i8.type);
+    i8.type = reinterpret_cast<PyTypeObject*>(args[4]);
+    Py_RETURN_NONE;
+}
+
+// i8_fits(codes, scales, cols): whether they are an ordinary matrix
+PyObject* i8_fits(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!count(n, 3)) return nullptr;
+    if (!THPVariable_CheckExact(args[0]) || !THPVariable_CheckExact(args[1]) ||
+        !PyLong_CheckExact(args[2]))
+        Py_RETURN_FALSE;
+    const long long cols = PyLong_AsLongLong(args[2]);
+    if (cols == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        Py_RETURN_FALSE;
+    }
+    I8Operand m;
+    if (i8_describe(THPVariable_Unpack(args[0]), THPVariable_Unpack(args[1]), cols, &m))
+        Py_RETURN_TRUE;
+    Py_RETURN_FALSE;
+    END_HANDLE_TH_ERRORS
+}
+
+// i8_store(x) -> matrix
+PyObject* i8_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    AnyMatrix x;
+    if (!count(n, 1)) return nullptr;
+    if (!any_matrix(args[0], &x)) Py_RETURN_NONE;
+    const I8New out(x.rows, x.cols, x.device);
+    const cudaStream_t s = stream_of(x.device);
+    if (!call("i8_store", [&] { return i8.store(x.p, x.type, x.ld, &out.q, s); })) return nullptr;
+    return out.object();
+    END_HANDLE_TH_ERRORS
+}
+
+// i8_norm(x, weight, residual or None, eps) -> (matrix, sum or None)
+PyObject* i8_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    AnyMatrix x, r = {};
+    if (!count(n, 4)) return nullptr;
+    if (!any_matrix(args[0], &x) || !THPVariable_CheckExact(args[1]) || !PyFloat_CheckExact(args[3]))
+        Py_RETURN_NONE;
+    const float eps = static_cast<float>(PyFloat_AS_DOUBLE(args[3]));
+    const at::Tensor& w = THPVariable_Unpack(args[1]);
+    if (w.layout() != at::kStrided || !w.is_cuda() || w.device().index() != x.device ||
+        w.scalar_type() != (x.type == GEMM_F32_TYPE_F32 ? at::kFloat : at::kBFloat16) ||
+        w.dim() != 1 || w.size(0) != x.cols || (x.cols > 1 && w.stride(0) != 1) ||
+        !(eps >= GEMM_F32_I8_LEAST_EPS))
+        Py_RETURN_NONE;
+    const bool residual = args[2] != Py_None;
+    if (residual && (!any_matrix(args[2], &r) || r.type != x.type || r.rows != x.rows ||
+                     r.cols != x.cols))
+        Py_RETURN_NONE;
+    const I8New out(x.rows, x.cols, x.device);
+    at::Tensor sum;
+    if (residual) sum = i8_output(x.rows, x.cols, x.type, x.device);
+    void *pw = w.data_ptr(), *ps = residual ? sum.data_ptr() : nullptr;
+    const cudaStream_t s = stream_of(x.device);
+    if (!call("i8_norm", [&] {
+            return i8.norm(x.p, x.ld, r.p, r.ld, pw, eps, x.type, ps, x.cols, &out.q, s);
+        }))
+        return nullptr;
+    Ref q{out.object()}, t;
+    if (residual) {
+        t.p = THPVariable_Wrap(sum);
+    } else {
+        Py_INCREF(Py_None);
+        t.p = Py_None;
+    }
+    return q.p && t.p ? PyTuple_Pack(2, q.p, t.p) : nullptr;
+    END_HANDLE_TH_ERRORS
+}
+
+// i8_matmul(a, w, type) -> tensor
+PyObject* i8_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    long type;
+    I8Operand a, w;
+    if (!count(n, 3) || !ints(args + 2, 1, &type)) return nullptr;
+    if (!i8_operand(args[0], &a) || !i8_operand(args[1], &w) || a.q.cols != w.q.cols ||
+        a.q.cols > GEMM_F32_I8_MAX_COLS || a.device != w.device)
+        Py_RETURN_NONE;
+    const at::Tensor y = i8_output(a.q.rows, w.q.rows, static_cast<int>(type), a.device);
+    void* p = y.data_ptr();
+    const cudaStream_t s = stream_of(a.device);
+    if (!call("i8_matmul", [&] {
+            return i8.matmul(&a.q, &w.q, p, static_cast<int>(type), w.q.rows, GEMM_F32_ALGO_AUTO, 0,
+                             s);
+        }))
+        return nullptr;
+    return THPVariable_Wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+// i8_gated(a, gate, up, act, type) -> tensor
+PyObject* i8_gated(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    long v[2];
+    I8Operand a, g, u;
+    if (!count(n, 5) || !ints(args + 3, 2, v)) return nullptr;
+    if (!i8_operand(args[0], &a) || !i8_operand(args[1], &g) || !i8_operand(args[2], &u) ||
+        a.q.cols != g.q.cols || a.q.cols > GEMM_F32_I8_MAX_COLS || u.q.cols != g.q.cols ||
+        u.q.rows != g.q.rows || a.device != g.device || a.device != u.device)
+        Py_RETURN_NONE;
+    const at::Tensor h = i8_output(a.q.rows, g.q.rows, static_cast<int>(v[1]), a.device);
+    void* p = h.data_ptr();
+    const cudaStream_t s = stream_of(a.device);
+    if (!call("i8_gated", [&] {
+            return i8.gated(static_cast<int>(v[0]), &a.q, &g.q, &u.q, p, static_cast<int>(v[1]),
+                            g.q.rows, GEMM_F32_ALGO_AUTO, 0, s);
+        }))
+        return nullptr;
+    return THPVariable_Wrap(h);
+    END_HANDLE_TH_ERRORS
+}
+
 typedef PyObject* (*Fast)(PyObject*, PyObject* const*, Py_ssize_t);
 PyCFunction as_c(Fast f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)); }
 
@@ -495,6 +753,12 @@ PyMethodDef methods[] = {{"bind", as_c(bind), METH_FASTCALL, nullptr},
                          {"wgrad", as_c(wgrad), METH_FASTCALL, nullptr},
                          {"gated", as_c(gated), METH_FASTCALL, nullptr},
                          {"gated_backward", as_c(gated_backward), METH_FASTCALL, nullptr},
+                         {"bind_i8", as_c(bind_i8), METH_FASTCALL, nullptr},
+                         {"i8_fits", as_c(i8_fits), METH_FASTCALL, nullptr},
+                         {"i8_store", as_c(i8_store), METH_FASTCALL, nullptr},
+                         {"i8_norm", as_c(i8_norm), METH_FASTCALL, nullptr},
+                         {"i8_matmul", as_c(i8_matmul), METH_FASTCALL, nullptr},
+                         {"i8_gated", as_c(i8_gated), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

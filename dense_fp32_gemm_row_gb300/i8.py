@@ -85,11 +85,17 @@ def _declare(lib) -> None:
 # ---- tensors ---------------------------------------------------------------------------------
 
 _torch = None  # set on first use: importing the package does not import torch
+_native = None  # the binding's module for quick calls, where it is built for the installed torch
 
 
 def _load_torch():
-    global _torch
+    global _torch, _native
     torch = _q8._torch or _q8._load_torch()
+    _native = _q8._native
+    if _native is not None:
+        lib = _g.load()
+        _native.bind_i8(*(ctypes.cast(getattr(lib, "gemm_f32_i8_" + name), ctypes.c_void_p).value
+                          for name in ("store", "norm", "matmul", "gated")), I8)
     _torch = torch
     return torch
 
@@ -136,7 +142,8 @@ class I8:
     def __init__(self, codes, scales, cols):
         if _torch is None:
             _load_torch()
-        _layout(codes, scales, cols)
+        if _native is None or not _native.i8_fits(codes, scales, cols):
+            _layout(codes, scales, cols)
         self.codes, self.scales, self.cols = codes, scales, cols
 
     @property
@@ -235,6 +242,10 @@ def i8_store(x, out=None, stream=None) -> I8:
     """The rows of ``x`` (float32 or bfloat16) in 8 bits, in ``out`` if given."""
     if _torch is None:
         _load_torch()
+    if out is None and stream is None and _native is not None:
+        q = _native.i8_store(x)
+        if q is not None:
+            return q
     code = _type(x.dtype, "x's type")
     rows, cols, ld = _matrix(x, "x")
     device = x.get_device()
@@ -256,6 +267,10 @@ def i8_norm(x, weight, residual=None, eps=1e-6, out=None, total=None, stream=Non
     """
     if _torch is None:
         _load_torch()
+    if out is None and total is None and stream is None and _native is not None:
+        made = _native.i8_norm(x, weight, residual, eps)
+        if made is not None:
+            return made
     code = _type(x.dtype, "x's type")
     rows, cols, ldx = _matrix(x, "x")
     device = x.get_device()
@@ -315,6 +330,10 @@ def i8_matmul(a, w, dtype=None, out=None, algo="auto", splits=0, stream=None):
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
     code = _type(dtype, "dtype", whole=True)
+    if out is None and stream is None and algo == "auto" and splits == 0 and _native is not None:
+        y = _native.i8_matmul(a, w, code)
+        if y is not None:
+            return y
     which = _q8._name(I8_ALGOS, algo, "algo")
     _q8._int(splits, "splits")
     _inputs(a, w)
@@ -339,6 +358,10 @@ def i8_gated(a, gate, up, act="silu", dtype=None, out=None, algo="auto", splits=
         dtype = torch.float32 if out is None else out.dtype
     code = _type(dtype, "dtype")
     which = _q8._name(_q8.ACTS, act, "act")
+    if out is None and stream is None and algo == "auto" and splits == 0 and _native is not None:
+        h = _native.i8_gated(a, gate, up, which, code)
+        if h is not None:
+            return h
     how = _q8._name(I8_ALGOS, algo, "algo")
     _q8._int(splits, "splits")
     _inputs(a, gate)

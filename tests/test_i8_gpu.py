@@ -419,6 +419,37 @@ def test_block_is_near_the_float_block():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("T", [1, 40])
+def test_the_binding_without_its_module(T, monkeypatch):
+    """The quick calls and the step by step ones: the same results, of the same kind."""
+    import dense_fp32_gemm_row_gb300.i8 as binding
+
+    b = Block(T, 250, 333, "bfloat16")
+    want = b()
+    assert binding._native is not None
+    plain, none = g.i8_norm(b.x, b.w)
+    monkeypatch.setattr(binding, "_native", None)
+    got = b()
+    q, s = g.i8_norm(b.x, b.w)
+    quiet()
+    assert same(got, want) and none is None and s is None and same({"q": q}, {"q": plain})
+    for x, y in zip(flat(got), flat(want)):
+        assert x.shape == y.shape and x.stride() == y.stride() and x.dtype == y.dtype
+    for x, y in ((got["q"], want["q"]), (got["hq"], want["hq"])):
+        assert (x.rows, x.cols, x.device, x.nbytes, x.codes.shape) == (y.rows, y.cols, y.device, y.nbytes, y.codes.shape)
+
+
+def test_matrices_whose_memory_is_gone():
+    torch = t()
+    q = g.i8_store(torch.randn(5, 70, device="cuda"))
+    w = g.i8_store(torch.randn(9, 70, device="cuda"))
+    q.codes.untyped_storage().resize_(0)
+    for call in (lambda: g.i8_matmul(q, w), lambda: g.i8_matmul(w, q), lambda: g.i8_gated(q, w, w),
+                 lambda: g.i8_store(torch.ones(5, 70, device="cuda"), out=q)):
+        with pytest.raises(ValueError, match="memory"):
+            call()
+
+
 @pytest.mark.parametrize("T", [1, 20, 300])
 def test_another_stream(T):
     torch = t()
