@@ -353,6 +353,21 @@ struct I8TmemArgs {
 cudaError_t launch_i8_tmem(const I8TmemMaps& maps, const I8TmemArgs& a, bool pair, int act,
                            cudaStream_t s, int dev, int sm_count);
 
+// The same for up to kI8StreamTokens tokens (i8_stream.cu).
+constexpr int kI8StreamTokens = 32;  // GEMM_F32_I8_STREAM_ROWS
+struct I8In {
+    const signed char* codes;
+    const float* scales;
+    long long ld;
+};
+struct I8StreamArgs {
+    I8In a, b, c;  // tokens, weights, with act >= 0 up's
+    void* y;
+    long long ldy;
+    int T, N, K, type, act;
+};
+cudaError_t launch_i8_stream(const I8StreamArgs& p, cudaStream_t s, int dev, int sm_count);
+
 // ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------
 // Device look-up and set-up, workspace and descriptors are one library-wide
 // state; api_mutex() is held around them and the launches of a call.

@@ -37,6 +37,8 @@ int check_arrays(const gemm_f32_i8* q) {
 Region codes_of(const gemm_f32_i8* q) { return region(q->codes, q->rows, q->cols, q->ld, 1); }
 Region scales_of(const gemm_f32_i8* q) { return region(q->scales, 1, q->rows, q->rows, 4); }
 
+I8In in_of(const gemm_f32_i8* q) { return {q->codes, q->scales, q->ld}; }
+
 int elem_of(int type) { return type == GEMM_F32_TYPE_BF16 ? 2 : 4; }
 bool is_float(int type) { return type == GEMM_F32_TYPE_F32 || type == GEMM_F32_TYPE_BF16; }
 
@@ -80,8 +82,8 @@ I8Share share_out(int T, int N, int K, bool gated, int algo, int splits, int sm_
 // Both products: y = a b^T, or with c the gated product of b and c.
 int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, int act, void* Y,
             int type, long long ldy, int algo, int splits, cudaStream_t stream) {
-    if ((algo != GEMM_F32_ALGO_AUTO && algo != GEMM_F32_ALGO_I8_PAIR &&
-         algo != GEMM_F32_ALGO_I8_SINGLE) ||
+    if ((algo != GEMM_F32_ALGO_AUTO &&
+         (algo < GEMM_F32_ALGO_I8_PAIR || algo > GEMM_F32_ALGO_I8_STREAM)) ||
         splits < 0 || splits > GEMM_F32_MAX_SPLITS)
         return GEMM_F32_ERR_INVALID_VALUE;
     I8_TRY(check_shape(a));
@@ -109,6 +111,12 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     if (K == 0)
         return status(launch_zero_rows(Y, ldy * elem_of(type), T,
                                        static_cast<long long>(N) * elem_of(type), stream));
+    if (algo == GEMM_F32_ALGO_I8_STREAM || (algo == GEMM_F32_ALGO_AUTO && T <= kI8StreamTokens)) {
+        if (T > kI8StreamTokens) return GEMM_F32_ERR_INVALID_VALUE;
+        const I8StreamArgs p = {in_of(a), in_of(b), c ? in_of(c) : I8In{}, Y, ldy, T, N, K, type,
+                                c ? act : -1};
+        return status(launch_i8_stream(p, stream, s.dev, s.sm_count));
+    }
     bool pair;
     I8TmemArgs k = {};
     k.share = share_out(T, N, K, c != nullptr, algo, splits, s.sm_count, &pair);

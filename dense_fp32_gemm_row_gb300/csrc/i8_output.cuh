@@ -1,6 +1,8 @@
-// i8_output.cuh -- from integer sums to the outputs of the 8-bit integer
-// products.
+// i8_output.cuh -- what the kernels of the 8-bit integer products share: from
+// codes to fp16 numbers, and from sums to outputs.
 #pragma once
+
+#include <cstdint>
 
 #include <cuda_bf16.h>
 
@@ -11,6 +13,22 @@ namespace gemm_f32_dev {
 constexpr int kI8Float = 0;
 constexpr int kI8Bfloat16 = 1;
 constexpr int kI8Int32 = 2;
+constexpr int kI8NoAct = -1;  // not the gated product
+
+// Four codes as two words of two fp16 numbers.
+__device__ __forceinline__ void decode_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t bias = 0x64806480u;  // 1024 + 128, twice
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(bias));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(bias));
+}
+
+__device__ __forceinline__ void decode_f16(const uint4& w, uint32_t (&h)[8]) {
+    decode_f16(w.x, h[0], h[1]);
+    decode_f16(w.y, h[2], h[3]);
+    decode_f16(w.z, h[4], h[5]);
+    decode_f16(w.w, h[6], h[7]);
+}
 
 // The value of a sum, as a float (rounded where it is beyond 2^24), the token's
 // scale first.

@@ -57,7 +57,6 @@ namespace {
 
 using namespace gemm_f32_dev;
 
-constexpr int kNoAct = -1;
 // Stages of K, 128 each, that one accumulator adds up, and the largest sum to
 // which another such is added exactly in fp32: 896 products of up to 2^14 are
 // 2^24 - 2^21.
@@ -136,21 +135,6 @@ __device__ __forceinline__ void sts_u32x8(uint32_t addr, const uint32_t (&h)[8])
 // Barrier `id` of the CTA's named ones, for `threads` of its threads.
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Four codes as two words of two fp16 numbers.
-__device__ __forceinline__ void decode_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t bias = 0x64806480u;  // 1024 + 128, twice
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(bias));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(bias));
-}
-
-__device__ __forceinline__ void decode_f16(const uint4& w, uint32_t (&h)[8]) {
-    decode_f16(w.x, h[0], h[1]);
-    decode_f16(w.y, h[2], h[3]);
-    decode_f16(w.z, h[4], h[5]);
-    decode_f16(w.w, h[6], h[7]);
 }
 
 // Offset of a 16-byte chunk: rows of 128 bytes, 128-byte swizzle.
@@ -299,7 +283,7 @@ __global__ void __launch_bounds__(I8Cfg<PAIR>::THREADS, 1)
 i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, I8TmemArgs p) {
     using C = I8Cfg<PAIR>;
-    constexpr bool GATED = ACT != kNoAct;
+    constexpr bool GATED = ACT != kI8NoAct;
     constexpr int STAGES = C::STAGES;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -804,7 +788,7 @@ cudaError_t launch_i8_tmem(const I8TmemMaps& maps, const I8TmemArgs& a, bool pai
                            cudaStream_t s, int dev, int sm_count) {
     if (act == kActSilu) return launch_form<kActSilu>(maps, a, pair, s, dev, sm_count);
     if (act == kActGelu) return launch_form<kActGelu>(maps, a, pair, s, dev, sm_count);
-    return launch_form<kNoAct>(maps, a, pair, s, dev, sm_count);
+    return launch_form<kI8NoAct>(maps, a, pair, s, dev, sm_count);
 }
 
 }  // namespace gemm_f32_impl

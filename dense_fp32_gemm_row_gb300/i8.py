@@ -25,7 +25,7 @@ from dense_fp32_gemm_row_gb300 import q8 as _q8
 
 __all__ = [
     "I8", "I8Struct", "TYPE_F32", "TYPE_BF16", "TYPE_I32", "I8_MAX_COLS", "I8_LEAST_EPS",
-    "ALGO_I8_PAIR", "ALGO_I8_SINGLE", "I8_ALGOS",
+    "ALGO_I8_PAIR", "ALGO_I8_SINGLE", "ALGO_I8_STREAM", "I8_STREAM_ROWS", "I8_ALGOS",
     "gemm_f32_i8_store", "gemm_f32_i8_norm", "gemm_f32_i8_matmul", "gemm_f32_i8_gated",
     "i8_empty", "i8_store", "i8_norm", "i8_matmul", "i8_gated",
 ]
@@ -37,7 +37,9 @@ I8_MAX_COLS = 131071
 I8_LEAST_EPS = 1e-30
 ALGO_I8_PAIR = 6
 ALGO_I8_SINGLE = 7
-I8_ALGOS = {"auto": 0, "pair": ALGO_I8_PAIR, "single": ALGO_I8_SINGLE}
+ALGO_I8_STREAM = 8
+I8_STREAM_ROWS = 32
+I8_ALGOS = {"auto": 0, "pair": ALGO_I8_PAIR, "single": ALGO_I8_SINGLE, "stream": ALGO_I8_STREAM}
 
 
 class I8Struct(ctypes.Structure):
@@ -323,8 +325,9 @@ def i8_matmul(a, w, dtype=None, out=None, algo="auto", splits=0, stream=None):
 
     The sums over codes are exact; ``dtype`` is float32 (the default) or
     bfloat16 for their values, or int32 for the sums themselves.  ``algo``
-    ("pair" or "single" CTAs a tile) and ``splits`` (of single CTAs' tiles, over
-    K) are chosen by size; results do not depend on them.
+    ("pair" or "single" CTAs a tile, or "stream" for at most 32 tokens) and
+    ``splits`` (of single CTAs' tiles, over K) are chosen by size; results do not
+    depend on them.
     """
     torch = _torch or _load_torch()
     if dtype is None:

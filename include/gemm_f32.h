@@ -537,11 +537,14 @@ int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr,
  * call, bit for bit.  algo: GEMM_F32_ALGO_AUTO, or this entry point's and
  * gated's own: the tensor-core kernel with tiles of CTA pairs (I8_PAIR) or of
  * single CTAs (I8_SINGLE), over how many ranges of K `splits` (at most
- * GEMM_F32_MAX_SPLITS; 0: the library chooses) splits the latter.  Results do
- * not depend on either.
+ * GEMM_F32_MAX_SPLITS; 0: the library chooses) splits the latter, or the kernel
+ * for a few tokens (I8_STREAM: a->rows at most GEMM_F32_I8_STREAM_ROWS).
+ * Results do not depend on either.
  */
 #define GEMM_F32_ALGO_I8_PAIR    6
 #define GEMM_F32_ALGO_I8_SINGLE  7
+#define GEMM_F32_ALGO_I8_STREAM  8
+#define GEMM_F32_I8_STREAM_ROWS  32
 #define GEMM_F32_I8_MAX_COLS 131071
 int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int type,
                        long long ldy, int algo, int splits, cudaStream_t stream);

@@ -86,7 +86,7 @@ def test_bad_arguments_are_invalid():
         assert g.gemm_f32_i8_gated(0, q, w, w, y, 0, ld) == BAD
     for act in (-1, 2):
         assert g.gemm_f32_i8_gated(act, q, w, w, Z, 0, 7) == BAD
-    for algo, splits in ((-1, 0), (1, 0), (5, 0), (8, 0), (0, -1), (7, 257)):
+    for algo, splits in ((-1, 0), (1, 0), (5, 0), (9, 0), (0, -1), (7, 257)):
         assert g.gemm_f32_i8_matmul(q, w, Z, 0, 7, algo, splits) == BAD
         assert g.gemm_f32_i8_gated(0, q, w, w, Z, 0, 7, algo, splits) == BAD
     # operands of one product have as many columns, those of a gated block one shape
@@ -135,8 +135,9 @@ def test_struct_and_constants_match_the_header(tmp_path):
                    "typedef void* cudaStream_t; typedef void* cudaEvent_t;\n"
                    "#include \"gemm_f32.h\"\nint main(void){\n"
                    + "".join(f'printf("%zu ", offsetof(gemm_f32_i8, {f}));' for f in fields)
-                   + 'printf("%zu %d %d %d %d %d\\n", sizeof(gemm_f32_i8), GEMM_F32_TYPE_F32, '
+                   + 'printf("%zu %d %d %d %d %d %d\\n", sizeof(gemm_f32_i8), GEMM_F32_TYPE_F32, '
                    "GEMM_F32_TYPE_BF16, GEMM_F32_TYPE_I32, GEMM_F32_I8_MAX_COLS, "
+                   "GEMM_F32_I8_STREAM_ROWS, "
                    "GEMM_F32_I8_LEAST_EPS == 1e-30f); return 0; }\n")
     (tmp_path / "cuda_runtime_api.h").write_text("")
     exe = tmp_path / "layout"
@@ -146,7 +147,7 @@ def test_struct_and_constants_match_the_header(tmp_path):
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
                                           check=True).stdout.split()]
     assert got == [getattr(g.I8Struct, f).offset for f in fields] + [
-        ctypes.sizeof(g.I8Struct), g.TYPE_F32, g.TYPE_BF16, g.TYPE_I32, g.I8_MAX_COLS, 1]
+        ctypes.sizeof(g.I8Struct), g.TYPE_F32, g.TYPE_BF16, g.TYPE_I32, g.I8_MAX_COLS, g.I8_STREAM_ROWS, 1]
 
 
 # ---- the binding, on stand-ins for CUDA tensors ---------------------------------------------------

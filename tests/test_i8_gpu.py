@@ -254,10 +254,15 @@ def test_gated(T, N, K, act, name):
     assert np.all(np.abs(down(y) - want) <= bound)
 
 
-@pytest.mark.parametrize("algo,splits", [("pair", 0), ("single", 1), ("single", 2), ("single", 5), ("single", 256)])
+@pytest.mark.parametrize("algo,splits", [("pair", 0), ("single", 1), ("single", 2), ("single", 5), ("single", 256), ("stream", 0)])
 @pytest.mark.parametrize("T,N,K", PRODUCTS[::3] + [(257, 129, 1024), (513, 1023, 1088), (129, 513, 8200)])
 def test_forced_forms(T, N, K, algo, splits):
     torch = t()
+    if algo == "stream" and T > g.I8_STREAM_ROWS:
+        some = g.i8_empty(T, K)
+        with pytest.raises(g.GemmError):
+            g.i8_matmul(some, some, algo=algo)
+        return
     rng = np.random.default_rng(T + N + K)
     qa, a, _ = operand(rng, T, K)
     (qb, b, sb), (qc, _, sc) = operand(rng, N, K), operand(rng, N, K)
