@@ -28,17 +28,17 @@
 // turn, its tiles split over K for few tokens.  The gated form has 16 channels of
 // the gate and the same of up in the lanes of a warp, which exchange sums.
 //
-// 640 threads per CTA, registers rebalanced at start (launched at 96 each):
+// 640 threads per CTA (of narrow tiles 768), registers rebalanced at start (launched
+// at 96 each, 80):
 //   warp 0       one lane: TMA loads of a 128-column stage of raw codes;
 //   warp 1       tensor-memory allocation; one lane (of a pair: the leader's)
 //                issues the MMAs and commits;
 //   warps 1-2 of a pair's peer  relay: one lane each tells the leader, in turn,
 //                that the peer's operands of a stage are written;
-//   warps 4-7, 8-11  conversion of every other stage each: weights to fp16 in
-//                tensor memory (warp 4 + q: lanes 32 q ..), tokens to fp16 in
-//                shared memory;
-//   warps 12-19  per chunk add the accumulator to the sums in their registers
-//                (warp 12 + e: lanes 32 (e % 4) .., half e / 4 of the columns);
+//   then 8 (12)  conversion, a warpgroup a stage: weights to fp16 in tensor memory
+//                (its warp q: lanes 32 q ..), tokens to fp16 in shared memory;
+//   the last 8   per chunk add the accumulator to the sums in their registers
+//                (warp e of them: lanes 32 (e % 4) .., half e / 4 of the columns);
 //                at the end of a unit scale and store them.
 // Splits of a tile write their sums to the workspace, and the one that comes
 // last, by a counter a tile, adds the others' to its own: nothing waits, and
@@ -64,17 +64,23 @@ constexpr int kStageK = 128;
 constexpr int kChunk = 7;
 constexpr float kMostBefore = 16777216.0f - kChunk * kStageK * 16384.0f;
 
-template <bool PAIR_>
+// A pair's CTA, a single one, and a single one for tiles of up to 64 tokens,
+// which has room for more stages and a third warpgroup that converts: there the
+// weights' way from DRAM is what a stage takes.
+enum Form { kPair, kWide, kNarrow };
+
+template <Form FORM>
 struct I8Cfg {
-    static constexpr bool PAIR = PAIR_;
+    static constexpr bool PAIR = FORM == kPair, NARROW = FORM == kNarrow;
     static constexpr int CTAS = PAIR ? 2 : 1;
     static constexpr int LANES = 128;                // rows of weights of a CTA
-    static constexpr int TOK = 128;                  // tokens of a CTA, at most
+    static constexpr int TOK = NARROW ? 64 : 128;    // tokens of a CTA, at most
     static constexpr int COLS = TOK * CTAS;          // accumulator columns
     static constexpr int KT = kStageK;               // K a stage
     static constexpr int UK = 16;                    // K an MMA
-    static constexpr int RAW = 3;                    // stages of raw codes
-    static constexpr int STAGES = 4;                 // stages of MMA operands
+    static constexpr int RAW = NARROW ? 5 : 3;       // stages of raw codes
+    static constexpr int STAGES = NARROW ? 6 : 4;    // stages of MMA operands
+    static constexpr int GROUPS = NARROW ? 3 : 2;    // warpgroups that convert, a stage each
     static constexpr int ACCS = PAIR ? 1 : 2;        // accumulators
     static constexpr int B_HALF = TOK * 128;         // tokens in fp16: rows of 64, K halves
     static constexpr int B_BYTES = 2 * B_HALF;
@@ -85,31 +91,33 @@ struct I8Cfg {
     static constexpr int EPI_WARPS = 8;
     static constexpr int BAR_OFF = RAW_OFF + RAW * RAW_BYTES;
     static constexpr int CONV_WARPS = 4;             // of a stage
-    // full, free (raw stages), empty, ready (per operand stage), acc_full and
-    // acc_empty (per accumulator), drain
-    static constexpr int NBARS = 3 * RAW + 2 * STAGES + 2 * ACCS + 1;
-    static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;
-    static constexpr int THREADS = 640;
-    static constexpr int TMEM_COLS = 512;
-    static constexpr int OP_COL0 = 256;              // operand stage s at OP_COL0 + 64 s
-    static constexpr int OP_COLS = KT / 2;
     static constexpr int RELAYS = 2;
     // A wait by parity has to come after the end of the barrier's phase before.
     // Each barrier's stages belong to one warpgroup of the conversion and to one
-    // relay, which take theirs in order; raw slots, an odd number of them, have
-    // two barriers each in turn.
-    static constexpr int FULLS = 2 * RAW;
+    // relay, which take theirs in order; raw slots, whose number the groups do not
+    // divide, have a barrier for each group.
+    static constexpr int FULLS = GROUPS * RAW;
+    // full, free (raw stages), empty, ready (per operand stage), acc_full and
+    // acc_empty (per accumulator), drain
+    static constexpr int NBARS = FULLS + RAW + 2 * STAGES + 2 * ACCS + 1;
+    static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;
+    static constexpr int EPI_WARP0 = 4 + 4 * GROUPS;
+    static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int OP_COL0 = ACCS * COLS;      // operand stage s at OP_COL0 + 64 s
+    static constexpr int OP_COLS = KT / 2;
     static constexpr int EPI_COLS = COLS / 2;        // of a warp, at most
-    static constexpr int REGS_LAUNCH = 96;
-    static constexpr int REGS_CONTROL = 32, REGS_CONV = 56, REGS_EPI = 168;
+    static constexpr int REGS_LAUNCH = NARROW ? 80 : 96;
+    static constexpr int REGS_CONTROL = 32, REGS_CONV = 56, REGS_EPI = NARROW ? 136 : 168;
     // D fp32, A and B fp16, both K-major, M = 128 a CTA; N is added
     static constexpr uint32_t IDESC = (1u << 4) | (static_cast<uint32_t>(LANES * CTAS >> 4) << 24);
-    static_assert(REGS_CONTROL + 2 * REGS_CONV + 2 * REGS_EPI <= 5 * REGS_LAUNCH,
+    static_assert(REGS_CONTROL + GROUPS * REGS_CONV + EPI_WARPS / 4 * REGS_EPI <=
+                      THREADS / 128 * REGS_LAUNCH,
                   "register shares");
-    static_assert(OP_COL0 + STAGES * OP_COLS <= TMEM_COLS && ACCS * COLS <= OP_COL0,
-                  "tensor-memory columns");
+    static_assert(OP_COL0 + STAGES * OP_COLS <= TMEM_COLS, "tensor-memory columns");
     static_assert(KT == 128, "two swizzled halves of K");
-    static_assert(STAGES % 2 == 0 && RELAYS % 2 == 0 && RAW < STAGES, "phases of the barriers");
+    static_assert(STAGES % GROUPS == 0 && (!PAIR || RELAYS == GROUPS) && RAW < STAGES,
+                  "phases of the barriers");
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -278,11 +286,12 @@ __device__ __forceinline__ void put_gated(const float (&acc)[COLS], const float 
     }
 }
 
-template <bool PAIR, int ACT>
-__global__ void __launch_bounds__(I8Cfg<PAIR>::THREADS, 1)
+template <Form FORM, int ACT>
+__global__ void __launch_bounds__(I8Cfg<FORM>::THREADS, 1)
 i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, I8TmemArgs p) {
-    using C = I8Cfg<PAIR>;
+    using C = I8Cfg<FORM>;
+    constexpr bool PAIR = C::PAIR;
     constexpr bool GATED = ACT != kI8NoAct;
     constexpr int STAGES = C::STAGES;
     extern __shared__ unsigned char smem_raw[];
@@ -300,7 +309,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t abort_flag = smem_addr(tmem_slot + 1);
     const uint32_t last_flag = smem_addr(tmem_slot + 2);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
     const int first = blockIdx.x / C::CTAS, step = gridDim.x / C::CTAS;
@@ -403,12 +412,17 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             __syncwarp();
         } else if (warp == 1) {
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
                 // -------------------------- MMA issuer (of a pair: the leader) --------
-                int it = 0;
-                int g = 0;  // chunks issued
+                // The whole warp waits, so that descriptors and addresses are the warp's
+                // and not a lane's; one lane issues.
+                const bool elected = elect_lane();
+                int s = 0;            // operand stage, and its phase
+                uint32_t phase = 0;
+                int g = 0;            // chunks issued
                 bool ok = true;
                 Work w;
+                const uint64_t x0 = smem_desc_sw128_kmajor(sbase);
                 for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
                     const uint32_t idesc =
                         C::IDESC | static_cast<uint32_t>(
@@ -418,42 +432,54 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         const int b = g % C::ACCS;
                         // the accumulator: its last chunk has been drained
                         if (g >= C::ACCS &&
-                            !role_wait(acce + 8 * b, ((g / C::ACCS) - 1) & 1, timeout_ns, fault,
-                                       kFaultAccumBarrier, abort_flag)) {
+                            !__all_sync(0xffffffffu,
+                                        role_wait(acce + 8 * b, ((g / C::ACCS) - 1) & 1, timeout_ns,
+                                                  fault, kFaultAccumBarrier, abort_flag))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::COLS);
                         const int c1 = min(w.nkb, c0 + kChunk);
-                        for (int kb = c0; kb < c1; ++kb, ++it) {
-                            const int s = it % STAGES;
-                            if (!role_wait<PAIR>(ready0 + 8 * s, (it / STAGES) & 1, timeout_ns,
-                                                 fault, kFaultFullBarrier, abort_flag)) {
+                        for (int kb = c0; kb < c1; ++kb) {
+                            if (!__all_sync(0xffffffffu,
+                                            role_wait<PAIR>(ready0 + 8 * s, phase, timeout_ns, fault,
+                                                            kFaultFullBarrier, abort_flag))) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
-                            const uint64_t x = smem_desc_sw128_kmajor(sbase + s * C::B_BYTES);
+                            const uint64_t x = x0 + static_cast<uint64_t>(s * (C::B_BYTES >> 4));
                             const uint32_t a =
                                 tmem_base + static_cast<uint32_t>(C::OP_COL0 + C::OP_COLS * s);
+                            if (elected) {
 #pragma unroll
-                            for (int k = 0; k < C::KT / C::UK; ++k)
-                                // 16 columns of K: 32 bytes of a row, 8 columns of tensor memory
-                                mma_f16_tmem_a<PAIR>(d, a + 8u * k,
-                                                     x + (k / 4) * (C::B_HALF >> 4) + 2u * (k % 4),
-                                                     idesc, (kb > c0 || k > 0) ? 1u : 0u);
-                            mma_commit_form<PAIR>(empty0 + 8 * s);
+                                for (int k = 0; k < C::KT / C::UK; ++k)
+                                    // 16 columns of K: 32 bytes of a row, 8 columns of tensor
+                                    // memory
+                                    mma_f16_tmem_a<PAIR>(
+                                        d, a + 8u * k,
+                                        x + (k / 4) * (C::B_HALF >> 4) + 2u * (k % 4), idesc,
+                                        (kb > c0 || k > 0) ? 1u : 0u);
+                                mma_commit_form<PAIR>(empty0 + 8 * s);
+                            }
+                            if (++s == STAGES) {
+                                s = 0;
+                                phase ^= 1;
+                            }
                         }
                         if (!ok) break;
-                        mma_commit_form<PAIR>(accf + 8 * b);
+                        if (elected) mma_commit_form<PAIR>(accf + 8 * b);
                     }
                 }
-                if (PAIR)
-                    mma_commit_pair(drain);
-                else
-                    mma_commit(drain);
-                mbar_wait(drain, 0, ok ? timeout_ns : timeout_ns / 8 + 1000, fault, kFaultDrain);
+                if (elected) {
+                    if (PAIR)
+                        mma_commit_pair(drain);
+                    else
+                        mma_commit(drain);
+                    mbar_wait(drain, 0, ok ? timeout_ns : timeout_ns / 8 + 1000, fault, kFaultDrain);
+                }
+                __syncwarp();
             } else if (PAIR && lane == 0) {
                 relay(0);
             }
@@ -463,9 +489,9 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             relay(1);
         }
         __syncwarp();
-    } else if (warp < 12) {
-        // ------------------------------ conversion (warps 4-11) ------------------------
-        // A warpgroup takes every other stage, a half of K at a time.  Weights: a
+    } else if (warp < C::EPI_WARP0) {
+        // ------------------------------ conversion -------------------------------------
+        // A warpgroup takes every second or third stage, a half of K at a time.  Weights: a
         // thread has its lane's row (gated: 16 of a warp's lanes the gate's, 16
         // up's).  Tokens: a lane takes 16 codes; each eight lanes load from two rows
         // whose numbers differ in bits 0 and 2, so that both the codes and the two
@@ -483,14 +509,14 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t weights_at = swizzled(row, 0);  // of the first chunk
         const uint32_t tokens_at = swizzled(row0, c), fp16_at = swizzled(row0, 2u * c);
         int it = 0;
-        const int parity = (warp >> 2) - 1;
+        const int group = (warp >> 2) - 1;
         bool ok = true;
         Work w;
         for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
             const int rows = cta_tokens<PAIR>(share.tokens, p.T - w.t0);
             const int items = (rows - 8 * q + 31) / 32;  // of this warp: 8 rows each
             for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                if ((it & 1) != parity) continue;
+                if (it % C::GROUPS != group) continue;
                 const int s = it % STAGES, raw = it % C::RAW;
                 const bool got = role_wait(full0 + 8 * (it % C::FULLS), (it / C::FULLS) & 1,
                                            timeout_ns, fault, kFaultFullBarrier, abort_flag);
@@ -545,6 +571,9 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         sts_u32x8(to_x + C::B_HALF + kItemBytes * i, h);
                     }
                 }
+                // every code has been read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(free0 + 8 * raw);
 #pragma unroll
                 for (uint32_t i = 0; i < 4; ++i) {
                     uint32_t h[8];
@@ -563,19 +592,16 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(ready0 + 8 * s);
-                    mbar_arrive(free0 + 8 * raw);
-                }
+                if (lane == 0) mbar_arrive(ready0 + 8 * s);
             }
         }
         __syncwarp();
     } else {
-        // ------------------------------ epilogue (warps 12-19) ------------------------
+        // ------------------------------ epilogue ---------------------------------------
         // All eight warps walk through the same units whatever happens, so that the
         // named barriers always find them.
         regs_inc<C::REGS_EPI>();
-        const int e = warp - 12;
+        const int e = warp - C::EPI_WARP0;
         const int q = warp & 3;                  // lanes 32 q .. 32 q + 31
         const int half = e >> 2;
         const int n_lane = GATED ? rank * (C::LANES / 2) + 16 * q + (lane & 15)
@@ -633,8 +659,12 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 const long long slot = static_cast<long long>(share.tokens) * C::LANES;
                 int* const mine = p.parts + u * slot + col0 * C::LANES + 32 * q + lane;
 #pragma unroll
-                for (int j = 0; j < C::EPI_COLS; ++j)
-                    if (j < count) __stcg(mine + j * C::LANES, __float_as_int(acc[j]));
+                for (int j = 0; j < C::EPI_COLS; j += 16) {
+                    if (j >= count) break;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        __stcg(mine + (j + i) * C::LANES, __float_as_int(acc[j + i]));
+                }
                 __threadfence();
                 named_sync(1, 32 * C::EPI_WARPS);
                 if (e == 0 && lane == 0) {
@@ -650,10 +680,16 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 for (int s = 0; s < share.splits; ++s) {
                     if (w.tile * share.splits + s == u) continue;
 #pragma unroll
-                    for (int j = 0; j < C::EPI_COLS; ++j)
-                        if (j < count)
-                            acc[j] = __int_as_float(__float_as_int(acc[j]) +
-                                                    __ldcg(all + s * slot + j * C::LANES));
+                    for (int j = 0; j < C::EPI_COLS; j += 16) {
+                        if (j >= count) break;
+                        int more[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            more[i] = __ldcg(all + s * slot + (j + i) * C::LANES);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            acc[j + i] = __int_as_float(__float_as_int(acc[j + i]) + more[i]);
+                    }
                 }
             }
             // from here the sums as floats, or as the integers they are
@@ -722,28 +758,28 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 // mutex is held).  The register rebalancing would wait for ever for registers
 // that the block was not launched with, so a build in which the compiler took
 // fewer than REGS_LAUNCH a thread is refused here.
-template <bool PAIR, int ACT>
+template <Form FORM, int ACT>
 cudaError_t configure(int dev) {
-    using C = I8Cfg<PAIR>;
+    using C = I8Cfg<FORM>;
     constexpr int kDevices = 64;
     static bool done[kDevices] = {};
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, i8_tmem_kernel<PAIR, ACT>);
+    cudaError_t e = cudaFuncGetAttributes(&attr, i8_tmem_kernel<FORM, ACT>);
     if (e != cudaSuccess) return e;
     if (attr.numRegs < C::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(i8_tmem_kernel<PAIR, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(i8_tmem_kernel<FORM, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::SMEM_BYTES);
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
 
-template <bool PAIR, int ACT>
+template <Form FORM, int ACT>
 cudaError_t launch(const I8TmemMaps& maps, const I8TmemArgs& a, cudaStream_t s, int dev,
                    int sm_count) {
-    using C = I8Cfg<PAIR>;
-    cudaError_t e = configure<PAIR, ACT>(dev);
+    using C = I8Cfg<FORM>;
+    cudaError_t e = configure<FORM, ACT>(dev);
     if (e != cudaSuccess) return e;
     const long long units =
         static_cast<long long>(a.share.tiles_c) * a.share.tiles_t * a.share.splits;
@@ -760,28 +796,29 @@ cudaError_t launch(const I8TmemMaps& maps, const I8TmemArgs& a, cudaStream_t s, 
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, i8_tmem_kernel<PAIR, ACT>, maps.a, maps.b, maps.c, a);
+    cfg.numAttrs = C::PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, i8_tmem_kernel<FORM, ACT>, maps.a, maps.b, maps.c, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int ACT>
 cudaError_t launch_form(const I8TmemMaps& maps, const I8TmemArgs& a, bool pair, cudaStream_t s,
                         int dev, int sm_count) {
-    return pair ? launch<true, ACT>(maps, a, s, dev, sm_count)
-                : launch<false, ACT>(maps, a, s, dev, sm_count);
+    if (pair) return launch<kPair, ACT>(maps, a, s, dev, sm_count);
+    return a.share.tokens <= I8Cfg<kNarrow>::TOK ? launch<kNarrow, ACT>(maps, a, s, dev, sm_count)
+                                                 : launch<kWide, ACT>(maps, a, s, dev, sm_count);
 }
 
 }  // namespace
 
 I8Tile i8_tile(bool pair) {
-    using P = I8Cfg<true>;
+    using P = I8Cfg<kPair>;
     return {pair ? 2 * P::LANES : P::LANES, P::TOK, P::KT};
 }
 
 size_t i8_parts_bytes(const I8Share& s) {
     if (s.splits < 2) return 0;
-    return static_cast<size_t>(s.tiles_c) * s.tiles_t * s.splits * s.tokens * I8Cfg<false>::LANES * 4;
+    return static_cast<size_t>(s.tiles_c) * s.tiles_t * s.splits * s.tokens * I8Cfg<kWide>::LANES * 4;
 }
 
 cudaError_t launch_i8_tmem(const I8TmemMaps& maps, const I8TmemArgs& a, bool pair, int act,
