@@ -182,11 +182,18 @@ __device__ __forceinline__ int cta_tokens(int tokens, int left) {
     return min(tokens, (each + 15) & ~15);
 }
 
+__device__ __forceinline__ void add_pair(float& a, float& b, uint32_t x, uint32_t y) {
+    asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\t"
+        "add.rn.f32x2 s, s, t;\n\tmov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x), "r"(y));
+}
+
 // Adds an accumulator's columns to acc, which holds floats or (`whole`) 32-bit
-// integers.
-template <int COLS>
+// integers; loaded() once it has been read.
+template <int COLS, typename F>
 __device__ __forceinline__ void add_columns(float (&acc)[COLS], uint32_t tbase, int count,
-                                            bool whole) {
+                                            bool whole, F loaded) {
     if (whole) {
 #pragma unroll
         for (int j = 0; j < COLS; j += 16) {
@@ -199,8 +206,10 @@ __device__ __forceinline__ void add_columns(float (&acc)[COLS], uint32_t tbase, 
                 acc[j + i] = __int_as_float(__float_as_int(acc[j + i]) +
                                             __float2int_rn(__uint_as_float(r[i])));
         }
+        loaded();
         return;
     }
+    if (count <= 0) loaded();
 #pragma unroll
     for (int j = 0; j < COLS; j += 32) {
         if (j >= count) break;
@@ -209,8 +218,10 @@ __device__ __forceinline__ void add_columns(float (&acc)[COLS], uint32_t tbase, 
         tmem_ld_32x32b_x16(tbase + j + 16, r[1]);
         tmem_ld_wait(r[0]);
         tmem_ld_wait(r[1]);
+        if (j + 32 >= count) loaded();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[j + i] += __uint_as_float(r[i / 16][i % 16]);
+        for (int i = 0; i < 32; i += 2)
+            add_pair(acc[j + i], acc[j + i + 1], r[i / 16][i % 16], r[i / 16][i % 16 + 1]);
     }
 }
 
@@ -375,34 +386,44 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     if (warp < 4) {
         regs_dec<C::REGS_CONTROL>();
         if (warp == 0) {
-            if (lane == 0) {
-                // -------------------------- TMA producer ------------------------------
-                int it = 0;
-                bool ok = true;
-                Work w;
-                const uint32_t bytes = C::W_RAW + static_cast<uint32_t>(share.tokens * C::KT);
-                for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
-                    const int tok0 = w.t0 + rank * cta_tokens<PAIR>(share.tokens, p.T - w.t0);
-                    const int ch0 = w.c0 + rank * (GATED ? C::LANES / 2 : C::LANES);
-                    for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                        const int r = it % C::RAW;
-                        if (it >= C::RAW &&
-                            !role_wait(free0 + 8 * r, ((it / C::RAW) & 1) ^ 1, timeout_ns, fault,
-                                       kFaultEmptyBarrier, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        const int k0 = (w.kb_begin + kb) * C::KT;
-                        const uint32_t fb = full0 + 8 * (it % C::FULLS);
-                        const uint32_t wb = sbase + C::RAW_OFF + r * C::RAW_BYTES;
+            // ------------------------------ TMA producer ------------------------------
+            const bool elected = elect_lane();
+            int it = 0;
+            int r = 0, f = 0;  // raw slot and its phase, barrier
+            uint32_t r_phase = 1;
+            bool ok = true;
+            Work w;
+            const uint32_t bytes = C::W_RAW + static_cast<uint32_t>(share.tokens * C::KT);
+            for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
+                const int tok0 = w.t0 + rank * cta_tokens<PAIR>(share.tokens, p.T - w.t0);
+                const int ch0 = w.c0 + rank * (GATED ? C::LANES / 2 : C::LANES);
+                int k0 = w.kb_begin * C::KT;
+                for (int kb = 0; kb < w.nkb; ++kb, ++it, k0 += C::KT) {
+                    if (it >= C::RAW &&
+                        !__all_sync(0xffffffffu,
+                                    role_wait(free0 + 8 * r, r_phase, timeout_ns, fault,
+                                              kFaultEmptyBarrier, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = full0 + 8 * f;
+                    const uint32_t wb = sbase + C::RAW_OFF + r * C::RAW_BYTES;
+                    if (elected) {
                         mbar_arrive_expect_tx(fb, bytes);
                         tma_load_2d(wb, &tmB, fb, k0, ch0);
                         if (GATED) tma_load_2d(wb + C::W_RAW / 2, &tmC, fb, k0, ch0);
                         tma_load_2d(wb + C::W_RAW, &tmA, fb, k0, tok0);
                     }
+                    if (++f == C::FULLS) f = 0;
+                    if (++r == C::RAW) {
+                        r = 0;
+                        r_phase ^= 1;
+                    }
                 }
-                // wind down: this CTA's copies have landed, and the MMAs' commits
-                // have reached its operand stages
+            }
+            // wind down: this CTA's copies have landed, and the MMAs' commits have
+            // reached its operand stages
+            if (elected) {
                 const long long tail = ok ? timeout_ns : timeout_ns / 8 + 1000;
                 for (int j = (it > C::RAW ? it - C::RAW : 0); j < it; ++j)
                     mbar_wait(full0 + 8 * (j % C::FULLS), (j / C::FULLS) & 1, tail, fault,
@@ -508,18 +529,19 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             static_cast<uint32_t>(8 * q + ((lane >> 3) ^ ((lane & 4) ? 5 : 0)));
         const uint32_t weights_at = swizzled(row, 0);  // of the first chunk
         const uint32_t tokens_at = swizzled(row0, c), fp16_at = swizzled(row0, 2u * c);
-        int it = 0;
         const int group = (warp >> 2) - 1;
+        // its next stage of all, operand stage and raw slot and barrier, with phases
+        int it = group, s = group, raw = group % C::RAW, f = group;
+        uint32_t s_phase = 1, f_phase = 0;
+        int base = 0;
         bool ok = true;
         Work w;
-        for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); u += step) {
+        for (int u = first; ok && work_at<PAIR, GATED>(share, u, w); base += w.nkb, u += step) {
             const int rows = cta_tokens<PAIR>(share.tokens, p.T - w.t0);
             const int items = (rows - 8 * q + 31) / 32;  // of this warp: 8 rows each
-            for (int kb = 0; kb < w.nkb; ++kb, ++it) {
-                if (it % C::GROUPS != group) continue;
-                const int s = it % STAGES, raw = it % C::RAW;
-                const bool got = role_wait(full0 + 8 * (it % C::FULLS), (it / C::FULLS) & 1,
-                                           timeout_ns, fault, kFaultFullBarrier, abort_flag);
+            for (; it < base + w.nkb; it += C::GROUPS) {
+                const bool got = role_wait(full0 + 8 * f, f_phase, timeout_ns, fault,
+                                           kFaultFullBarrier, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
@@ -537,8 +559,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 for (int i = 0; i < kItems; ++i)
                     if (items == kItems) x[i] = lds_u32x4(from_x + kItemBytes * i);
                 if (it >= STAGES) {
-                    const bool can = role_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, timeout_ns,
-                                               fault, kFaultEmptyBarrier, abort_flag);
+                    const bool can = role_wait(empty0 + 8 * s, s_phase, timeout_ns, fault,
+                                               kFaultEmptyBarrier, abort_flag);
                     if (!__all_sync(0xffffffffu, can)) {
                         ok = false;
                         break;
@@ -593,6 +615,15 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ready0 + 8 * s);
+                if ((s += C::GROUPS) >= STAGES) {
+                    s -= STAGES;
+                    s_phase ^= 1;
+                }
+                if ((f += C::GROUPS) >= C::FULLS) {
+                    f -= C::FULLS;
+                    f_phase ^= 1;
+                }
+                raw = (raw + C::GROUPS) % C::RAW;
             }
         }
         __syncwarp();
@@ -637,16 +668,17 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 tc_fence_after();
                 const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                                        static_cast<uint32_t>(b * C::COLS + col0);
-                add_columns<C::EPI_COLS>(acc, tbase, count, whole);
-                // the loads have completed: the arrival orders no writes
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR)
-                        mbar_arrive_remote(acce_leader + 8 * b);
-                    else
-                        mbar_arrive(acce + 8 * b);
-                }
+                add_columns<C::EPI_COLS>(acc, tbase, count, whole, [&] {
+                    // the loads have completed: the arrival orders no writes
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR)
+                            mbar_arrive_remote(acce_leader + 8 * b);
+                        else
+                            mbar_arrive(acce + 8 * b);
+                    }
+                });
                 // off the MMAs' path
                 if (c0 + kChunk < w.nkb) keep_exact<C::EPI_COLS>(acc, whole);
             }
