@@ -11,8 +11,8 @@
 // codes do not depend on the order in which a row is summed.  A row in which z
 // is not finite gets codes 0 and scale NaN.
 //
-// Bounded by HBM: a row is read once, held in registers (32 columns a thread)
-// between the two steps, and written once.  Rows beyond 16384 columns are read
+// Bounded by HBM: a row is read once, held in registers (up to 32 columns a
+// thread) between the two steps, and written once.  Rows beyond 16384 columns are read
 // a second time, from L2.
 #include <cstdint>
 
@@ -27,7 +27,6 @@ namespace {
 using namespace gemm_f32_dev;
 
 constexpr int kLane = 8;   // consecutive columns of a thread: 8 bytes of codes
-constexpr int kHeld = 4;   // such groups that a thread holds
 constexpr unsigned kInfinity = 0x7F800000u;
 constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
 
@@ -37,8 +36,11 @@ struct Group {
     float v[kLane];
 };
 
-// Columns of a thread: kLane consecutive ones from col (VEC), or, where rows do
-// not start on 16-byte boundaries, every stride-th from col.
+// Columns of a thread: kLane consecutive ones from col, all or none of them in the
+// row (VEC), or, where rows do not start on 16-byte boundaries or are no multiple
+// of kLane, every stride-th from col.  No load is behind a branch, so that all
+// are under way at once (a test of each vector's columns: 8192 x 8192 bf16 157
+// us).
 struct Columns {
     int col, n, stride;  // n of kLane are in the row
 };
@@ -48,7 +50,7 @@ __device__ __forceinline__ Columns columns(int group, int thread, int threads, i
     if (VEC) {
         c.col = (group * threads + thread) * kLane;
         c.stride = 1;
-        c.n = max(0, min(kLane, cols - c.col));
+        c.n = c.col < cols ? kLane : 0;
     } else {
         c.col = group * threads * kLane + thread;
         c.stride = threads;
@@ -63,9 +65,12 @@ __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162floa
 template <bool VEC>
 __device__ __forceinline__ Group load(const float* p, const Columns& c) {
     Group g;
-    if (VEC && c.n == kLane) {
-        const float4 lo = reinterpret_cast<const float4*>(p + c.col)[0];
-        const float4 hi = reinterpret_cast<const float4*>(p + c.col)[1];
+    if (VEC) {
+        float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+        if (c.n) {
+            lo = reinterpret_cast<const float4*>(p + c.col)[0];
+            hi = reinterpret_cast<const float4*>(p + c.col)[1];
+        }
         g.v[0] = lo.x, g.v[1] = lo.y, g.v[2] = lo.z, g.v[3] = lo.w;
         g.v[4] = hi.x, g.v[5] = hi.y, g.v[6] = hi.z, g.v[7] = hi.w;
     } else {
@@ -77,8 +82,9 @@ __device__ __forceinline__ Group load(const float* p, const Columns& c) {
 template <bool VEC>
 __device__ __forceinline__ Group load(const __nv_bfloat16* p, const Columns& c) {
     Group g;
-    if (VEC && c.n == kLane) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p + c.col);
+    if (VEC) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (c.n) w = *reinterpret_cast<const uint4*>(p + c.col);
         const unsigned u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -93,7 +99,8 @@ __device__ __forceinline__ Group load(const __nv_bfloat16* p, const Columns& c) 
 }
 template <bool VEC>
 __device__ __forceinline__ void put(float* p, const Columns& c, const Group& g) {
-    if (VEC && c.n == kLane) {
+    if (VEC) {
+        if (!c.n) return;
         reinterpret_cast<float4*>(p + c.col)[0] = make_float4(g.v[0], g.v[1], g.v[2], g.v[3]);
         reinterpret_cast<float4*>(p + c.col)[1] = make_float4(g.v[4], g.v[5], g.v[6], g.v[7]);
     } else {
@@ -104,14 +111,14 @@ __device__ __forceinline__ void put(float* p, const Columns& c, const Group& g) 
 }
 template <bool VEC>
 __device__ __forceinline__ void put(__nv_bfloat16* p, const Columns& c, const Group& g) {
-    if (VEC && c.n == kLane) {
+    if (VEC) {
         unsigned u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __nv_bfloat162 two = __floats2bfloat162_rn(g.v[2 * i], g.v[2 * i + 1]);
             u[i] = *reinterpret_cast<const unsigned*>(&two);
         }
-        *reinterpret_cast<uint4*>(p + c.col) = make_uint4(u[0], u[1], u[2], u[3]);
+        if (c.n) *reinterpret_cast<uint4*>(p + c.col) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < kLane; ++i)
@@ -129,11 +136,11 @@ __device__ __forceinline__ void put_codes(signed char* p, const Columns& c, cons
 #pragma unroll
     for (int i = 0; i < kLane; ++i)
         q[i] = finite ? __float_as_uint(__fadd_rn(__fmul_rn(z.v[i], inv), 12582912.0f)) : 0u;
-    if (VEC && c.n == kLane) {
+    if (VEC) {
         uint2 w;
         w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
         w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
-        *reinterpret_cast<uint2*>(p + c.col) = w;
+        if (c.n) *reinterpret_cast<uint2*>(p + c.col) = w;
     } else {
 #pragma unroll
         for (int i = 0; i < kLane; ++i)
@@ -141,22 +148,29 @@ __device__ __forceinline__ void put_codes(signed char* p, const Columns& c, cons
     }
 }
 
-// One group of a row: s, which is written, and z = s w.
+// One group of a row: s, and z = s w.
 template <typename T, Mode MODE, bool VEC>
-__device__ __forceinline__ Group values(const I8RowsArgs& a, long long row, const Columns& c,
-                                        bool write, Group* s) {
-    *s = load<VEC>(static_cast<const T*>(a.x) + row * a.ldx, c);
-    if (MODE == kStore) return *s;
+__device__ __forceinline__ Group sum_of(const I8RowsArgs& a, long long row, const Columns& c) {
+    Group s = load<VEC>(static_cast<const T*>(a.x) + row * a.ldx, c);
     if (MODE == kNormResidual) {
         const Group r = load<VEC>(static_cast<const T*>(a.r) + row * a.ldr, c);
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) s->v[i] = __fadd_rn(s->v[i], r.v[i]);
-        if (write && a.s) put<VEC>(static_cast<T*>(a.s) + row * a.lds, c, *s);
+        for (int i = 0; i < kLane; ++i) s.v[i] = __fadd_rn(s.v[i], r.v[i]);
     }
+    return s;
+}
+template <typename T, Mode MODE, bool VEC>
+__device__ __forceinline__ Group weighted(const I8RowsArgs& a, const Columns& c, const Group& s) {
+    if (MODE == kStore) return s;
     Group z = load<VEC>(static_cast<const T*>(a.w), c);
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) z.v[i] = __fmul_rn(s->v[i], z.v[i]);
+    for (int i = 0; i < kLane; ++i) z.v[i] = __fmul_rn(s.v[i], z.v[i]);
     return z;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void put_sum(const I8RowsArgs& a, long long row, const Columns& c,
+                                        const Group& s) {
+    if (a.s) put<VEC>(static_cast<T*>(a.s) + row * a.lds, c, s);
 }
 
 __device__ __forceinline__ unsigned top_of(const Group& z, unsigned top) {
@@ -200,33 +214,45 @@ struct Across {
     }
 };
 
-// G threads a row (a block of 256 takes eight rows where G is a warp); HELD:
-// the row fits the registers of its threads.
-template <typename T, Mode MODE, bool VEC, int G, bool HELD>
+// G threads a row (a block of 256 takes eight rows where G is a warp), which hold
+// E groups of columns each, or (E = 0) read the row twice.
+template <typename T, Mode MODE, bool VEC, int G, int E>
 __global__ void __launch_bounds__(G == 32 ? 256 : G) i8_rows_kernel(I8RowsArgs a) {
     __shared__ float sums[2][G / 32];
     __shared__ unsigned tops[2][G / 32];
+    constexpr bool HELD = E > 0;
+    constexpr int kHeld = HELD ? E : 1;
     const int thread = static_cast<int>(threadIdx.x) % G;
     const long long row = G == 32 ? blockIdx.x * 8LL + (threadIdx.x >> 5) : blockIdx.x;
     pdl_wait();
     pdl_trigger();
     if (G == 32 && row >= a.rows) return;
     const int groups = HELD ? kHeld : (a.cols - 1) / (G * kLane) + 1;
-    Group held[HELD ? kHeld : 1], s;
+    Group held[kHeld];
     float sum = 0.0f;
     unsigned top = 0u;
     if (HELD) {
+        // every load before the first store, which might be to where they read
+        Group s[kHeld];
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e)
+            s[e] = sum_of<T, MODE, VEC>(a, row, columns<VEC>(e, thread, G, a.cols));
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e)
+            held[HELD ? e : 0] = weighted<T, MODE, VEC>(a, columns<VEC>(e, thread, G, a.cols), s[e]);
 #pragma unroll
         for (int e = 0; e < kHeld; ++e) {
-            const Columns c = columns<VEC>(e, thread, G, a.cols);
-            held[e] = values<T, MODE, VEC>(a, row, c, true, &s);
-            top = top_of(held[e], top);
-            if (MODE != kStore) sum = squares_of(s, 1.0f, sum);
+            if (MODE == kNormResidual)
+                put_sum<T, VEC>(a, row, columns<VEC>(e, thread, G, a.cols), s[e]);
+            top = top_of(held[HELD ? e : 0], top);
+            if (MODE != kStore) sum = squares_of(s[e], 1.0f, sum);
         }
     } else {
         for (int e = 0; e < groups; ++e) {
             const Columns c = columns<VEC>(e, thread, G, a.cols);
-            top = top_of(values<T, MODE, VEC>(a, row, c, true, &s), top);
+            const Group s = sum_of<T, MODE, VEC>(a, row, c);
+            top = top_of(weighted<T, MODE, VEC>(a, c, s), top);
+            if (MODE == kNormResidual) put_sum<T, VEC>(a, row, c, s);
             if (MODE != kStore) sum = squares_of(s, 1.0f, sum);
         }
     }
@@ -238,8 +264,8 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G) i8_rows_kernel(I8RowsArgs a
         shrink = 8.271806125530277e-25f;
         sum = 0.0f;
         for (int e = 0; e < groups; ++e) {
-            values<T, MODE, VEC>(a, row, columns<VEC>(e, thread, G, a.cols), false, &s);
-            sum = squares_of(s, shrink, sum);
+            sum = squares_of(sum_of<T, MODE, VEC>(a, row, columns<VEC>(e, thread, G, a.cols)), shrink,
+                             sum);
         }
         unsigned none = 0u;
         Across<G>{sums[1], tops[1]}(sum, none);
@@ -253,7 +279,8 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G) i8_rows_kernel(I8RowsArgs a
         if (HELD)
             put_codes<VEC>(codes, c, held[HELD ? e : 0], inv, finite);
         else
-            put_codes<VEC>(codes, c, values<T, MODE, VEC>(a, row, c, false, &s), inv, finite);
+            put_codes<VEC>(codes, c, weighted<T, MODE, VEC>(a, c, sum_of<T, MODE, VEC>(a, row, c)),
+                           inv, finite);
     }
     if (thread == 0) {
         float scale = __fdiv_rn(most, 127.0f);
@@ -266,7 +293,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G) i8_rows_kernel(I8RowsArgs a
     }
 }
 
-template <typename T, Mode MODE, bool VEC, int G, bool HELD>
+template <typename T, Mode MODE, bool VEC, int G, int E>
 cudaError_t launch(const I8RowsArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
@@ -275,20 +302,38 @@ cudaError_t launch(const I8RowsArgs& a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, MODE, VEC, G, HELD>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, i8_rows_kernel<T, MODE, VEC, G, E>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Threads a row: as few as hold it, or, for too few rows to fill the GPU, as
-// many as have eight columns each.
+// Threads a row: for many rows as few as hold it, for too few to fill the GPU as
+// many as have eight columns each.  The float32 norm with its residual, which
+// has most values under way, takes twice as many (8192 x 8192 122 us against
+// 129, 4096 x 1000 10.5 against 14.7; the store of 50000 x 1000 51 against 36).
 template <typename T, Mode MODE, bool VEC>
 cudaError_t choose(const I8RowsArgs& a, cudaStream_t stream, int sm_count) {
-    const int each = a.rows <= 2 * sm_count ? kLane : kLane * kHeld;
-    if (a.cols <= 32 * each) return launch<T, MODE, VEC, 32, true>(a, stream);
-    if (a.cols <= 128 * each) return launch<T, MODE, VEC, 128, true>(a, stream);
-    if (a.cols <= 256 * each) return launch<T, MODE, VEC, 256, true>(a, stream);
-    if (a.cols <= 512 * kLane * kHeld) return launch<T, MODE, VEC, 512, true>(a, stream);
-    return launch<T, MODE, VEC, 512, false>(a, stream);
+    if (a.rows <= 2 * sm_count) {
+        if (a.cols <= 32 * kLane) return launch<T, MODE, VEC, 32, 1>(a, stream);
+        if (a.cols <= 128 * kLane) return launch<T, MODE, VEC, 128, 1>(a, stream);
+        if (a.cols <= 512 * kLane) return launch<T, MODE, VEC, 512, 1>(a, stream);
+        if (a.cols <= 1024 * kLane) return launch<T, MODE, VEC, 1024, 1>(a, stream);
+    }
+    if constexpr (MODE == kNormResidual && sizeof(T) == 4) {
+        if (a.cols > 64 * kLane && a.cols <= 128 * kLane)
+            return launch<T, MODE, VEC, 128, 1>(a, stream);
+        if (a.cols > 256 * kLane && a.cols <= 512 * kLane)
+            return launch<T, MODE, VEC, 256, 2>(a, stream);
+        if (a.cols > 512 * kLane && a.cols <= 1024 * kLane)
+            return launch<T, MODE, VEC, 512, 2>(a, stream);
+    }
+    if (a.cols <= 32 * kLane) return launch<T, MODE, VEC, 32, 1>(a, stream);
+    if (a.cols <= 64 * kLane) return launch<T, MODE, VEC, 32, 2>(a, stream);
+    if (a.cols <= 128 * kLane) return launch<T, MODE, VEC, 32, 4>(a, stream);
+    if (a.cols <= 256 * kLane) return launch<T, MODE, VEC, 128, 2>(a, stream);
+    if (a.cols <= 512 * kLane) return launch<T, MODE, VEC, 128, 4>(a, stream);
+    if (a.cols <= 1024 * kLane) return launch<T, MODE, VEC, 256, 4>(a, stream);
+    if (a.cols <= 2048 * kLane) return launch<T, MODE, VEC, 512, 4>(a, stream);
+    return launch<T, MODE, VEC, 512, 0>(a, stream);
 }
 
 // Whether rows can be moved 16 bytes at a time.
@@ -299,7 +344,7 @@ bool aligned(const void* p, long long ld, int rows, int elem) {
 template <typename T, Mode MODE>
 cudaError_t by_alignment(const I8RowsArgs& a, cudaStream_t stream, int sm_count) {
     const int elem = static_cast<int>(sizeof(T));
-    const bool vec = aligned(a.x, a.ldx, a.rows, elem) && aligned(a.r, a.ldr, a.rows, elem) &&
+    const bool vec = a.cols % kLane == 0 && aligned(a.x, a.ldx, a.rows, elem) && aligned(a.r, a.ldr, a.rows, elem) &&
                      aligned(a.s, a.lds, a.rows, elem) && aligned(a.w, 0, 1, elem);
     return vec ? choose<T, MODE, true>(a, stream, sm_count)
                : choose<T, MODE, false>(a, stream, sm_count);
