@@ -3,8 +3,10 @@
 // as in the GEMM entry points; nothing here exits the process.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "arguments.h"
 #include "gemm_f32.h"
@@ -47,36 +49,90 @@ int map_codes(CUtensorMap* map, const gemm_f32_i8* q, int k, int rows) {
                            rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How a product is shared out.
-I8Share share_out(int T, int N, int K, bool gated, int algo, int splits, int sm_count, bool* pair) {
+// The tensor-core kernel's times in microseconds, fitted to 2700 calls back to
+// back with each form forced (T 9 .. 4096, N 256 .. 16384, K 512 .. 8192, weights
+// from DRAM; within 3 to 7 % of them): a launch, a stage of 128 columns of K and
+// its part for each of a CTA's tokens, a tile and its part a token, joining
+// splits and each of them.  Below these, what the weights take from DRAM.
+struct I8Times {
+    float launch, stage, stage_token, tile, tile_token, split, each_split;
+};
+constexpr I8Times kI8Pair = {4.3f, 0.41f, 0.0018f, 0.68f, 0.019f, 0.0f, 0.0f};
+constexpr I8Times kI8Wide = {3.5f, 0.45f, 0.0001f, 0.0f, 0.0145f, 2.3f, 0.97f};
+constexpr I8Times kI8Narrow = {3.15f, 0.27f, 0.0004f, 0.5f, 0.016f, 2.2f, 0.35f};
+constexpr float kI8WeightsUsPerMb = 0.19f;
+// The same for the kernel for a few tokens, in groups of eight (24 x 8192 x 8192
+// 20.4 us, by single CTAs in two splits 19.0; 9 tokens 16.3 and 19.0).
+constexpr float kI8StreamLaunch = 2.0f;
+constexpr float kI8StreamUsPerMb[kI8StreamTokens / 8] = {0.175f, 0.215f, 0.26f, 0.32f};
+constexpr int kI8MostSplits = 16;    // that the library chooses
+constexpr int kI8NarrowTokens = 64;  // of a CTA, from which on its form is the wide one
+constexpr int kI8Counters = kWorkspaceCounterBytes / 4;
+
+int div_up(int a, int b) { return (a - 1) / b + 1; }
+int to_16(int a) { return (a + 15) & ~15; }
+// the fewest tokens a tile, of at most `most`, that make as few tiles
+int even_share(int T, int most) { return to_16(div_up(T, div_up(T, most))); }
+
+struct I8Choice {
+    I8Share share;
+    bool pair;
+    float us;
+};
+
+// One way to share a product out, if it is faster than the best so far.
+void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits, int sm_count,
+              I8Choice* best) {
+    const I8Tile t = i8_tile(pair);
+    const I8Times& time = pair ? kI8Pair : tokens > kI8NarrowTokens ? kI8Wide : kI8Narrow;
     I8Share s = {};
-    const auto tiles = [&](bool p, int tokens) {
-        const I8Tile t = i8_tile(p);
-        s.tokens = tokens;
-        s.tiles_c = (N - 1) / (gated ? t.channels / 2 : t.channels) + 1;
-        s.tiles_t = (T - 1) / (p ? 2 * tokens : tokens) + 1;
-        s.stages = (K - 1) / t.k + 1;
-        s.splits = 1;
-        return static_cast<long long>(s.tiles_c) * s.tiles_t;
+    s.tokens = tokens;
+    s.tiles_c = div_up(N, gated ? t.channels / 2 : t.channels);
+    s.tiles_t = div_up(T, pair ? 2 * tokens : tokens);
+    s.stages = div_up(K, t.k);
+    s.splits = std::min(splits, s.stages);
+    const long long tiles = static_cast<long long>(s.tiles_c) * s.tiles_t;
+    if (tiles > kI8Counters) s.splits = 1;
+    // requested splits: no more than keep the workspace within bounds
+    while (s.splits > 1 && tiles * s.splits > 16LL * sm_count) --s.splits;
+    const long long rounds = (tiles * s.splits - 1) / (pair ? sm_count / 2 : sm_count) + 1;
+    const float loop = rounds * (div_up(s.stages, s.splits) * (time.stage + time.stage_token * tokens) +
+                                 time.tile + time.tile_token * tokens);
+    const float weights = kI8WeightsUsPerMb * 1e-6f * N * K * (gated ? 2 : 1);
+    const float us = time.launch + std::max(loop, weights) +
+                     (s.splits > 1 ? time.split + time.each_split * s.splits : 0.0f);
+    if (us < best->us) *best = {s, pair, us};
+}
+
+// How a product is shared out: a few tile widths of each form, whole or split so
+// that a round's units fill the SMs, whichever should be fastest.
+I8Choice share_out(int T, int N, int K, bool gated, int algo, int splits, int sm_count) {
+    I8Choice best = {};
+    best.us = std::numeric_limits<float>::max();
+    const auto single = [&](int tokens) {
+        const I8Tile t = i8_tile(false);
+        const long long tiles = static_cast<long long>(div_up(N, gated ? t.channels / 2 : t.channels)) *
+                                div_up(T, tokens);
+        if (splits > 0) return consider(T, N, K, gated, false, tokens, splits, sm_count, &best);
+        const int most = std::min<long long>(std::min(div_up(K, t.k) / 2, kI8MostSplits),
+                                             sm_count / tiles);
+        consider(T, N, K, gated, false, tokens, 1, sm_count, &best);
+        if (most > 1) consider(T, N, K, gated, false, tokens, most, sm_count, &best);
+        if (most > 2) consider(T, N, K, gated, false, tokens, (most + 1) / 2, sm_count, &best);
     };
-    *pair = algo == GEMM_F32_ALGO_I8_PAIR;
-    if (algo == GEMM_F32_ALGO_AUTO) *pair = tiles(true, 128) >= sm_count / 4;
-    if (*pair) {
-        int w = 128;
-        while (w > 16 && T <= w) w -= 16;
-        tiles(true, w);
-        return s;
+    if (algo != GEMM_F32_ALGO_I8_SINGLE) {
+        const int tokens = to_16(div_up(even_share(T, 256), 2));
+        consider(T, N, K, gated, true, tokens, 1, sm_count, &best);
+        if (tokens > 64) consider(T, N, K, gated, true, 64, 1, sm_count, &best);
     }
-    int w = 128;
-    while (w > 16 && w - 16 >= T) w -= 16;
-    while (w > 32 && 2 * tiles(false, w) <= sm_count) w = (w / 2 + 15) / 16 * 16;
-    const long long n = tiles(false, w);
-    long long most = n * 8 <= kWorkspaceCounterBytes / 4 * 8 && n <= 1024 ? sm_count / n : 1;
-    if (splits > 0) most = n <= 1024 ? splits : 1;
-    else if (most > s.stages / 4) most = s.stages / 4;
-    if (most > s.stages) most = s.stages;
-    s.splits = most < 1 ? 1 : static_cast<int>(most);
-    return s;
+    if (algo != GEMM_F32_ALGO_I8_PAIR) {
+        const int tokens = even_share(T, kI8NarrowTokens);
+        if (T > kI8NarrowTokens) single(even_share(T, 128));
+        single(tokens);
+        if (tokens > 32) single(32);
+        if (tokens > 16) single(16);
+    }
+    return best;
 }
 
 // Both products: y = a b^T, or with c the gated product of b and c.
@@ -95,6 +151,8 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     }
     const int T = a->rows, N = b->rows, K = a->cols;
     if (T == 0 || N == 0) return GEMM_F32_SUCCESS;
+    // more tiles than an index holds: no memory does either
+    if (1.0 * T * N > 1e12) return GEMM_F32_ERR_INVALID_VALUE;
     I8_TRY(check_matrix(Y, T, N, ldy, elem_of(type)));
     if (K > 0) {
         I8_TRY(check_arrays(a));
@@ -111,15 +169,23 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     if (K == 0)
         return status(launch_zero_rows(Y, ldy * elem_of(type), T,
                                        static_cast<long long>(N) * elem_of(type), stream));
-    if (algo == GEMM_F32_ALGO_I8_STREAM || (algo == GEMM_F32_ALGO_AUTO && T <= kI8StreamTokens)) {
-        if (T > kI8StreamTokens) return GEMM_F32_ERR_INVALID_VALUE;
+    if (algo == GEMM_F32_ALGO_I8_STREAM && T > kI8StreamTokens) return GEMM_F32_ERR_INVALID_VALUE;
+    I8Choice how = {};
+    bool stream_form = algo == GEMM_F32_ALGO_I8_STREAM || (algo == GEMM_F32_ALGO_AUTO && T <= 8);
+    if (!stream_form) {
+        how = share_out(T, N, K, c != nullptr, algo, splits, s.sm_count);
+        if (algo == GEMM_F32_ALGO_AUTO && T <= kI8StreamTokens)
+            stream_form = kI8StreamLaunch + kI8StreamUsPerMb[(T - 1) / 8] * 1e-6f * N * K * (c ? 2 : 1) <
+                          how.us;
+    }
+    if (stream_form) {
         const I8StreamArgs p = {in_of(a), in_of(b), c ? in_of(c) : I8In{}, Y, ldy, T, N, K, type,
                                 c ? act : -1};
         return status(launch_i8_stream(p, stream, s.dev, s.sm_count));
     }
-    bool pair;
+    const bool pair = how.pair;
     I8TmemArgs k = {};
-    k.share = share_out(T, N, K, c != nullptr, algo, splits, s.sm_count, &pair);
+    k.share = how.share;
     unsigned char* ws = nullptr;
     if (k.share.splits > 1)
         I8_TRY(call_workspace(s, stream, kWorkspaceCounterBytes + i8_parts_bytes(k.share), &ws));
