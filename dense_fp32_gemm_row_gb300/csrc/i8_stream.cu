@@ -3,12 +3,15 @@
 //   acc[t][n] = sum_k a[t][k] b[n][k],  y = acc sa[t] sb[n]
 // and the gated product of two of them, h = act(g) u.
 //
-// Arithmetic as in the kernel for many tokens (i8_tmem.cu): codes become fp16
-// numbers, sums of up to 1024 products are exact in the fp32 accumulators of
-// the tensor core and are added up in 32-bit integers.  Here they stay in
-// registers from the load to the warp's own 16 x 8 x 16 MMAs (A the weights of 16
-// channels, B eight tokens): the weights pass through nothing else, and there
-// is no pipeline to fill.
+// Codes stay in registers from the load to the warp's own MMAs (A the weights of
+// 16 channels, B eight tokens): the weights pass through nothing else, and there
+// is no pipeline to fill.  Up to eight tokens take the integer MMA, whose sums are
+// exact by themselves.  On this part it runs at half the rate of the fp16 one, to
+// which codes have first to be converted, but that leaves it fast enough there
+// (8192 x 8192: 8 tokens 14.1 us against 15.3 through fp16, but 16 21.4 against
+// 16.4, 24 30.6 against 20.4).  More tokens take the fp16 MMA as the kernel for
+// many does (i8_tmem.cu): sums of up to 1024 products are exact in its fp32
+// accumulators, and are then added up in 32-bit integers.
 //
 // A block takes 16 or 32 channels (gated: 16 of both weights) and all of K, its
 // warps every W-th 64 columns each.  A lane copies 16 consecutive codes of its
@@ -17,6 +20,10 @@
 // their sums meet.  That the codes' order along K is not that of the MMA's
 // fragments makes no difference, as it is the same in both operands.  Codes
 // beyond K's end are masked in the tokens alone.
+//
+// Bounded by HBM and by a launch's 3 to 4 us: a token through 16384 x 16384 45.7
+// us, 5.9 TB/s, 8192 x 8192 13.4, 4096 x 4096 5.4.  From 17 tokens on by the MMAs:
+// 24 x 8192 x 8192 20.4 us, 3.6 for each group of eight.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -294,10 +301,13 @@ cudaError_t configure(int dev, int* regs) {
     return cudaSuccess;
 }
 
-// Warps a block: as many as make 24 an SM, if the blocks that an SM gets of them
-// find room in it side by side.  Each then asks for its whole share of the SM's
-// shared memory: a block more, on an SM that was done sooner with the kernel
-// before, would take it longer than the others.
+// Warps a block: four, or as many more as make 24 an SM, if the blocks that an SM
+// gets of them find room in it side by side.  (Of a token through 8192 x 8192
+// four, 13.4 us, eight 14.0; 4096 x 4096 eight 5.4, sixteen 5.9, four 6.5; 16384 x
+// 16384 four 45.7, two 49.0.)  Each block then asks for its whole share of the
+// SM's shared memory: a block more, on an SM that was done sooner with the kernel
+// before, would take it longer than the others (gated 8192 x 2048 8.4 us against
+// 9.8, 14336 x 4096 12.0 against 14.5).
 template <int NT, int CG, int ACT>
 cudaError_t launch(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_count) {
     using S = Stream<NT, CG, ACT>;
@@ -311,14 +321,15 @@ cudaError_t launch(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_c
         return w * S::WARP_BYTES <= share && per * w * 32 * ((regs + 7) & ~7) <= 65536;
     };
     int warps = S::WARPS;
-    while (warps > 2 && (!room(warps) || steps < 2 * warps ||
-                         static_cast<long long>(blocks) * warps > 24LL * sm_count))
+    while (warps > 2 &&
+           (!room(warps) || steps < 2 * warps ||
+            (warps > 4 && static_cast<long long>(blocks) * warps > 24LL * sm_count)))
         warps /= 2;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = std::max(warps * S::WARP_BYTES, share);
+    cfg.dynamicSmemBytes = per > 1 ? std::max(warps * S::WARP_BYTES, share) : warps * S::WARP_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

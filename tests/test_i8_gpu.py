@@ -548,11 +548,73 @@ def test_threads_at_once():
     assert all(same(m, w) for ms, w in zip(made, want) for m in ms)
 
 
+def test_host_faults():
+    """A workspace or a descriptor that cannot be had: reported, nothing written, and gone after."""
+    torch = t()
+    rng = np.random.default_rng(3)
+    qa, a, _ = operand(rng, 40, 4096)
+    qb, b, _ = operand(rng, 200, 4096)
+    want = sums_of(a, b).astype(np.int64)
+    y, _ = output(40, 200, "int32")
+    for algo, splits, kind, status in (("single", 16, g.INJECT_WORKSPACE, g.ERR_WORKSPACE),
+                                       ("single", 16, g.INJECT_DESCRIPTOR, g.ERR_DESCRIPTOR),
+                                       ("pair", 0, g.INJECT_DESCRIPTOR, g.ERR_DESCRIPTOR)):
+        g.gemm_f32_release()  # the next split needs its workspace again
+        y.fill_(55)
+        g.gemm_f32_inject_host_fault(kind)
+        try:
+            with pytest.raises(g.GemmError) as e:
+                g.i8_matmul(qa, qb, out=y, algo=algo, splits=splits)
+        finally:
+            g.gemm_f32_inject_host_fault(g.INJECT_NONE)
+        assert e.value.status == status
+        torch.cuda.synchronize()
+        assert bool((y == 55).all())
+        g.i8_matmul(qa, qb, out=y, algo=algo, splits=splits)
+        quiet()
+        assert np.array_equal(down(y), want)
+
+
+def test_weights_side_by_side():
+    """Gate and up as the row halves of one matrix, tokens as rows of a larger one."""
+    torch = t()
+    rng = np.random.default_rng(6)
+    for T in (3, 70):
+        qa, a, sa = operand(rng, T + 9, 200)
+        qw, w, sw = operand(rng, 2 * 150, 200)
+        part = g.I8(qa.codes[4:T + 4], qa.scales[4:T + 4], 200)
+        gate, upper = (g.I8(qw.codes[i:i + 150], qw.scales[i:i + 150], 200) for i in (0, 150))
+        own = [g.i8_empty(m.rows, 200) for m in (part, gate, upper)]
+        for m, o in zip((part, gate, upper), own):
+            o.codes[:, :200].copy_(m.codes[:, :200])
+            o.scales.copy_(m.scales)
+        assert torch.equal(g.i8_gated(part, gate, upper), g.i8_gated(*own))
+        assert np.array_equal(down(g.i8_matmul(part, upper, dtype=torch.int32)),
+                              sums_of(a[4:T + 4], w[150:]).astype(np.int64))
+
+
 def test_results_do_not_change_from_run_to_run():
     for T in (1, 24, 300):
         b = Block(T, 1024, 2048, "float32")
         first = b()
         assert all(same(b(), first) for _ in range(5))
+
+
+def test_many_calls_back_to_back():
+    """Forms after one another without a wait between, as kernels that start early meet."""
+    torch = t()
+    rng = np.random.default_rng(12)
+    cases = []
+    for T, N, K, algo, splits in ((1, 700, 900, "auto", 0), (300, 520, 1100, "pair", 0), (20, 640, 4096, "auto", 0),
+                                  (50, 300, 2048, "single", 7), (600, 200, 300, "single", 1), (9, 64, 9000, "single", 2),
+                                  (130, 1000, 700, "auto", 0), (257, 129, 2600, "pair", 0)):
+        (qa, a, _), (qb, b, _) = operand(rng, T, K), operand(rng, N, K)
+        cases.append((qa, qb, algo, splits, torch.from_numpy(sums_of(a, b)).to(torch.int32).cuda()))
+    made = [g.i8_matmul(qa, qb, dtype=torch.int32, algo=algo, splits=splits)
+            for _ in range(40) for qa, qb, algo, splits, _ in cases]
+    quiet()
+    for i, y in enumerate(made):
+        assert torch.equal(y, cases[i % len(cases)][4])
 
 
 def test_offsets_beyond_32_bits():
