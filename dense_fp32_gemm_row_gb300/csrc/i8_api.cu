@@ -67,6 +67,7 @@ constexpr float kI8StreamLaunch = 2.0f;
 constexpr float kI8StreamUsPerMb[kI8StreamTokens / 8] = {0.175f, 0.215f, 0.26f, 0.32f};
 constexpr int kI8MostSplits = 16;    // that the library chooses
 constexpr int kI8NarrowTokens = 64;  // of a CTA, from which on its form is the wide one
+constexpr int kI8MostRows = 2147483647 - 1023;
 constexpr int kI8Counters = kWorkspaceCounterBytes / 4;
 
 int div_up(int a, int b) { return (a - 1) / b + 1; }
@@ -151,8 +152,9 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     }
     const int T = a->rows, N = b->rows, K = a->cols;
     if (T == 0 || N == 0) return GEMM_F32_SUCCESS;
-    // more tiles than an index holds: no memory does either
-    if (1.0 * T * N > 1e12) return GEMM_F32_ERR_INVALID_VALUE;
+    // more tiles than an index holds (no memory does either), or rows whose
+    // number plus a tile's it does not
+    if (1.0 * T * N > 1e12 || T > kI8MostRows || N > kI8MostRows) return GEMM_F32_ERR_INVALID_VALUE;
     I8_TRY(check_matrix(Y, T, N, ldy, elem_of(type)));
     if (K > 0) {
         I8_TRY(check_arrays(a));

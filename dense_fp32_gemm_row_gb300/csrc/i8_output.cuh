@@ -36,8 +36,9 @@ __device__ __forceinline__ float i8_value(float sum, float token, float channel)
     return __fmul_rn(__fmul_rn(sum, token), channel);
 }
 
-// act(z) with the quotient of silu to 2 ulp (act_value rounds it correctly):
-// the sums' own roundings are as large.
+// act(z) with the quotient of silu to 2 ulp (act_value rounds it correctly): the
+// sums' own roundings are as large.  Where e^-z is beyond 2^126, z below -87.3,
+// the quotient is 0 instead of up to 1e-36.
 template <int ACT>
 __device__ __forceinline__ float i8_act(float z) {
     return ACT == kActSilu ? __fdividef(z, 1.0f + expf(-z)) : act_value<kActGelu>(z);

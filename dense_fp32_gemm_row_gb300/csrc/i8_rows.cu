@@ -12,8 +12,11 @@
 // is not finite gets codes 0 and scale NaN.
 //
 // Bounded by HBM: a row is read once, held in registers (up to 32 columns a
-// thread) between the two steps, and written once.  Rows beyond 16384 columns are read
-// a second time, from L2.
+// thread) between the two steps, and written once.  Rows beyond 16384 columns are
+// read a second time, from L2.  8192 x 8192, of the measured copy rate: store
+// float32 47 us, 105 %, bf16 30.5, 97 %; norm with residual float32 122, 105 %,
+// bf16 75.7, 91 %.  Rows off 16-byte boundaries: norm 8191 x 8191 float32 129 us, 99
+// %, but bf16, two bytes at a time, 168, 41 %.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -259,8 +262,8 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G) i8_rows_kernel(I8RowsArgs a
     Across<G>{sums[0], tops[0]}(sum, top);
     const bool finite = top < kInfinity;
     float shrink = 1.0f;
-    if (MODE != kStore && finite && __float_as_uint(sum) >= kInfinity) {
-        // squares beyond fp32, of a row that is not: again at 2^-80
+    if (MODE != kStore && finite && __float_as_uint(__fadd_rn(sum, a.eps)) >= kInfinity) {
+        // squares (or they and eps) beyond fp32, of a row that is not: again at 2^-80
         shrink = 8.271806125530277e-25f;
         sum = 0.0f;
         for (int e = 0; e < groups; ++e) {

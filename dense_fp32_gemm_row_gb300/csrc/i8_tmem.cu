@@ -19,19 +19,22 @@
 // Conversion is 5 instructions for four codes: a code with its sign bit flipped
 // in the low mantissa bits of 1024 is 1152 + code, less 1152.
 //
-// Two forms.  A cluster of two CTAs computes 256 channels x up to 256 tokens
+// Three forms.  A cluster of two CTAs computes 256 channels x up to 256 tokens
 // with cta_group::2 MMAs, each CTA holding 128 channels in its tensor memory
-// and half of the tokens in its shared memory: per 16 columns of K an SM's
-// tensor core works 128 cycles, and its shared memory moves 4 KB for the
-// weights (copy in, read out) and 12 KB for the tokens (copy in, read out, fp16
-// in, MMA).  Or one CTA computes 128 x up to 128, with two accumulators in
-// turn, its tiles split over K for few tokens.  The gated form has 16 channels of
-// the gate and the same of up in the lanes of a warp, which exchange sums.
+// and half of the tokens in its shared memory.  Per 16 columns of K an SM's
+// tensor core works 128 cycles, and its shared memory moves 4 KB for the weights
+// (copy in, read out) and 12 KB for the tokens (copy in, read out, fp16 in,
+// MMA): all that it can.  (Both operands in shared memory would take one and a
+// half times as long, one CTA with 128 x 256 tiles 1.7 times.)  Or one CTA
+// computes 128 x up to 128, or up to 64 with more stages and a third warpgroup
+// to convert them, with two accumulators in turn; their tiles may be split over
+// K.  The gated form has 16 channels of the gate and the same of up in the lanes
+// of a warp, which exchange sums by a shuffle.
 //
-// 640 threads per CTA (of narrow tiles 768), registers rebalanced at start (launched
-// at 96 each, 80):
-//   warp 0       one lane: TMA loads of a 128-column stage of raw codes;
-//   warp 1       tensor-memory allocation; one lane (of a pair: the leader's)
+// 640 threads per CTA, 768 for narrow tiles, registers rebalanced at start
+// (launched at 96 or 80 each):
+//   warp 0       TMA loads of a 128-column stage of raw codes;
+//   warp 1       tensor-memory allocation; in a single CTA or the pair's leader it
 //                issues the MMAs and commits;
 //   warps 1-2 of a pair's peer  relay: one lane each tells the leader, in turn,
 //                that the peer's operands of a stage are written;
@@ -44,6 +47,18 @@
 // last, by a counter a tile, adds the others' to its own: nothing waits, and
 // the order makes no difference to integers.
 // Waits are bounded and wind down as in the GEMM kernels.
+//
+// What set the speed, 8192 x 8192 x 8192, pairs: chunks' sums converted to
+// integers one by one, at 16 a clock and SM, 928 us; added as floats 852; token
+// scales loaded past the outputs' stores, which may alias them, 790; stages of
+// 128 columns instead of 64, as each role's turn takes some 300 cycles whatever
+// a stage holds, 663; the MMA and copy warps whole instead of one lane each, so
+// that descriptors are the warp's and not a lane's, 634 to 640: 1720 TFLOP/s, 90
+// % of the rate of the library's bf16 product.  Of that the waits for the
+// accumulator at the end of each chunk take 65 (without them 573, 1920 TFLOP/s)
+// and the peer's relay 23.  One token to a few hundred are bound by the start
+// (3.2 us to the first MMA's end and the store of the last tile), then by 0.28 us
+// a stage: 1000 x 1023 x 1025 7.2 us, 64 x 8192 x 8192 20.
 #include <cstdint>
 
 #include "device_sync.cuh"
@@ -148,6 +163,14 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 // Offset of a 16-byte chunk: rows of 128 bytes, 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(uint32_t row, uint32_t chunk) {
     return row * 128u + ((chunk ^ (row & 7u)) << 4);
+}
+
+// A scale, which the kernel before may have written: not before the wait for that
+// kernel, and apart from that whenever it suits, past stores that it cannot alias.
+__device__ __forceinline__ float load_scale(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
 }
 
 // One unit of work: a split of a tile.
@@ -654,8 +677,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             float token[C::EPI_COLS / 32];
 #pragma unroll
             for (int i = 0; i < C::EPI_COLS / 32; ++i) {
-                const int t = w.t0 + col0 + 32 * i + lane;
-                token[i] = t < p.T ? __ldg(p.as + t) : 0.0f;
+                // (of tokens that there are not the last one's, which nothing uses)
+                token[i] = load_scale(p.as + min(w.t0 + col0 + 32 * i + lane, p.T - 1));
             }
             for (int c0 = 0; ok && c0 < w.nkb; c0 += kChunk, ++g) {
                 const int b = g % C::ACCS;
@@ -737,10 +760,10 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             const int n = w.c0 + n_lane;
             const bool mine = ok && n < p.N;
-            const float channel = n < p.N ? __ldg(p.bs + n) : 0.0f;
+            const float channel = load_scale(p.bs + min(n, p.N - 1));
             const int t_first = w.t0 + col0;
             if (GATED) {
-                const float channel_up = n < p.N ? __ldg(p.cs + n) : 0.0f;
+                const float channel_up = load_scale(p.cs + min(n, p.N - 1));
                 const int left = mine ? min(count, p.T - t_first) : 0;
                 const long long at = static_cast<long long>(t_first) * p.ldy + n;
                 if (p.type == kI8Bfloat16)

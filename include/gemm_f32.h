@@ -531,12 +531,13 @@ int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr,
  * gemm_f32_i8_matmul -- Y = a b^T, T x N from T x K tokens a and N x K weights
  * b: the integer sums of code products, exact whatever the sizes, times a's and
  * then b's scale, each product rounded to fp32, as floats or bf16 by type; or
- * with GEMM_F32_TYPE_I32 the sums themselves (the scales are then not read).
+ * with GEMM_F32_TYPE_I32 the sums themselves (the scales then play no part).
  * K is at most GEMM_F32_I8_MAX_COLS, so that no sum overflows 32 bits; K = 0
- * writes zeros.  A token's outputs do not depend on the other tokens of the
- * call, bit for bit.  algo: GEMM_F32_ALGO_AUTO, or this entry point's and
- * gated's own: the tensor-core kernel with tiles of CTA pairs (I8_PAIR) or of
- * single CTAs (I8_SINGLE), over how many ranges of K `splits` (at most
+ * writes zeros.  T and N are at most 2^31 - 1024, and T N at most 10^12.  A
+ * token's outputs do not depend on the other tokens of the call, bit for bit.
+ * algo: GEMM_F32_ALGO_AUTO, or this entry point's and gated's own: the
+ * tensor-core kernel with tiles of CTA pairs (I8_PAIR) or of single CTAs
+ * (I8_SINGLE), over how many ranges of K `splits` (at most
  * GEMM_F32_MAX_SPLITS; 0: the library chooses) splits the latter, or the kernel
  * for a few tokens (I8_STREAM: a->rows at most GEMM_F32_I8_STREAM_ROWS).
  * Results do not depend on either.

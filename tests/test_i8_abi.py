@@ -102,6 +102,20 @@ def test_bad_arguments_are_invalid():
         assert g.gemm_f32_i8_gated(0, a, b, b, Z, 0, 7) == want
 
 
+def test_the_most_rows():
+    most, far = 2 ** 31 - 1024, 0x1000_0000_0000  # far from an output of 4 TB
+    for rows, other, want in ((most, 4, None), (most + 1, 4, BAD), (2 ** 31 - 1, 4, BAD),
+                              (10 ** 6, 10 ** 6, None), (10 ** 6, 10 ** 6 + 1, BAD)):
+        a = i8(rows=rows, cols=16, ld=16)
+        b = i8(rows=other, cols=16, codes=W, scales=W + 0x10_0000_0000, ld=16)
+        if want is None:
+            want = accepted()
+        assert g.gemm_f32_i8_matmul(a, b, far, 0, other) == want
+        assert g.gemm_f32_i8_matmul(b, a, far, 0, rows) == want
+        assert g.gemm_f32_i8_gated(0, a, b, b, far, 1, other) == want
+        assert g.gemm_f32_i8_gated(0, b, a, a, far, 1, rows) == want
+
+
 def test_outputs_apart_from_inputs_and_each_other():
     want = accepted()
     q, w = i8(), i8(rows=7, codes=W, scales=W + 0x10000)

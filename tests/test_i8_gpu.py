@@ -168,6 +168,17 @@ def test_least_eps():
     assert abs(down(q.scales)[0] / scales[0] - 1) < _i8.norm_bound(64)
 
 
+def test_squares_and_eps_beyond_float32_together():
+    x = np.full((3, 40), 1.8e19, np.float32)  # squares of 3.24e38, a mean below the largest float
+    x[1, 1:] = 0
+    x[2] = 1
+    w = np.linspace(0.5, 2, 40, dtype=np.float32)
+    codes, scales, _ = _i8.norm(x, None, w, float(np.float32(3e38)))
+    q, _ = g.i8_norm(up(x), up(w[None])[0], eps=3e38)
+    assert np.array_equal(down(q.codes)[:, :40], codes)
+    assert (np.abs(down(q.scales) / scales - 1) < _i8.norm_bound(40)).all()
+
+
 # ---- products -------------------------------------------------------------------------------------
 
 
@@ -293,6 +304,32 @@ def test_sums_of_the_largest_products(T, N, K, a, b):
     want = a * b * (K - 1) + 1
     assert bool((g.i8_matmul(q, w, dtype=torch.int32) == want).all())
     quiet()
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gates_of_all_sizes(T, act):
+    """One code a row, so that gate and up are what their scales say."""
+    torch = t()
+    g64 = np.array([0.0, -0.0, 1e-30, -1e-30, 0.5, -0.5, 5, -5, 13, -13, 20, -20, 60, -60, 86, -86, 87.5, -87.5, 88,
+                    -88, 89, -89, 100, -100, 1e4, -1e4, 1e30, -1e30])
+    N = len(g64)
+    one = g.i8_empty(T, 1)
+    one.codes.zero_()
+    one.codes[:, 0] = 1
+    one.scales.fill_(1.0)
+    w, v = g.i8_empty(N, 1), g.i8_empty(N, 1)
+    for m, s in ((w, g64), (v, np.full(N, 3.0))):
+        m.codes.zero_()
+        m.codes[:, 0] = 1
+        m.scales.copy_(torch.from_numpy(s.astype(np.float32)))
+    gate = np.tile(g64.astype(np.float32).astype(np.float64), (T, 1))
+    got = down(g.i8_gated(one, w, v, act=act)).astype(np.float64)
+    quiet()
+    want = _q8.act(gate, act)[0] * 3.0
+    assert np.all(np.abs(got - want) <= _i8.gated_bound(gate, np.full((T, N), 3.0), act))
+    w.scales.fill_(float("inf"))
+    assert bool((g.i8_gated(one, w, v, act=act) == float("inf")).all())
 
 
 def test_scales_that_are_no_numbers():
