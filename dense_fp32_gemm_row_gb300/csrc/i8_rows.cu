@@ -15,8 +15,8 @@
 // thread) between the two steps, and written once.  Rows beyond 16384 columns are
 // read a second time, from L2.  8192 x 8192, of the measured copy rate: store
 // float32 47 us, 105 %, bf16 30.5, 97 %; norm with residual float32 122, 105 %,
-// bf16 75.7, 91 %.  Rows off 16-byte boundaries: norm 8191 x 8191 float32 129 us, 99
-// %, but bf16, two bytes at a time, 168, 41 %.
+// bf16 75.3, 92 %.  Rows off 16-byte boundaries: norm 8191 x 8191 float32 128 us,
+// 100 %, bf16, two bytes at a time, 95, 73 %, store 40, 75 %.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -62,8 +62,28 @@ __device__ __forceinline__ Columns columns(int group, int thread, int threads, i
     return c;
 }
 
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+// An element if it is there, or 0, without a branch.  (Written in C++ a bf16 load
+// waited for the one before: norm 8191 x 8191 167 us, like this 95; store 62 and
+// 40.)  The asm keeps its place behind the wait for the kernel before, but not
+// among this one's stores, which never go to an operand.
+__device__ __forceinline__ float load_if(const float* p, bool there) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
+        "@q ld.global.f32 %0, [%1];\n\t}"
+        : "=f"(v)
+        : "l"(p), "r"(static_cast<int>(there)));
+    return v;
+}
+__device__ __forceinline__ float load_if(const __nv_bfloat16* p, bool there) {
+    unsigned short v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.s32 q, %2, 0;\n\tmov.u16 %0, 0;\n\t"
+        "@q ld.global.u16 %0, [%1];\n\t}"
+        : "=h"(v)
+        : "l"(p), "r"(static_cast<int>(there)));
+    return __uint_as_float(static_cast<unsigned>(v) << 16);
+}
 
 template <bool VEC>
 __device__ __forceinline__ Group load(const float* p, const Columns& c) {
@@ -78,7 +98,7 @@ __device__ __forceinline__ Group load(const float* p, const Columns& c) {
         g.v[4] = hi.x, g.v[5] = hi.y, g.v[6] = hi.z, g.v[7] = hi.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) g.v[i] = i < c.n ? p[c.col + i * c.stride] : 0.0f;
+        for (int i = 0; i < kLane; ++i) g.v[i] = load_if(p + c.col + i * c.stride, i < c.n);
     }
     return g;
 }
@@ -96,7 +116,7 @@ __device__ __forceinline__ Group load(const __nv_bfloat16* p, const Columns& c) 
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) g.v[i] = i < c.n ? widen(p[c.col + i * c.stride]) : 0.0f;
+        for (int i = 0; i < kLane; ++i) g.v[i] = load_if(p + c.col + i * c.stride, i < c.n);
     }
     return g;
 }
@@ -312,7 +332,8 @@ cudaError_t launch(const I8RowsArgs& a, cudaStream_t stream) {
 // Threads a row: for many rows as few as hold it, for too few to fill the GPU as
 // many as have eight columns each.  The float32 norm with its residual, which
 // has most values under way, takes twice as many (8192 x 8192 122 us against
-// 129, 4096 x 1000 10.5 against 14.7; the store of 50000 x 1000 51 against 36).
+// 129, 4096 x 1000 10.5 against 14.7; the store of 50000 x 1000 51 against 36),
+// but not for long rows off 16-byte boundaries (8191 x 8191 128 against 146).
 template <typename T, Mode MODE, bool VEC>
 cudaError_t choose(const I8RowsArgs& a, cudaStream_t stream, int sm_count) {
     if (a.rows <= 2 * sm_count) {
@@ -324,9 +345,9 @@ cudaError_t choose(const I8RowsArgs& a, cudaStream_t stream, int sm_count) {
     if constexpr (MODE == kNormResidual && sizeof(T) == 4) {
         if (a.cols > 64 * kLane && a.cols <= 128 * kLane)
             return launch<T, MODE, VEC, 128, 1>(a, stream);
-        if (a.cols > 256 * kLane && a.cols <= 512 * kLane)
+        if (VEC && a.cols > 256 * kLane && a.cols <= 512 * kLane)
             return launch<T, MODE, VEC, 256, 2>(a, stream);
-        if (a.cols > 512 * kLane && a.cols <= 1024 * kLane)
+        if (VEC && a.cols > 512 * kLane && a.cols <= 1024 * kLane)
             return launch<T, MODE, VEC, 512, 2>(a, stream);
     }
     if (a.cols <= 32 * kLane) return launch<T, MODE, VEC, 32, 1>(a, stream);
