@@ -21,9 +21,9 @@
 // fragments makes no difference, as it is the same in both operands.  Codes
 // beyond K's end are masked in the tokens alone.
 //
-// Bounded by HBM and by a launch's 3 to 4 us: a token through 16384 x 16384 45.7
-// us, 5.9 TB/s, 8192 x 8192 13.4, 4096 x 4096 5.4.  From 17 tokens on by the MMAs:
-// 24 x 8192 x 8192 20.4 us, 3.6 for each group of eight.
+// Bounded by HBM and by a launch's 3 to 4 us: a token through 16384 x 16384 45.4
+// us, 5.9 TB/s, 8192 x 8192 13.3, 4096 x 4096 5.2.  From 17 tokens on by the MMAs:
+// 24 x 8192 x 8192 20 us, 3.6 for each group of eight.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -41,9 +41,14 @@ using namespace gemm_f32_dev;
 
 constexpr int kExactSteps = 1024 / 64;  // steps of 64 columns of K
 constexpr int kAhead = 4;             // steps of a warp under way
+constexpr int kEarlyBytes = 512;      // of a channel, prefetched before the kernel's turn
 constexpr int kSharedBytes = 233472;  // shared memory of an SM
 constexpr int kBlockBytes = 232448;   // of a block, at most
 
+// To L2; from a 16-byte boundary, a multiple of 16 bytes.
+__device__ __forceinline__ void prefetch_codes(const signed char* from, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
 // 16 bytes to shared memory, or zeros, behind the thread's back.
 __device__ __forceinline__ void copy_weights(uint32_t to, const signed char* from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
@@ -186,6 +191,16 @@ i8_stream_kernel(I8StreamArgs p) {
     int total[SETS * NT * 4] = {};  // of fp32 sums
 
     const int stride = 64 * warps;
+    // While the kernel before ends, the first codes of each channel are sent for,
+    // to L2, which reads no value (a token, 4096 x 4096 5.4 to 5.2 us, 8192 x 8192
+    // 13.7 to 13.3; 2048 bytes instead of 512 made gated 8192 x 2048 9.5 of 8.0).
+    if (threadIdx.x < 16 * SETS) {
+        const int s = threadIdx.x / 16;
+        const I8In& m = S::GATED && s >= CG ? p.c : p.b;
+        const int n = n0 + 16 * (s % CG) + threadIdx.x % 16;
+        const int bytes = min(p.K, kEarlyBytes) & ~15;
+        if (n < p.N && bytes) prefetch_codes(m.codes + n * m.ld, bytes);
+    }
     pdl_wait();
     pdl_trigger();
     int ahead = first;  // the next step to copy: this lane's column
