@@ -320,7 +320,8 @@ cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t s, int sm_count);
 // (i8_tmem.cu): CTA pairs with tiles of 256 channels
 // x 2 `tokens`, or single CTAs with 128 x `tokens` (gated: half the channels),
 // `tokens` a multiple of 16, at most 128; single CTAs' tiles in `splits` ranges
-// of the stages of K.
+// of the stages of K, if they are few enough for their counters.
+constexpr int kI8CountersPerTile = 8;
 struct I8Share {
     int tiles_c, tiles_t;  // tiles of channels and of tokens
     int tokens;            // of a CTA
@@ -345,7 +346,7 @@ struct I8TmemArgs {
     int T, N, type;
     I8Share share;
     int* parts;     // the splits' sums
-    int* counters;  // one a tile, zero between calls
+    int* counters;  // kI8CountersPerTile a tile, zero between calls
     unsigned* fault;
     long long timeout_ns;
 };

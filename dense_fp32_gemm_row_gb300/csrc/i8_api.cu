@@ -68,7 +68,7 @@ constexpr float kI8StreamUsPerMb[kI8StreamTokens / 8] = {0.175f, 0.215f, 0.26f, 
 constexpr int kI8MostSplits = 16;    // that the library chooses
 constexpr int kI8NarrowTokens = 64;  // of a CTA, from which on its form is the wide one
 constexpr int kI8MostRows = 2147483647 - 1023;
-constexpr int kI8Counters = kWorkspaceCounterBytes / 4;
+constexpr int kI8MostSplitTiles = kWorkspaceCounterBytes / 4 / kI8CountersPerTile;
 
 int div_up(int a, int b) { return (a - 1) / b + 1; }
 int to_16(int a) { return (a + 15) & ~15; }
@@ -93,7 +93,7 @@ void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits
     s.stages = div_up(K, t.k);
     s.splits = std::min(splits, s.stages);
     const long long tiles = static_cast<long long>(s.tiles_c) * s.tiles_t;
-    if (tiles > kI8Counters) s.splits = 1;
+    if (tiles > kI8MostSplitTiles) s.splits = 1;
     // requested splits: no more than keep the workspace within bounds
     while (s.splits > 1 && tiles * s.splits > 16LL * sm_count) --s.splits;
     const long long rounds = (tiles * s.splits - 1) / (pair ? sm_count / 2 : sm_count) + 1;

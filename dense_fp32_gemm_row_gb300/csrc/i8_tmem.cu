@@ -43,9 +43,9 @@
 //   the last 8   per chunk add the accumulator to the sums in their registers
 //                (warp e of them: lanes 32 (e % 4) .., half e / 4 of the columns);
 //                at the end of a unit scale and store them.
-// Splits of a tile write their sums to the workspace, and the one that comes
-// last, by a counter a tile, adds the others' to its own: nothing waits, and
-// the order makes no difference to integers.
+// Splits of a tile write their sums to the workspace, and of each warp's part the
+// split that comes last, by a counter, adds the others' to its own: nothing
+// waits, and the order makes no difference to integers.
 // Waits are bounded and wind down as in the GEMM kernels.
 //
 // What set the speed, 8192 x 8192 x 8192, pairs: chunks' sums converted to
@@ -135,6 +135,7 @@ struct I8Cfg {
     static_assert(STAGES % GROUPS == 0 && (!PAIR || RELAYS == GROUPS) && RAW < STAGES,
                   "phases of the barriers");
     static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+    static_assert(EPI_WARPS == kI8CountersPerTile, "counters of a split tile");
 };
 
 __device__ __forceinline__ uint4 lds_u32x4(uint32_t addr) {
@@ -156,9 +157,23 @@ __device__ __forceinline__ void sts_u32x8(uint32_t addr, const uint32_t (&h)[8])
     sts_u32x4(addr, h[0], h[1], h[2], h[3]);
     sts_u32x4(addr ^ 16u, h[4], h[5], h[6], h[7]);
 }
-// Barrier `id` of the CTA's named ones, for `threads` of its threads.
-__device__ __forceinline__ void named_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// Whether the warp is the last of `all` that call this with one counter, which is
+// then 0 again: what the others wrote before their calls is visible to it.
+__device__ __forceinline__ bool last_to_come(int* counter, int all) {
+    int before = 0;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        asm volatile("atom.relaxed.gpu.global.add.s32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(counter)
+                     : "memory");
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        if (before == all - 1)
+            asm volatile("st.relaxed.gpu.global.s32 [%0], 0;" ::"l"(counter) : "memory");
+    }
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, before, 0) == all - 1;
 }
 
 // Offset of a 16-byte chunk: rows of 128 bytes, 128-byte swizzle.
@@ -342,7 +357,6 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t drain = acce + 8 * C::ACCS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + C::NBARS * 8);
     const uint32_t abort_flag = smem_addr(tmem_slot + 1);
-    const uint32_t last_flag = smem_addr(tmem_slot + 2);
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
@@ -666,8 +680,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         __syncwarp();
     } else {
         // ------------------------------ epilogue ---------------------------------------
-        // All eight warps walk through the same units whatever happens, so that the
-        // named barriers always find them.
+        // Every warp walks through all units whatever happens, so that the counters of
+        // split tiles come round to 0.
         regs_inc<C::REGS_EPI>();
         const int e = warp - C::EPI_WARP0;
         const int q = warp & 3;                  // lanes 32 q .. 32 q + 31
@@ -720,6 +734,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (c0 + kChunk < w.nkb) keep_exact<C::EPI_COLS>(acc, whole);
             }
             if (!PAIR && share.splits > 1) {
+                if (count <= 0) continue;
                 if (!whole)
 #pragma unroll
                     for (int j = 0; j < C::EPI_COLS; ++j)
@@ -734,16 +749,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     for (int i = 0; i < 16; ++i)
                         __stcg(mine + (j + i) * C::LANES, __float_as_int(acc[j + i]));
                 }
-                __threadfence();
-                named_sync(1, 32 * C::EPI_WARPS);
-                if (e == 0 && lane == 0) {
-                    const bool last = atomicAdd(p.counters + w.tile, 1) == share.splits - 1;
-                    if (last) atomicExch(p.counters + w.tile, 0);  // for the next call
-                    st_shared_volatile(last_flag, last ? 1u : 0u);
-                    __threadfence();
-                }
-                named_sync(1, 32 * C::EPI_WARPS);
-                if (!ld_shared_volatile(last_flag)) continue;
+                if (!last_to_come(p.counters + C::EPI_WARPS * w.tile + e, share.splits)) continue;
                 const int* const all = p.parts + w.tile * share.splits * slot + col0 * C::LANES +
                                        32 * q + lane;
                 for (int s = 0; s < share.splits; ++s) {
