@@ -327,12 +327,17 @@ struct I8Share {
     int tokens;            // of a CTA
     int stages;            // of one tile
     int splits;            // not more than stages; 1 for pairs
+    int clusters;          // whether the splits of a tile are a cluster
 };
 struct I8Tile {
     int channels, tokens, k;  // of a tile; of a CTA, at most; of a pipeline stage
 };
 I8Tile i8_tile(bool pair);
-// bytes of the splits' sums
+// Whether a cluster's first CTA has room for the others' sums, and how many
+// clusters run at once on device `dev`, the current one (the ABI's mutex is held).
+bool i8_joins_in_clusters(int splits, int tokens);
+int i8_most_clusters(int splits, int dev);
+// bytes of the splits' sums in the workspace
 size_t i8_parts_bytes(const I8Share& s);
 // Codes as {K, rows} bytes with 128-byte swizzle: a's box 128 x tokens, b's (and
 // c's, gated) 128 x 128, or gated 128 x 64.

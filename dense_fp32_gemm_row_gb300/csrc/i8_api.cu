@@ -82,8 +82,8 @@ struct I8Choice {
 };
 
 // One way to share a product out, if it is faster than the best so far.
-void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits, int sm_count,
-              I8Choice* best) {
+void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits, int dev,
+              int sm_count, I8Choice* best) {
     const I8Tile t = i8_tile(pair);
     const I8Times& time = pair ? kI8Pair : tokens > kI8NarrowTokens ? kI8Wide : kI8Narrow;
     I8Share s = {};
@@ -96,6 +96,8 @@ void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits
     if (tiles > kI8MostSplitTiles) s.splits = 1;
     // requested splits: no more than keep the workspace within bounds
     while (s.splits > 1 && tiles * s.splits > 16LL * sm_count) --s.splits;
+    if (s.splits > 1 && i8_joins_in_clusters(s.splits, tokens) && tiles <= i8_most_clusters(s.splits, dev))
+        s.clusters = 1;
     const long long rounds = (tiles * s.splits - 1) / (pair ? sm_count / 2 : sm_count) + 1;
     const float loop = rounds * (div_up(s.stages, s.splits) * (time.stage + time.stage_token * tokens) +
                                  time.tile + time.tile_token * tokens);
@@ -107,24 +109,25 @@ void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits
 
 // How a product is shared out: a few tile widths of each form, whole or split so
 // that a round's units fill the SMs, whichever should be fastest.
-I8Choice share_out(int T, int N, int K, bool gated, int algo, int splits, int sm_count) {
+I8Choice share_out(int T, int N, int K, bool gated, int algo, int splits, int dev,
+                   int sm_count) {
     I8Choice best = {};
     best.us = std::numeric_limits<float>::max();
     const auto single = [&](int tokens) {
         const I8Tile t = i8_tile(false);
         const long long tiles = static_cast<long long>(div_up(N, gated ? t.channels / 2 : t.channels)) *
                                 div_up(T, tokens);
-        if (splits > 0) return consider(T, N, K, gated, false, tokens, splits, sm_count, &best);
+        if (splits > 0) return consider(T, N, K, gated, false, tokens, splits, dev, sm_count, &best);
         const int most = std::min<long long>(std::min(div_up(K, t.k) / 2, kI8MostSplits),
                                              sm_count / tiles);
-        consider(T, N, K, gated, false, tokens, 1, sm_count, &best);
-        if (most > 1) consider(T, N, K, gated, false, tokens, most, sm_count, &best);
-        if (most > 2) consider(T, N, K, gated, false, tokens, (most + 1) / 2, sm_count, &best);
+        consider(T, N, K, gated, false, tokens, 1, dev, sm_count, &best);
+        if (most > 1) consider(T, N, K, gated, false, tokens, most, dev, sm_count, &best);
+        if (most > 2) consider(T, N, K, gated, false, tokens, (most + 1) / 2, dev, sm_count, &best);
     };
     if (algo != GEMM_F32_ALGO_I8_SINGLE) {
         const int tokens = to_16(div_up(even_share(T, 256), 2));
-        consider(T, N, K, gated, true, tokens, 1, sm_count, &best);
-        if (tokens > 64) consider(T, N, K, gated, true, 64, 1, sm_count, &best);
+        consider(T, N, K, gated, true, tokens, 1, dev, sm_count, &best);
+        if (tokens > 64) consider(T, N, K, gated, true, 64, 1, dev, sm_count, &best);
     }
     if (algo != GEMM_F32_ALGO_I8_PAIR) {
         const int tokens = even_share(T, kI8NarrowTokens);
@@ -175,7 +178,7 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     I8Choice how = {};
     bool stream_form = algo == GEMM_F32_ALGO_I8_STREAM || (algo == GEMM_F32_ALGO_AUTO && T <= 8);
     if (!stream_form) {
-        how = share_out(T, N, K, c != nullptr, algo, splits, s.sm_count);
+        how = share_out(T, N, K, c != nullptr, algo, splits, s.dev, s.sm_count);
         if (algo == GEMM_F32_ALGO_AUTO && T <= kI8StreamTokens)
             stream_form = kI8StreamLaunch + kI8StreamUsPerMb[(T - 1) / 8] * 1e-6f * N * K * (c ? 2 : 1) <
                           how.us;
@@ -189,7 +192,7 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     I8TmemArgs k = {};
     k.share = how.share;
     unsigned char* ws = nullptr;
-    if (k.share.splits > 1)
+    if (k.share.splits > 1 && !k.share.clusters)
         I8_TRY(call_workspace(s, stream, kWorkspaceCounterBytes + i8_parts_bytes(k.share), &ws));
     const I8Tile tile = i8_tile(pair);
     const int rows = c ? 64 : 128;

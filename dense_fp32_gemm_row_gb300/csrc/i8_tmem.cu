@@ -43,9 +43,11 @@
 //   the last 8   per chunk add the accumulator to the sums in their registers
 //                (warp e of them: lanes 32 (e % 4) .., half e / 4 of the columns);
 //                at the end of a unit scale and store them.
-// Splits of a tile write their sums to the workspace, and of each warp's part the
-// split that comes last, by a counter, adds the others' to its own: nothing
-// waits, and the order makes no difference to integers.
+// Splits of a tile are a cluster where the clusters fit the GPU at once: they send
+// their sums to its first CTA, when its stages are free, and that adds them up.
+// Otherwise they write them to the workspace, and of each warp's part the split
+// that comes last, by a counter, adds the others' to its own.  The order makes no
+// difference to integers.
 // Waits are bounded and wind down as in the GEMM kernels.
 //
 // What set the speed, 8192 x 8192 x 8192, pairs: chunks' sums converted to
@@ -114,8 +116,8 @@ struct I8Cfg {
     // divide, have a barrier for each group.
     static constexpr int FULLS = GROUPS * RAW;
     // full, free (raw stages), empty, ready (per operand stage), acc_full and
-    // acc_empty (per accumulator), drain
-    static constexpr int NBARS = FULLS + RAW + 2 * STAGES + 2 * ACCS + 1;
+    // acc_empty (per accumulator), drain, room, joined (per warp of the epilogue)
+    static constexpr int NBARS = FULLS + RAW + 2 * STAGES + 2 * ACCS + 2 + EPI_WARPS;
     static constexpr int SMEM_BYTES = BAR_OFF + NBARS * 8 + 16 + 1024;
     static constexpr int EPI_WARP0 = 4 + 4 * GROUPS;
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
@@ -174,6 +176,15 @@ __device__ __forceinline__ bool last_to_come(int* counter, int all) {
     }
     __syncwarp();
     return __shfl_sync(0xffffffffu, before, 0) == all - 1;
+}
+
+// Sums to another CTA of the cluster, counted by its barrier there.
+__device__ __forceinline__ void send_f32x4(uint32_t to, uint32_t bar, const float* v) {
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+        "[%5];" ::"r"(to),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(bar)
+        : "memory");
 }
 
 // Offset of a 16-byte chunk: rows of 128 bytes, 128-byte swizzle.
@@ -355,12 +366,15 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t accf = ready0 + 8 * STAGES;      // own, multicast commit
     const uint32_t acce = accf + 8 * C::ACCS;       // leader: 8 warps a CTA
     const uint32_t drain = acce + 8 * C::ACCS;
+    const uint32_t room0 = drain + 8;               // a cluster's others: its first has room
+    const uint32_t joined0 = room0 + 8;             // its first: the others' sums, a warp's
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + C::NBARS * 8);
     const uint32_t abort_flag = smem_addr(tmem_slot + 1);
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const bool cluster = PAIR || p.share.clusters;
     const int first = blockIdx.x / C::CTAS, step = gridDim.x / C::CTAS;
     const long long timeout_ns = p.timeout_ns;
     unsigned* const fault = p.fault;
@@ -382,6 +396,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             mbar_init(acce + 8 * a, C::CTAS * C::EPI_WARPS);
         }
         mbar_init(drain, 1);
+        mbar_init(room0, 1);
+        for (int e = 0; e < C::EPI_WARPS; ++e) mbar_init(joined0 + 8 * e, 1);
         st_shared_volatile(abort_flag, 0u);
         fence_barrier_init();
     }
@@ -395,7 +411,7 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
     }
     tc_fence_before();
-    if (PAIR)
+    if (cluster)
         cluster_sync();
     else
         __syncthreads();
@@ -740,30 +756,75 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     for (int j = 0; j < C::EPI_COLS; ++j)
                         acc[j] = __int_as_float(__float2int_rn(acc[j]));
                 whole = true;
-                const long long slot = static_cast<long long>(share.tokens) * C::LANES;
-                int* const mine = p.parts + u * slot + col0 * C::LANES + 32 * q + lane;
+                // a warp's lanes' sums of four columns lie side by side
+                const uint32_t slice = static_cast<uint32_t>(col0 * C::LANES + q * count * 32) * 4u +
+                                       16u * static_cast<uint32_t>(lane);
+                const uint32_t part = static_cast<uint32_t>(share.tokens) * (4u * C::LANES);
+                if (share.clusters) {
+                    const int split = u - w.tile * share.splits;
+                    if (!ok) continue;
+                    if (split == 0) {
+                        // every MMA of this CTA is done, and so are its copies: its
+                        // stages are free
+                        if (e == 0 && lane > 0 && lane < share.splits)
+                            mbar_arrive_remote(map_to_cta(room0, lane));
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(joined0 + 8 * e,
+                                                  (share.splits - 1) * count * (4 * 32));
+                        const bool got = role_wait<true>(joined0 + 8 * e, 0, timeout_ns, fault,
+                                                         kFaultAccumBarrier, abort_flag);
+                        ok = __all_sync(0xffffffffu, got);
+                        for (int s = 0; ok && s < share.splits - 1; ++s) {
 #pragma unroll
-                for (int j = 0; j < C::EPI_COLS; j += 16) {
-                    if (j >= count) break;
+                            for (int j = 0; j < C::EPI_COLS; j += 4) {
+                                if (j % 16 == 0 && j >= count) break;
+                                const uint4 more = lds_u32x4(sbase + s * part + slice + j * 128);
+                                const uint32_t m[4] = {more.x, more.y, more.z, more.w};
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        __stcg(mine + (j + i) * C::LANES, __float_as_int(acc[j + i]));
-                }
-                if (!last_to_come(p.counters + C::EPI_WARPS * w.tile + e, share.splits)) continue;
-                const int* const all = p.parts + w.tile * share.splits * slot + col0 * C::LANES +
-                                       32 * q + lane;
-                for (int s = 0; s < share.splits; ++s) {
-                    if (w.tile * share.splits + s == u) continue;
+                                for (int i = 0; i < 4; ++i)
+                                    acc[j + i] = __int_as_float(__float_as_int(acc[j + i]) +
+                                                                static_cast<int>(m[i]));
+                            }
+                        }
+                    } else {
+                        const bool got = role_wait<true>(room0, 0, timeout_ns, fault,
+                                                         kFaultAccumBarrier, abort_flag);
+                        if (!__all_sync(0xffffffffu, got)) continue;
+                        const uint32_t to = map_to_cta(sbase + (split - 1) * part + slice, 0);
+                        const uint32_t bar = map_to_cta(joined0 + 8 * e, 0);
+#pragma unroll
+                        for (int j = 0; j < C::EPI_COLS; j += 4) {
+                            if (j % 16 == 0 && j >= count) break;
+                            send_f32x4(to + j * 128, bar, acc + j);
+                        }
+                        continue;
+                    }
+                } else {
+                    const long long slot = static_cast<long long>(share.tokens) * C::LANES;
+                    int* const mine = p.parts + u * slot + col0 * C::LANES + 32 * q + lane;
 #pragma unroll
                     for (int j = 0; j < C::EPI_COLS; j += 16) {
                         if (j >= count) break;
-                        int more[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            more[i] = __ldcg(all + s * slot + (j + i) * C::LANES);
+                            __stcg(mine + (j + i) * C::LANES, __float_as_int(acc[j + i]));
+                    }
+                    if (!last_to_come(p.counters + C::EPI_WARPS * w.tile + e, share.splits)) continue;
+                    const int* const all = p.parts + w.tile * share.splits * slot + col0 * C::LANES +
+                                           32 * q + lane;
+                    for (int s = 0; s < share.splits; ++s) {
+                        if (w.tile * share.splits + s == u) continue;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[j + i] = __int_as_float(__float_as_int(acc[j + i]) + more[i]);
+                        for (int j = 0; j < C::EPI_COLS; j += 16) {
+                            if (j >= count) break;
+                            int more[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                more[i] = __ldcg(all + s * slot + (j + i) * C::LANES);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                acc[j + i] = __int_as_float(__float_as_int(acc[j + i]) + more[i]);
+                        }
                     }
                 }
             }
@@ -813,10 +874,10 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         __syncwarp();
     }
 
-    // neither CTA of a pair may leave while the other can still reach its shared
-    // or tensor memory
+    // no CTA of a cluster may leave while another can still reach its shared or
+    // tensor memory
     tc_fence_before();
-    if (PAIR)
+    if (cluster)
         cluster_sync();
     else
         __syncthreads();
@@ -863,7 +924,7 @@ cudaError_t launch(const I8TmemMaps& maps, const I8TmemArgs& a, cudaStream_t s, 
     cudaLaunchAttribute attr[2];
     attr[0] = pdl_attribute();
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = C::PAIR ? 2 : a.share.splits;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(C::CTAS * static_cast<int>(units < slots ? units : slots));
@@ -871,7 +932,7 @@ cudaError_t launch(const I8TmemMaps& maps, const I8TmemArgs& a, cudaStream_t s, 
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = C::PAIR ? 2 : 1;
+    cfg.numAttrs = C::PAIR || a.share.clusters ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, i8_tmem_kernel<FORM, ACT>, maps.a, maps.b, maps.c, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -886,13 +947,50 @@ cudaError_t launch_form(const I8TmemMaps& maps, const I8TmemArgs& a, bool pair, 
 
 }  // namespace
 
+bool i8_joins_in_clusters(int splits, int tokens) {
+    using W = I8Cfg<kWide>;
+    using N = I8Cfg<kNarrow>;
+    const int room = tokens <= N::TOK ? N::BAR_OFF : W::BAR_OFF;
+    return splits > 1 && splits <= 8 && (splits - 1) * tokens * (4 * W::LANES) <= room;
+}
+
+int i8_most_clusters(int splits, int dev) {
+    constexpr int kDevices = 64;
+    static int known[kDevices][9] = {};  // and 1
+    if (dev < 0 || dev >= kDevices || splits < 2 || splits > 8) return 0;
+    int& n = known[dev][splits];
+    if (!n) {
+        using C = I8Cfg<kNarrow>;
+        if (configure<kNarrow, kI8NoAct>(dev) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = splits;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(splits);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM_BYTES;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, i8_tmem_kernel<kNarrow, kI8NoAct>, &cfg) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            clusters = 0;
+        }
+        n = clusters + 1;
+    }
+    return n - 1;
+}
+
 I8Tile i8_tile(bool pair) {
     using P = I8Cfg<kPair>;
     return {pair ? 2 * P::LANES : P::LANES, P::TOK, P::KT};
 }
 
 size_t i8_parts_bytes(const I8Share& s) {
-    if (s.splits < 2) return 0;
+    if (s.splits < 2 || s.clusters) return 0;
     return static_cast<size_t>(s.tiles_c) * s.tiles_t * s.splits * s.tokens * I8Cfg<kWide>::LANES * 4;
 }
 
