@@ -372,6 +372,8 @@ struct I8StreamArgs {
     long long ldy;
     int T, N, K, type, act;
 };
+// Rows of weights that the busiest SM reads.
+int i8_stream_channels(int T, int N, bool gated, int sm_count);
 cudaError_t launch_i8_stream(const I8StreamArgs& p, cudaStream_t s, int dev, int sm_count);
 
 // ---- what the ABI files share (defined in gemm_f32_api.cu) --------------------

@@ -49,22 +49,25 @@ int map_codes(CUtensorMap* map, const gemm_f32_i8* q, int k, int rows) {
                            rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// The tensor-core kernel's times in microseconds, fitted to 2700 calls back to
-// back with each form forced (T 9 .. 4096, N 256 .. 16384, K 512 .. 8192, weights
-// from DRAM; within 3 to 7 % of them): a launch, a stage of 128 columns of K and
-// its part for each of a CTA's tokens, a tile and its part a token, joining
-// splits and each of them.  Below these, what the weights take from DRAM.
+// The tensor-core kernel's times in microseconds, fitted to 3600 calls back to
+// back with each form forced (T 9 .. 1024, N 256 .. 16384, K 512 .. 14336, weights
+// from DRAM; within 4 to 7 % of them on average): a launch, a stage of 128 columns
+// of K and its part for each of a CTA's tokens, a tile and its part a token,
+// joining splits in a cluster and each of them, and the same through the workspace.
+// Below these, what the weights take from DRAM.  Choices by them take 0.9 % longer
+// than the best of all forms, on average of 234 sizes.
 struct I8Times {
-    float launch, stage, stage_token, tile, tile_token, split, each_split;
+    float launch, stage, stage_token, tile, tile_token, join, each_join, split, each_split;
 };
-constexpr I8Times kI8Pair = {4.3f, 0.41f, 0.0018f, 0.68f, 0.019f, 0.0f, 0.0f};
-constexpr I8Times kI8Wide = {3.5f, 0.45f, 0.0001f, 0.0f, 0.0145f, 2.3f, 0.97f};
-constexpr I8Times kI8Narrow = {3.15f, 0.27f, 0.0004f, 0.5f, 0.016f, 2.2f, 0.35f};
+constexpr I8Times kI8Pair = {4.3f, 0.43f, 0.0016f, 0.5f, 0.0193f, 0.0f, 0.0f, 0.0f, 0.0f};
+constexpr I8Times kI8Wide = {3.3f, 0.445f, 0.0001f, 0.0f, 0.016f, 0.6f, 0.9f, 1.9f, 0.97f};
+constexpr I8Times kI8Narrow = {3.2f, 0.275f, 0.0002f, 0.27f, 0.0227f, 1.0f, 0.2f, 2.7f, 0.31f};
 constexpr float kI8WeightsUsPerMb = 0.19f;
-// The same for the kernel for a few tokens, in groups of eight (24 x 8192 x 8192
-// 20.4 us, by single CTAs in two splits 19.0; 9 tokens 16.3 and 19.0).
-constexpr float kI8StreamLaunch = 2.0f;
-constexpr float kI8StreamUsPerMb[kI8StreamTokens / 8] = {0.175f, 0.215f, 0.26f, 0.32f};
+// The same for the kernel for a few tokens: a launch, and a thousand codes of the
+// weights that the busiest SM reads, for 9 to 16, 24 and 32 tokens (24 x 8192 x 8192
+// 20.4 us, by single CTAs in two splits 16.8; 9 tokens 16.0 and 16.8).
+constexpr float kI8StreamLaunch = 3.3f;
+constexpr float kI8StreamUsPerK[kI8StreamTokens / 8 - 1] = {0.0245f, 0.0327f, 0.037f};
 constexpr int kI8MostSplits = 16;    // that the library chooses
 constexpr int kI8NarrowTokens = 64;  // of a CTA, from which on its form is the wide one
 constexpr int kI8MostRows = 2147483647 - 1023;
@@ -96,19 +99,23 @@ void consider(int T, int N, int K, bool gated, bool pair, int tokens, int splits
     if (tiles > kI8MostSplitTiles) s.splits = 1;
     // requested splits: no more than keep the workspace within bounds
     while (s.splits > 1 && tiles * s.splits > 16LL * sm_count) --s.splits;
-    if (s.splits > 1 && i8_joins_in_clusters(s.splits, tokens) && tiles <= i8_most_clusters(s.splits, dev))
+    if (s.splits > 1 && i8_joins_in_clusters(s.splits, tokens) &&
+        tiles <= i8_most_clusters(s.splits, dev))
         s.clusters = 1;
     const long long rounds = (tiles * s.splits - 1) / (pair ? sm_count / 2 : sm_count) + 1;
     const float loop = rounds * (div_up(s.stages, s.splits) * (time.stage + time.stage_token * tokens) +
                                  time.tile + time.tile_token * tokens);
     const float weights = kI8WeightsUsPerMb * 1e-6f * N * K * (gated ? 2 : 1);
-    const float us = time.launch + std::max(loop, weights) +
-                     (s.splits > 1 ? time.split + time.each_split * s.splits : 0.0f);
+    const float join = s.splits == 1 ? 0.0f
+                       : s.clusters  ? time.join + time.each_join * s.splits
+                                     : time.split + time.each_split * s.splits;
+    const float us = time.launch + std::max(loop, weights) + join;
     if (us < best->us) *best = {s, pair, us};
 }
 
 // How a product is shared out: a few tile widths of each form, whole or split so
-// that a round's units fill the SMs, whichever should be fastest.
+// that a round's units fill the SMs or half of them, or in as many clusters as run
+// at once, whichever should be fastest.
 I8Choice share_out(int T, int N, int K, bool gated, int algo, int splits, int dev,
                    int sm_count) {
     I8Choice best = {};
@@ -123,16 +130,23 @@ I8Choice share_out(int T, int N, int K, bool gated, int algo, int splits, int de
         consider(T, N, K, gated, false, tokens, 1, dev, sm_count, &best);
         if (most > 1) consider(T, N, K, gated, false, tokens, most, dev, sm_count, &best);
         if (most > 2) consider(T, N, K, gated, false, tokens, (most + 1) / 2, dev, sm_count, &best);
+        for (int n = std::min(most, 8); n > 1; --n)
+            if (i8_joins_in_clusters(n, tokens) && tiles <= i8_most_clusters(n, dev)) {
+                if (n != most) consider(T, N, K, gated, false, tokens, n, dev, sm_count, &best);
+                break;
+            }
     };
     if (algo != GEMM_F32_ALGO_I8_SINGLE) {
         const int tokens = to_16(div_up(even_share(T, 256), 2));
         consider(T, N, K, gated, true, tokens, 1, dev, sm_count, &best);
+        if (tokens > 96) consider(T, N, K, gated, true, 96, 1, dev, sm_count, &best);
         if (tokens > 64) consider(T, N, K, gated, true, 64, 1, dev, sm_count, &best);
     }
     if (algo != GEMM_F32_ALGO_I8_PAIR) {
         const int tokens = even_share(T, kI8NarrowTokens);
         if (T > kI8NarrowTokens) single(even_share(T, 128));
         single(tokens);
+        if (tokens > 48) single(48);
         if (tokens > 32) single(32);
         if (tokens > 16) single(16);
     }
@@ -179,9 +193,10 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     bool stream_form = algo == GEMM_F32_ALGO_I8_STREAM || (algo == GEMM_F32_ALGO_AUTO && T <= 8);
     if (!stream_form) {
         how = share_out(T, N, K, c != nullptr, algo, splits, s.dev, s.sm_count);
-        if (algo == GEMM_F32_ALGO_AUTO && T <= kI8StreamTokens)
-            stream_form = kI8StreamLaunch + kI8StreamUsPerMb[(T - 1) / 8] * 1e-6f * N * K * (c ? 2 : 1) <
-                          how.us;
+        if (algo == GEMM_F32_ALGO_AUTO && T <= kI8StreamTokens) {
+            const float codes = 1e-3f * K * i8_stream_channels(T, N, c != nullptr, s.sm_count);
+            stream_form = kI8StreamLaunch + kI8StreamUsPerK[(T - 9) / 8] * codes < how.us;
+        }
     }
     if (stream_form) {
         const I8StreamArgs p = {in_of(a), in_of(b), c ? in_of(c) : I8In{}, Y, ldy, T, N, K, type,

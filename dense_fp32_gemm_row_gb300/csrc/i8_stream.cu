@@ -353,12 +353,13 @@ cudaError_t launch(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_c
 }
 
 // 32 channels a block convert the tokens' codes half as often as 16, but are
-// half as many blocks: from about half a block an SM on (24 x 4096 x 4096 8.1 us
-// against 9.3, 24 x 1024 x 8192 11.1 against 8.0).
+// half as many blocks: from about half a block an SM on (24 x 4096 x 4096 8.0 us
+// against 9.1, 24 x 1024 x 8192 10.7 against 7.4).
+bool two_groups(int N, int sm_count) { return (N - 1) / 32 + 1 > sm_count / 2; }
 template <int NT, int ACT>
 cudaError_t by_channels(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_count) {
     constexpr int kTwo = ACT == kI8NoAct && NT > 1 ? 2 : 1;
-    if ((p.N - 1) / 32 + 1 <= sm_count / 2) return launch<NT, 1, ACT>(p, stream, dev, sm_count);
+    if (!two_groups(p.N, sm_count)) return launch<NT, 1, ACT>(p, stream, dev, sm_count);
     return launch<NT, kTwo, ACT>(p, stream, dev, sm_count);
 }
 
@@ -371,6 +372,12 @@ cudaError_t by_tokens(const I8StreamArgs& p, cudaStream_t stream, int dev, int s
 }
 
 }  // namespace
+
+int i8_stream_channels(int T, int N, bool gated, int sm_count) {
+    const int channels = T > 8 && !gated && two_groups(N, sm_count) ? 32 : 16;
+    const int blocks = (N - 1) / channels + 1;
+    return ((blocks - 1) / sm_count + 1) * channels * (gated ? 2 : 1);
+}
 
 cudaError_t launch_i8_stream(const I8StreamArgs& p, cudaStream_t stream, int dev,
                              int sm_count) {

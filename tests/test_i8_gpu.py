@@ -265,7 +265,7 @@ def test_gated(T, N, K, act, name):
     assert np.all(np.abs(down(y) - want) <= bound)
 
 
-@pytest.mark.parametrize("algo,splits", [("pair", 0), ("single", 1), ("single", 2), ("single", 5), ("single", 256), ("stream", 0)])
+@pytest.mark.parametrize("algo,splits", [("pair", 0), ("single", 1), ("single", 2), ("single", 3), ("single", 5), ("single", 8), ("single", 256), ("stream", 0)])
 @pytest.mark.parametrize("T,N,K", PRODUCTS[::3] + [(257, 129, 1024), (513, 1023, 1088), (129, 513, 8200)])
 def test_forced_forms(T, N, K, algo, splits):
     torch = t()
