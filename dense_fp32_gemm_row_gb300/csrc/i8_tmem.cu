@@ -60,7 +60,8 @@
 // accumulator at the end of each chunk take 65 (without them 573, 1920 TFLOP/s)
 // and the peer's relay 23.  One token to a few hundred are bound by the start
 // (3.2 us to the first MMA's end and the store of the last tile), then by 0.28 us
-// a stage: 1000 x 1023 x 1025 7.2 us, 64 x 8192 x 8192 20.
+// a stage or the weights' way from HBM: 1000 x 1023 x 1025 7.1 us, 64 x 8192 x 8192
+// 17.9 (with splits that meet in the workspace 19.0).
 #include <cstdint>
 
 #include "device_sync.cuh"
