@@ -978,7 +978,7 @@ int i8_most_clusters(int splits, int dev) {
         if (cudaOccupancyMaxActiveClusters(&clusters, i8_tmem_kernel<kNarrow, kI8NoAct>, &cfg) !=
             cudaSuccess) {
             cudaGetLastError();
-            clusters = 0;
+            return 0;
         }
         n = clusters + 1;
     }

@@ -1,5 +1,8 @@
 """The 8-bit integer layers on the GPU against their plain forms."""
 
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -530,6 +533,32 @@ def test_captured_and_replayed(T):
         want = b()
         quiet()
         assert same(made, want)
+
+
+FIRST = """
+import torch, dense_fp32_gemm_row_gb300 as g
+torch.manual_seed(0)
+q = [g.i8_store(torch.randn(r, 4096, device="cuda")) for r in (64, 4096, 4096)]
+one = g.i8_matmul(g.i8_store(torch.randn(1, 4096, device="cuda")), q[1])
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):
+    y = g.i8_matmul(q[0], q[1], dtype=torch.int32)
+    h = g.i8_gated(*q)
+graph.replay()
+torch.cuda.synchronize()
+g.check(g.gemm_f32_device_status(1), "device status")
+assert torch.equal(y.double(), q[0].codes.double() @ q[1].codes.double().t())
+assert torch.equal(y, g.i8_matmul(q[0], q[1], dtype=torch.int32)) and torch.equal(h, g.i8_gated(*q))
+print("captured")
+"""
+
+
+def test_the_first_split_product_is_a_captured_one():
+    made = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert made.returncode == 0 and "captured" in made.stdout, made.stderr[-2000:]
 
 
 def test_graphs_side_by_side():
