@@ -537,9 +537,10 @@ int gemm_f32_i8_norm(const void* X, long long ldx, const void* R, long long ldr,
  * token's outputs do not depend on the other tokens of the call, bit for bit.
  * algo: GEMM_F32_ALGO_AUTO, or this entry point's and gated's own: the
  * tensor-core kernel with tiles of CTA pairs (I8_PAIR) or of single CTAs
- * (I8_SINGLE), over how many ranges of K `splits` (at most
- * GEMM_F32_MAX_SPLITS; 0: the library chooses) splits the latter, or the kernel
- * for a few tokens (I8_STREAM: a->rows at most GEMM_F32_I8_STREAM_ROWS).
+ * (I8_SINGLE), `splits` being how many ranges of K the latter are split over
+ * (at most GEMM_F32_MAX_SPLITS; fewer where K or the workspace's bounds do not
+ * allow it; 0: the library chooses), or the kernel for a few tokens (I8_STREAM:
+ * a->rows at most GEMM_F32_I8_STREAM_ROWS).
  * Results do not depend on either.
  */
 #define GEMM_F32_ALGO_I8_PAIR    6
