@@ -18,8 +18,8 @@
 // rows, and four lanes 64, to slots of its own in shared memory, several steps
 // ahead, and reads them itself: no warp waits for another before the end, where
 // their sums meet.  That the codes' order along K is not that of the MMA's
-// fragments makes no difference, as it is the same in both operands.  Codes
-// beyond K's end are masked in the tokens alone.
+// fragments makes no difference, as it is the same in both operands.  A copy
+// ends with K and leaves zeros behind it.
 //
 // Bounded by HBM and by a launch's 3 to 4 us: a token through 16384 x 16384 45.4
 // us, 5.9 TB/s, 8192 x 8192 13.3, 4096 x 4096 5.2.  From 17 tokens on by the MMAs:
@@ -49,15 +49,13 @@ constexpr int kBlockBytes = 232448;   // of a block, at most
 __device__ __forceinline__ void prefetch_codes(const signed char* from, int bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
 }
-// 16 bytes to shared memory, or zeros, behind the thread's back.
-__device__ __forceinline__ void copy_weights(uint32_t to, const signed char* from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
-                 "r"(there ? 16 : 0)
+// Up to 16 bytes to shared memory, zeros behind them, behind the thread's back.
+__device__ __forceinline__ void copy_weights(uint32_t to, const signed char* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void copy_tokens(uint32_t to, const signed char* from, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
-                 "r"(there ? 16 : 0)
+__device__ __forceinline__ void copy_tokens(uint32_t to, const signed char* from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
@@ -67,18 +65,6 @@ __device__ __forceinline__ void copies_commit() {
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// The first `left` of 16 codes, the others zero.
-__device__ __forceinline__ uint4 first_codes(uint4 v, int left) {
-    if (left >= 16) return v;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = left - 4 * i;
-        w[i] = n >= 4 ? w[i] : n <= 0 ? 0u : w[i] & ((1u << (8 * n)) - 1u);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Sums of fp16 products in fp32, and of integer products in integers.
@@ -205,16 +191,18 @@ i8_stream_kernel(I8StreamArgs p) {
     pdl_trigger();
     int ahead = first;  // the next step to copy: this lane's column
     const auto copy = [&](uint32_t slot) {
+        // the last row's memory may end with its last column
+        const int there = min(max(p.K - ahead, 0), 16);
 #pragma unroll
         for (int s = 0; s < SETS; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                copy_weights(slot + 512 * (2 * s + h), weights[s][h], ahead < p.K);
+                copy_weights(slot + 512 * (2 * s + h), weights[s][h], there);
                 weights[s][h] += stride;
             }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            copy_tokens(slot + 512 * (2 * SETS + i), tokens[i], ahead < p.K && 8 * i + g < p.T);
+            copy_tokens(slot + 512 * (2 * SETS + i), tokens[i], 8 * i + g < p.T ? there : 0);
             tokens[i] += stride;
         }
         ahead += stride;
@@ -226,15 +214,11 @@ i8_stream_kernel(I8StreamArgs p) {
     uint32_t slot = slots, last = slots + (kAhead - 1) * S::STEP_BYTES;
 
     int exact = 0;
-    for (int k = first; k - 16 * c < p.K; k += stride) {
+    for (int k = 64 * warp; k < p.K; k += stride) {
         copies_wait<kAhead - 2>();
         typename S::Step now;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            uint4 v = lds_u32x4(slot + 512 * (2 * SETS + i));
-            if (k + 16 > p.K) v = first_codes(v, p.K - k);
-            now.token(i, v);
-        }
+        for (int i = 0; i < NT; ++i) now.token(i, lds_u32x4(slot + 512 * (2 * SETS + i)));
 #pragma unroll
         for (int s = 0; s < SETS; ++s)
             now.add(acc[s], lds_u32x4(slot + 512 * (2 * s)), lds_u32x4(slot + 512 * (2 * s + 1)));
