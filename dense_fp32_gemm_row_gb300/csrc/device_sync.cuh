@@ -224,7 +224,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                  : "memory");
 }
 // The same arrival with the default (CTA-scope) release: for a hand-back
-// that orders no memory writes the waiter reads (e.g. a tensor-memory
+// that orders no accesses to memory, neither writes that the waiter reads nor
+// reads and writes of what it will overwrite (e.g. of a tensor-memory
 // accumulator whose loads have completed).  A release at cluster scope
 // costs ~650 ns per arrival on this part.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {

@@ -566,8 +566,18 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         mma_commit_pair(drain);
                     else
                         mma_commit(drain);
-                    mbar_wait(drain, 0, ok ? timeout_ns : timeout_ns / 8 + 1000, fault, kFaultDrain);
+                    if (!mbar_wait(drain, 0, ok ? timeout_ns : timeout_ns / 8 + 1000, fault,
+                                   kFaultDrain))
+                        ok = false;
                 }
+                ok = __all_sync(0xffffffffu, ok);
+                // The first CTA of a cluster: its MMAs are done, and with them (its operands
+                // were ready) its copies and their conversion: its stages are free.  The
+                // release is at cluster scope, as the others' sums overwrite what this CTA's
+                // threads wrote and read there; it takes long, but not on the epilogue's path.
+                if (!PAIR && share.clusters && ok && lane > 0 && lane < share.splits &&
+                    cluster_ctarank() == 0)
+                    mbar_arrive_cluster(map_to_cta(room0, lane));
                 __syncwarp();
             } else if (PAIR && lane == 0) {
                 relay(0);
@@ -765,10 +775,6 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     const int split = u - w.tile * share.splits;
                     if (!ok) continue;
                     if (split == 0) {
-                        // every MMA of this CTA is done, and so are its copies: its
-                        // stages are free
-                        if (e == 0 && lane > 0 && lane < share.splits)
-                            mbar_arrive_remote(map_to_cta(room0, lane));
                         if (lane == 0)
                             mbar_arrive_expect_tx(joined0 + 8 * e,
                                                   (share.splits - 1) * count * (4 * 32));
