@@ -26,6 +26,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <optional>
@@ -675,12 +676,13 @@ PyObject* i8_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!count(n, 4)) return nullptr;
     if (!any_matrix(args[0], &x) || !THPVariable_CheckExact(args[1]) || !PyFloat_CheckExact(args[3]))
         Py_RETURN_NONE;
-    const float eps = static_cast<float>(PyFloat_AS_DOUBLE(args[3]));
+    const double given = PyFloat_AS_DOUBLE(args[3]);
+    const float eps = static_cast<float>(given);
     const at::Tensor& w = THPVariable_Unpack(args[1]);
     if (w.layout() != at::kStrided || !w.is_cuda() || w.device().index() != x.device ||
         w.scalar_type() != (x.type == GEMM_F32_TYPE_F32 ? at::kFloat : at::kBFloat16) ||
         w.dim() != 1 || w.size(0) != x.cols || (x.cols > 1 && w.stride(0) != 1) ||
-        !(eps >= GEMM_F32_I8_LEAST_EPS))
+        !(given >= 1e-30) || !std::isfinite(eps))
         Py_RETURN_NONE;
     const bool residual = args[2] != Py_None;
     if (residual && (!any_matrix(args[2], &r) || r.type != x.type || r.rows != x.rows ||

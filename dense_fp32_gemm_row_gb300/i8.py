@@ -35,6 +35,7 @@ TYPE_BF16 = 1
 TYPE_I32 = 2
 I8_MAX_COLS = 131071
 I8_LEAST_EPS = 1e-30
+_EPS_TOO_LARGE = 2.0 ** 128 - 2.0 ** 103  # the least number that float32 rounds to an infinity
 ALGO_I8_PAIR = 6
 ALGO_I8_SINGLE = 7
 ALGO_I8_STREAM = 8
@@ -284,8 +285,8 @@ def i8_norm(x, weight, residual=None, eps=1e-6, out=None, total=None, stream=Non
     ldr = 0 if residual is None else _like(residual, rows, cols, x.dtype, device, "residual")
     if total is not None and residual is None:
         raise ValueError("total is x + residual: it needs residual")
-    if not I8_LEAST_EPS <= eps < float("inf"):
-        raise ValueError("eps must be finite and at least 1e-30")
+    if not I8_LEAST_EPS <= eps < _EPS_TOO_LARGE:
+        raise ValueError("eps must be at least 1e-30 and finite in float32")
     if stream is not None or _q8._away(device):
         return _q8._elsewhere(lambda: i8_norm(x, weight, residual, eps, out, total), device, stream,
                               (x, weight, residual, out, total))
