@@ -56,20 +56,33 @@ class I8Struct(ctypes.Structure):
 # ---- raw entry points: addresses and the stream are plain integers --------------------------
 
 
+def _wide(*values) -> bool:
+    """Whether one of them is not what the library's int of 32 bits would get."""
+    return any(not -2 ** 31 <= value < 2 ** 31 for value in values)
+
+
 def gemm_f32_i8_store(X, type, ldx, q, stream=0) -> int:
+    if _wide(type):
+        return _g.ERR_INVALID_VALUE
     return _g.load().gemm_f32_i8_store(X or None, type, ldx, q, stream or None)
 
 
 def gemm_f32_i8_norm(X, ldx, R, ldr, W, eps, type, S, lds, q, stream=0) -> int:
+    if _wide(type):
+        return _g.ERR_INVALID_VALUE
     return _g.load().gemm_f32_i8_norm(X or None, ldx, R or None, ldr, W or None, eps, type, S or None,
                                       lds, q, stream or None)
 
 
 def gemm_f32_i8_matmul(a, b, Y, type, ldy, algo=0, splits=0, stream=0) -> int:
+    if _wide(type, algo, splits):
+        return _g.ERR_INVALID_VALUE
     return _g.load().gemm_f32_i8_matmul(a, b, Y or None, type, ldy, algo, splits, stream or None)
 
 
 def gemm_f32_i8_gated(act, a, gate, up, H, type, ldh, algo=0, splits=0, stream=0) -> int:
+    if _wide(act, type, algo, splits):
+        return _g.ERR_INVALID_VALUE
     return _g.load().gemm_f32_i8_gated(act, a, gate, up, H or None, type, ldh, algo, splits,
                                        stream or None)
 

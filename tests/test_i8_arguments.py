@@ -35,3 +35,17 @@ def test_eps_with_and_without_the_module(module, monkeypatch):
     for eps in (1e-30, LARGEST, 2.0 ** 128 - 2.0 ** 103 - 2.0 ** 80, 1):
         q, _ = g.i8_norm(x, w, eps=eps)
         assert bool(torch.isfinite(q.scales).all())
+
+
+def test_raw_arguments_beyond_32_bits():
+    """Whose low 32 bits would be arguments as they should be: before any look at device or memory."""
+    q = g.I8Struct(0x7000_0000_0000, 0x7100_0000_0000, 48, 4, 40)
+    w = g.I8Struct(0x7200_0000_0000, 0x7300_0000_0000, 48, 7, 40)
+    y, wide = 0x7400_0000_0000, 2 ** 32
+    assert g.gemm_f32_i8_store(y, wide, 40, q) == g.ERR_INVALID_VALUE
+    assert g.gemm_f32_i8_norm(y, 40, 0, 0, y + 0x10000, 1e-6, wide + 1, 0, 0, q) == g.ERR_INVALID_VALUE
+    for type, algo, splits in ((wide, 0, 0), (0, wide, 0), (0, wide + 7, 0), (0, 7, wide + 2), (0, 7, -wide),
+                               (-wide, 0, 0)):
+        assert g.gemm_f32_i8_matmul(q, w, y, type, 7, algo, splits) == g.ERR_INVALID_VALUE
+        assert g.gemm_f32_i8_gated(0, q, w, w, y, type, 7, algo, splits) == g.ERR_INVALID_VALUE
+    assert g.gemm_f32_i8_gated(wide, q, w, w, y, 0, 7) == g.ERR_INVALID_VALUE
