@@ -168,6 +168,7 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
         if (c->rows != b->rows || c->cols != b->cols) return GEMM_F32_ERR_INVALID_VALUE;
     }
     const int T = a->rows, N = b->rows, K = a->cols;
+    if (algo == GEMM_F32_ALGO_I8_STREAM && T > kI8StreamTokens) return GEMM_F32_ERR_INVALID_VALUE;
     if (T == 0 || N == 0) return GEMM_F32_SUCCESS;
     // more tiles than an index holds (no memory does either), or rows whose
     // number plus a tile's it does not
@@ -188,7 +189,6 @@ int product(const gemm_f32_i8* a, const gemm_f32_i8* b, const gemm_f32_i8* c, in
     if (K == 0)
         return status(launch_zero_rows(Y, ldy * elem_of(type), T,
                                        static_cast<long long>(N) * elem_of(type), stream));
-    if (algo == GEMM_F32_ALGO_I8_STREAM && T > kI8StreamTokens) return GEMM_F32_ERR_INVALID_VALUE;
     I8Choice how = {};
     bool stream_form = algo == GEMM_F32_ALGO_I8_STREAM || (algo == GEMM_F32_ALGO_AUTO && T <= 8);
     if (!stream_form) {

@@ -49,3 +49,13 @@ def test_raw_arguments_beyond_32_bits():
         assert g.gemm_f32_i8_matmul(q, w, y, type, 7, algo, splits) == g.ERR_INVALID_VALUE
         assert g.gemm_f32_i8_gated(0, q, w, w, y, type, 7, algo, splits) == g.ERR_INVALID_VALUE
     assert g.gemm_f32_i8_gated(wide, q, w, w, y, 0, 7) == g.ERR_INVALID_VALUE
+
+
+def test_more_tokens_than_the_streaming_kernel_takes():
+    """Refused whatever else there is to do, and without a device."""
+    y = 0x7400_0000_0000
+    for K, N in ((40, 7), (0, 7), (40, 0)):
+        a = g.I8Struct(0x7000_0000_0000, 0x7100_0000_0000, 48, g.I8_STREAM_ROWS + 1, K)
+        b = g.I8Struct(0x7200_0000_0000, 0x7300_0000_0000, 48, N, K)
+        assert g.gemm_f32_i8_matmul(a, b, y, 0, 7, g.ALGO_I8_STREAM) == g.ERR_INVALID_VALUE
+        assert g.gemm_f32_i8_gated(0, a, b, b, y, 0, 7, g.ALGO_I8_STREAM) == g.ERR_INVALID_VALUE
