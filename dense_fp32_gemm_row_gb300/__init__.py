@@ -286,6 +286,7 @@ def matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None):
     for t in (A, B):
         if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError("A and B must be contiguous float32 CUDA tensors")
+        _q8._as_stored(t, "an operand")
     M, K = A.shape
     N = B.shape[1]
     for value in (M, N, K, int(splits)):
@@ -295,6 +296,7 @@ def matmul(A, B, out=None, algo=ALGO_AUTO, splits=0, stream=None):
         out = torch.empty((M, N), dtype=torch.float32, device=A.device)
     elif out.shape != (M, N) or out.dtype != torch.float32 or not out.is_contiguous():
         raise ValueError("out must be a contiguous float32 (M, N) tensor")
+    _q8._as_stored(out, "out")
     s = stream if stream is not None else torch.cuda.current_stream(A.device)
     with torch.cuda.device(A.device):
         st = gemm_f32_algo_splitk(A.data_ptr(), B.data_ptr(), out.data_ptr(), M, N, K, int(algo),

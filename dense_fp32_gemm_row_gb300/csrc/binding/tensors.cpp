@@ -83,6 +83,12 @@ void held_dealloc(PyObject* self) {
     Py_TYPE(self)->tp_free(self);
 }
 
+// A dense CUDA tensor whose memory holds its values as they are, not a view of
+// their negatives.
+bool plain(const at::Tensor& t) {
+    return t.layout() == at::kStrided && t.is_cuda() && !t.is_neg();
+}
+
 // Whether a tensor's last row of `width` bytes lies in its memory.
 bool covers(const at::Tensor& t, long long width) {
     const unsigned long long end = t.storage_offset() + (t.size(0) - 1) * t.stride(0) + width;
@@ -93,8 +99,7 @@ bool covers(const at::Tensor& t, long long width) {
 bool describe(const at::Tensor& c, const at::Tensor& s, long long cols, int format,
               gemm_f32_q8* q) {
     for (const at::Tensor* t : {&c, &s})
-        if (t->layout() != at::kStrided || !t->is_cuda() || t->scalar_type() != at::kByte ||
-            t->dim() != 2)
+        if (!plain(*t) || t->scalar_type() != at::kByte || t->dim() != 2)
             return false;
     const long long rows = c.size(0), blocks = (cols + 31) >> 5;
     if (rows < 2 || rows > INT_MAX || cols < 1 || cols > INT_MAX || s.size(0) != rows ||
@@ -238,7 +243,7 @@ struct Matrix {
 bool matrix(PyObject* o, Matrix* m) {
     if (!THPVariable_CheckExact(o)) return false;
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (t.layout() != at::kStrided || !t.is_cuda() || t.scalar_type() != at::kFloat || t.dim() != 2)
+    if (!plain(t) || t.scalar_type() != at::kFloat || t.dim() != 2)
         return false;
     m->rows = t.size(0);
     m->cols = t.size(1);
@@ -504,8 +509,8 @@ struct I8Operand {
     Ref codes, scales;
 };
 bool i8_describe(const at::Tensor& c, const at::Tensor& s, long long cols, I8Operand* m) {
-    if (c.layout() != at::kStrided || !c.is_cuda() || c.scalar_type() != at::kChar || c.dim() != 2 ||
-        s.layout() != at::kStrided || !s.is_cuda() || s.scalar_type() != at::kFloat || s.dim() != 1)
+    if (!plain(c) || c.scalar_type() != at::kChar || c.dim() != 2 || !plain(s) ||
+        s.scalar_type() != at::kFloat || s.dim() != 1)
         return false;
     const long long rows = c.size(0), width = c.size(1);
     if (rows < 1 || rows > INT_MAX || cols < 1 || cols > INT_MAX || width < cols ||
@@ -588,7 +593,7 @@ struct AnyMatrix {
 bool any_matrix(PyObject* o, AnyMatrix* m) {
     if (!THPVariable_CheckExact(o)) return false;
     const at::Tensor& t = THPVariable_Unpack(o);
-    if (t.layout() != at::kStrided || !t.is_cuda() || t.dim() != 2) return false;
+    if (!plain(t) || t.dim() != 2) return false;
     const at::ScalarType type = t.scalar_type();
     if (type != at::kFloat && type != at::kBFloat16) return false;
     m->type = type == at::kFloat ? GEMM_F32_TYPE_F32 : GEMM_F32_TYPE_BF16;
@@ -679,7 +684,7 @@ PyObject* i8_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const double given = PyFloat_AS_DOUBLE(args[3]);
     const float eps = static_cast<float>(given);
     const at::Tensor& w = THPVariable_Unpack(args[1]);
-    if (w.layout() != at::kStrided || !w.is_cuda() || w.device().index() != x.device ||
+    if (!plain(w) || w.device().index() != x.device ||
         w.scalar_type() != (x.type == GEMM_F32_TYPE_F32 ? at::kFloat : at::kBFloat16) ||
         w.dim() != 1 || w.size(0) != x.cols || (x.cols > 1 && w.stride(0) != 1) ||
         !(given >= 1e-30) || !std::isfinite(eps))

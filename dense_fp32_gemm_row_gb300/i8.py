@@ -121,6 +121,8 @@ def _layout(codes, scales, cols):
     if (codes.dtype is not _torch.int8 or scales.dtype is not _torch.float32 or codes.dim() != 2
             or scales.dim() != 1 or not codes.is_cuda):
         raise ValueError("codes must be a 2-D int8 and scales a 1-D float32 CUDA tensor")
+    _q8._as_stored(codes, "codes")
+    _q8._as_stored(scales, "scales")
     device = codes.get_device()
     if scales.get_device() != device:
         raise ValueError("codes and scales must be on one device")
@@ -294,6 +296,7 @@ def i8_norm(x, weight, residual=None, eps=1e-6, out=None, total=None, stream=Non
         raise ValueError(f"weight must be ({cols},) of x's type")
     if cols > 1 and weight.stride()[0] != 1:
         raise ValueError("weight must be contiguous")
+    _q8._as_stored(weight, "weight")
     _on(weight.get_device(), device)
     ldr = 0 if residual is None else _like(residual, rows, cols, x.dtype, device, "residual")
     if total is not None and residual is None:

@@ -61,6 +61,13 @@ def _int(value, what):
     return value
 
 
+def _as_stored(t, what):
+    """Refuses a view of memory that holds its values with the other sign (``z.conj().imag``)."""
+    negated = getattr(t, "is_neg", None)
+    if negated is not None and negated():
+        raise ValueError(f"{what} must not be a negated view (resolve_neg makes a copy)")
+
+
 class Q8Struct(ctypes.Structure):
     """``gemm_f32_q8`` of the C header."""
 
@@ -154,6 +161,8 @@ def _layout(codes, scales, cols):
     if (codes.dtype is not _torch.uint8 or scales.dtype is not _torch.uint8 or codes.dim() != 2
             or scales.dim() != 2 or not codes.is_cuda):
         raise ValueError("codes and scales must be 2-D uint8 CUDA tensors")
+    _as_stored(codes, "codes")
+    _as_stored(scales, "scales")
     if scales.get_device() != codes.get_device():
         raise ValueError("codes and scales must be on one device")
     (rows, width), (rows2, width2) = codes.shape, scales.shape
@@ -294,6 +303,7 @@ def _matrix(t, what):
 
 
 def _strides(t, what):
+    _as_stored(t, what)
     rows, cols = t.shape
     if rows > _INT_MAX or cols > _INT_MAX:
         raise ValueError(f"{what} must have fewer than 2^31 rows and columns, not {rows} x {cols}")
