@@ -37,8 +37,9 @@ __device__ __forceinline__ float i8_value(float sum, float token, float channel)
 }
 
 // act(z) with the quotient of silu to 2 ulp (act_value rounds it correctly): the
-// sums' own roundings are as large.  Where e^-z is beyond 2^126, z below -87.3,
-// the quotient is 0 instead of up to 1e-36.
+// sums' own roundings are as large, and act_value would make gated 8192 x 8192 x
+// 4096 736 us of 638, 1000 x 1023 x 1025 11.7 of 9.8.  Where e^-z is beyond 2^126, z
+// below -87.33, the quotient is 0 instead of up to 1.1e-36.
 template <int ACT>
 __device__ __forceinline__ float i8_act(float z) {
     return ACT == kActSilu ? __fdividef(z, 1.0f + expf(-z)) : act_value<kActGelu>(z);

@@ -554,7 +554,10 @@ int gemm_f32_i8_matmul(const gemm_f32_i8* a, const gemm_f32_i8* b, void* Y, int 
 /*
  * gemm_f32_i8_gated -- both projections of a gated block and their product,
  * H = act(a gate^T) * (a up^T), each as gemm_f32_i8_matmul gives it in fp32;
- * act as for gemm_f32_q8_gated, type F32 or BF16.
+ * type F32 or BF16.  act: the functions of gemm_f32_q8_gated, but with silu's
+ * quotient z / (1 + e^-z) to 2 ulp where that one's is rounded correctly; and
+ * where e^-z is beyond 2^126 (z below -87.33) silu is 0, not the up to 1.1e-36
+ * that it stands for.
  */
 int gemm_f32_i8_gated(int act, const gemm_f32_i8* a, const gemm_f32_i8* gate,
                       const gemm_f32_i8* up, void* H, int type, long long ldh, int algo,
