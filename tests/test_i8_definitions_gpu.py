@@ -5,8 +5,8 @@ import numpy as np
 import pytest
 
 import dense_fp32_gemm_row_gb300 as g
-from tests import _q8
-from tests.test_i8_gpu import down, quiet, t
+from tests import _i8, _q8
+from tests.test_i8_gpu import activations, down, dtype, quiet, t, up
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,41 @@ def test_gates_far_from_zero(T, act):
     assert np.all(np.abs(got - want) <= bound)
     gone = z <= (-111 if act == "silu" else -15)
     assert gone.any() and np.all(got[:, gone] == 0.0)
+
+
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 8), (9, 257), (1, 4096), (700, 130), (310, 1024), (40, 5001),
+                                       (4, 16384), (2, 20000)])
+def test_values_of_stored_rows(rows, cols, name):
+    """Within half a step: what code = z (127 / a) loses before it is rounded are two roundings, and
+    a / 127 one, each half an ulp of the value."""
+    rng = np.random.default_rng(rows + 13 * cols)
+    x = activations(rng, rows, cols, name)
+    q = g.i8_store(up(x, name))
+    quiet()
+    scale = down(q.scales).astype(np.float64)[:, None]
+    value = down(q.codes)[:, :cols] * scale
+    assert np.all(np.abs(value - x) <= 0.5 * scale + 3.01 * ULP / 2 * np.abs(x))
+
+
+@pytest.mark.parametrize("name", ["float32", "bfloat16"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 8), (9, 257), (1, 4096), (700, 130), (310, 1024), (40, 5001),
+                                       (4, 16384), (2, 20000)])
+def test_values_of_the_norm(rows, cols, residual, name):
+    """code * scale against s w / sqrt(mean s^2 + eps): half a step, the two roundings of z (127 / a),
+    and the scale's own error, which counts z's."""
+    torch = t()
+    rng = np.random.default_rng(rows + 17 * cols)
+    x = activations(rng, rows, cols, name)
+    r = activations(rng, rows, cols, name) if residual else None
+    w = down(torch.from_numpy(rng.standard_normal(cols).astype(np.float32)).to(dtype(name)))
+    w[cols // 2:cols // 2 + 1] = 0.0 if cols > 1 else 0.5
+    eps = float(np.float32(1e-3))
+    q, _ = g.i8_norm(up(x, name), up(w[None], name)[0], residual=up(r, name) if residual else None, eps=eps)
+    quiet()
+    s = x.astype(np.float64) + (r if residual else 0.0)
+    want = s * w / np.sqrt((s * s).mean(axis=1, keepdims=True) + eps)
+    scale = down(q.scales).astype(np.float64)[:, None]
+    value = down(q.codes)[:, :cols] * scale
+    assert np.all(np.abs(value - want) <= 0.5 * scale + (_i8.norm_bound(cols) + 4 * ULP / 2) * np.abs(want))
