@@ -65,7 +65,9 @@ constexpr I8Times kI8Narrow = {3.2f, 0.275f, 0.0002f, 0.27f, 0.0227f, 1.0f, 0.2f
 constexpr float kI8WeightsUsPerMb = 0.19f;
 // The same for the kernel for a few tokens: a launch, and a thousand codes of the
 // weights that the busiest SM reads, for 9 to 16, 24 and 32 tokens (24 x 8192 x 8192
-// 20.4 us, by single CTAs in two splits 16.8; 9 tokens 16.0 and 16.8).
+// 19.2 us, by single CTAs in two splits 16.7; 9 tokens 15.1 and 16.2).  Fitted when
+// copies of any size made each step longer: large layers now take up to a seventh less
+// than this says, small ones, which end far below the other form's, a third less.
 constexpr float kI8StreamLaunch = 3.3f;
 constexpr float kI8StreamUsPerK[kI8StreamTokens / 8 - 1] = {0.0245f, 0.0327f, 0.037f};
 constexpr int kI8MostSplits = 16;    // that the library chooses

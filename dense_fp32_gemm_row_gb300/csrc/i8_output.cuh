@@ -15,7 +15,9 @@ constexpr int kI8Bfloat16 = 1;
 constexpr int kI8Int32 = 2;
 constexpr int kI8NoAct = -1;  // not the gated product
 
-// Four codes as two words of two fp16 numbers.
+// Four codes as two words of two fp16 numbers: a code's bits, offset to be positive,
+// in the mantissa of 1024 are 1024 plus that number (for fp16 weights: Kim, Henry,
+// Fahim and Awadalla, "Who Says Elephants Can't Run", 2022).
 __device__ __forceinline__ void decode_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t u = w ^ 0x80808080u;
     const uint32_t bias = 0x64806480u;  // 1024 + 128, twice

@@ -8,8 +8,8 @@
 // is no pipeline to fill.  Up to eight tokens take the integer MMA, whose sums are
 // exact by themselves.  On this part it runs at half the rate of the fp16 one, to
 // which codes have first to be converted, but that leaves it fast enough there
-// (8192 x 8192: 8 tokens 14.1 us against 15.3 through fp16, but 16 21.4 against
-// 16.4, 24 30.6 against 20.4).  More tokens take the fp16 MMA as the kernel for
+// (8192 x 8192: 8 tokens 13.6 us against 13.9 through fp16, but 16 20.0 against
+// 15.3, 24 28.9 against 19.0).  More tokens take the fp16 MMA as the kernel for
 // many does (i8_tmem.cu): sums of up to 1024 products are exact in its fp32
 // accumulators, and are then added up in 32-bit integers.
 //
@@ -21,9 +21,9 @@
 // fragments makes no difference, as it is the same in both operands.  A copy
 // ends with K and leaves zeros behind it.
 //
-// Bounded by HBM and by a launch's 3 to 4 us: a token through 16384 x 16384 45.4
-// us, 5.9 TB/s, 8192 x 8192 13.3, 4096 x 4096 5.2.  From 17 tokens on by the MMAs:
-// 24 x 8192 x 8192 20 us, 3.6 for each group of eight.
+// Bounded by HBM and by a launch's 3 to 4 us: a token through 16384 x 16384 46
+// us, 5.8 TB/s, 8192 x 8192 13.1, 4096 x 4096 5.1.  From 17 tokens on by the MMAs:
+// 24 x 8192 x 8192 19.1 us, about 3 for each group of eight.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -183,8 +183,8 @@ i8_stream_kernel(I8StreamArgs p) {
     const int whole = p.K & ~15;
     const bool tail = whole < p.K && warp == (whole + 63) / 64 % warps;
     // While the kernel before ends, the first codes of each channel are sent for,
-    // to L2, which reads no value (a token, 4096 x 4096 5.4 to 5.2 us, 8192 x 8192
-    // 13.7 to 13.3; 2048 bytes instead of 512 made gated 8192 x 2048 9.5 of 8.0).
+    // to L2, which reads no value (a token, 4096 x 4096 5.3 to 5.1 us, 8192 x 8192
+    // 13.6 to 13.2; 2048 bytes instead of 512 make gated 8192 x 2048 9.2 of 8.3).
     if (threadIdx.x < 16 * SETS) {
         const int s = threadIdx.x / 16;
         const I8In& m = S::GATED && s >= CG ? p.c : p.b;
@@ -322,11 +322,11 @@ cudaError_t configure(int dev, int* regs) {
 
 // Warps a block: four, or as many more as make 24 an SM, if the blocks that an SM
 // gets of them find room in it side by side.  (Of a token through 8192 x 8192
-// four, 13.4 us, eight 14.0; 4096 x 4096 eight 5.4, sixteen 5.9, four 6.5; 16384 x
-// 16384 four 45.7, two 49.0.)  Each block then asks for its whole share of the
+// four, 13.1 us, eight 14.1; 4096 x 4096 eight 5.1, sixteen 5.7, four 6.0; 16384 x
+// 16384 four 46.6, two 49.8.)  Each block then asks for its whole share of the
 // SM's shared memory: a block more, on an SM that was done sooner with the kernel
-// before, would take it longer than the others (gated 8192 x 2048 8.4 us against
-// 9.8, 14336 x 4096 12.0 against 14.5).
+// before, would take it longer than the others (gated 8192 x 2048 8.3 us against
+// 9.3, 14336 x 4096 11.4 against 14.3).
 template <int NT, int CG, int ACT>
 cudaError_t launch(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_count) {
     using S = Stream<NT, CG, ACT>;
@@ -357,8 +357,8 @@ cudaError_t launch(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_c
 }
 
 // 32 channels a block convert the tokens' codes half as often as 16, but are
-// half as many blocks: from about half a block an SM on (24 x 4096 x 4096 8.0 us
-// against 9.1, 24 x 1024 x 8192 10.7 against 7.4).
+// half as many blocks: from about half a block an SM on (24 x 4096 x 4096 7.4 us
+// against 8.5, 24 x 1024 x 8192 9.6 against 7.0).
 bool two_groups(int N, int sm_count) { return (N - 1) / 32 + 1 > sm_count / 2; }
 template <int NT, int ACT>
 cudaError_t by_channels(const I8StreamArgs& p, cudaStream_t stream, int dev, int sm_count) {

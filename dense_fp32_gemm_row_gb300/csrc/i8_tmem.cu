@@ -61,7 +61,7 @@
 // and the peer's relay 23.  One token to a few hundred are bound by the start
 // (3.2 us to the first MMA's end and the store of the last tile), then by 0.28 us
 // a stage or the weights' way from HBM: 1000 x 1023 x 1025 7.1 us, 64 x 8192 x 8192
-// 17.9 (with splits that meet in the workspace 19.0).
+// 17.8 (with splits that meet in the workspace 19.1).
 #include <cstdint>
 
 #include "device_sync.cuh"
@@ -419,9 +419,8 @@ i8_tmem_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     // While the kernel before ends, the weights' way to L2 is begun, which reads
-    // no value: 24 x 8192 x 8192 18.9 to 18.2 us, 64 x 4096 x 4096 12.4 to 11.6.
-    // (One stage 18.5, six 18.5; by all tiles of tokens 1000 x 1023 x 1025 7.5
-    // against 6.9.)
+    // no value: 24 x 8192 x 8192 17.5 to 16.7 us, 64 x 4096 x 4096 11.2 to 10.6.
+    // (One stage 17.1, six 17.0; by all tiles of tokens nothing more.)
     if (!PAIR && warp == 3 && elect_lane()) {
         Work w;
         if (work_at<PAIR, GATED>(share, first, w) && w.t0 == 0)
